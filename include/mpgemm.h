@@ -263,6 +263,111 @@ mpgemm_status_t mpgemm_quantize_w4(mpgemm_handle_t h, int64_t N, int64_t K,
                                    uint8_t *Wq, int64_t ldwq, uint16_t *S, int64_t lds,
                                    void *stream);
 
+/* ------------------------------------------------------------------ MXFP4
+ *
+ * Microscaled 4-bit floating point (OCP Microscaling Formats, MXFP4): blocks
+ * of 32 elements along the contracted axis share one power-of-two scale.
+ * A matrix of R rows and K columns is held as
+ *   codes   R rows of nb = ceil(K / 32) blocks of 16 bytes (row stride ldq
+ *           BYTES >= 16 nb): byte j of a block holds element 2j in its low
+ *           nibble and 2j + 1 in its high nibble, as e2m1 (sign, two exponent
+ *           bits, one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6). Elements past
+ *           K are zero (the quantiser writes them; a product relies on it).
+ *   scales  R rows of nb bytes (row stride lds BYTES >= nb), e8m0: the value
+ *           of an element is e2m1(code) * 2^(scale - 127); 255 makes the whole
+ *           block NaN.
+ * Codes and scales must be 16-byte aligned with row strides that are multiples
+ * of 16 bytes below 2^23 (else MPGEMM_ERR_UNSUPPORTED); a call may read (and
+ * discard) the scale bytes of a row up to the next multiple of 16, and writes
+ * none past nb. No size may exceed MPGEMM_MAX_K_MXFP4 (else
+ * MPGEMM_ERR_UNSUPPORTED).
+ *
+ * Quantisation of a block with largest magnitude amax (in the input's type,
+ * subnormals included): scale = max(floor(log2 amax) - 2, -127) + 127 (0 for a
+ * block of zeros), code = the nearest e2m1 of x / 2^(scale - 127), ties to
+ * even, magnitudes over 6 to 6. A block that holds NaN or an infinity gets
+ * scale 255. The sign of zero is kept.
+ *
+ * The calls below take scratch memory from the caller (16-byte aligned, at
+ * least the bytes that the matching _workspace call returns, which is -1 for
+ * sizes that the call refuses; NULL when that is 0) instead of the handle's
+ * workspace, so calls that share a handle may run on several streams at once.
+ * Everything else is the common contract above. */
+#define MPGEMM_MAX_K_MXFP4 ((1 << 24) - 32)
+
+/* Types of the activations, gradients and results. */
+enum {
+    MPGEMM_TYPE_F16 = 0,
+    MPGEMM_TYPE_BF16 = 1,
+    MPGEMM_TYPE_F32 = 2
+};
+
+/* X (M x K, `type`, row stride ldx elements, element-aligned) into MXFP4:
+ * along rows (Q, S: M rows of ceil(K / 32) blocks), along columns (QT, ST: the
+ * MXFP4 form of X^T, K rows of ceil(M / 32) blocks), or both in one pass over
+ * X. Either pair may be NULL; not both. */
+mpgemm_status_t mpgemm_quantize_mxfp4(mpgemm_handle_t h, int64_t M, int64_t K, int type, const void *X,
+                                      int64_t ldx, uint8_t *Q, int64_t ldq, uint8_t *S, int64_t lds,
+                                      uint8_t *QT, int64_t ldqt, uint8_t *ST, int64_t ldst, void *stream);
+
+/* Y (M x K, `type`, row stride ldy) = the values that Q, S stand for, rounded
+ * once to the type (exact in fp32; to bf16 unless they overflow nothing is
+ * rounded either). */
+mpgemm_status_t mpgemm_dequantize_mxfp4(mpgemm_handle_t h, int64_t M, int64_t K, const uint8_t *Q,
+                                        int64_t ldq, const uint8_t *S, int64_t lds, int type, void *Y,
+                                        int64_t ldy, void *stream);
+
+/* C = A B^T + bias for A (M x K) and B (N x K) held in MXFP4: fp32 sums, the
+ * bias (N values of `type`, or NULL) added in fp32, one rounding to `type`.
+ * C: M x N, row stride ldc elements. */
+mpgemm_status_t mpgemm_run_mxfp4(mpgemm_handle_t h, int64_t M, int64_t N, int64_t K, const uint8_t *A,
+                                 int64_t lda, const uint8_t *SA, int64_t ldsa, const uint8_t *B,
+                                 int64_t ldb, const uint8_t *SB, int64_t ldsb, const void *bias, int type,
+                                 void *C, int64_t ldc, void *workspace, int64_t workspace_bytes,
+                                 void *stream);
+int64_t mpgemm_run_mxfp4_workspace(int64_t M, int64_t N, int64_t K, int cu_count);
+
+/* Y = MX(X) W^T + bias: mpgemm_run_mxfp4 with the activations X (M x K,
+ * `type`, row stride ldx elements, element-aligned) quantised along rows in
+ * the call. Bit-identical to quantising X first. */
+mpgemm_status_t mpgemm_run_mxfp4_dyn(mpgemm_handle_t h, int64_t M, int64_t N, int64_t K, int type,
+                                     const void *X, int64_t ldx, const uint8_t *W, int64_t ldw,
+                                     const uint8_t *SW, int64_t ldsw, const void *bias, void *Y,
+                                     int64_t ldy, void *workspace, int64_t workspace_bytes, void *stream);
+int64_t mpgemm_run_mxfp4_dyn_workspace(int64_t M, int64_t N, int64_t K, int cu_count);
+
+/* Gradients of Y = X W^T (X: M x K, W: N x K) from dY (M x N, `type`, row
+ * stride lddy elements), quantised in the call along both axes:
+ *   dX = MX(dY) W      M x K, `type`, one rounding (WT: W^T in MXFP4, K rows
+ *                      of ceil(N / 32) blocks)
+ *   dW = MX(dY^T) X    N x K, fp32 (XT: X^T in MXFP4, K rows of ceil(M / 32)
+ *                      blocks)
+ * dX or dW may be NULL (with its operand): that gradient is not computed. */
+mpgemm_status_t mpgemm_run_mxfp4_backward(mpgemm_handle_t h, int64_t M, int64_t N, int64_t K, int type,
+                                          const void *dY, int64_t lddy, const uint8_t *WT, int64_t ldwt,
+                                          const uint8_t *SWT, int64_t ldswt, const uint8_t *XT,
+                                          int64_t ldxt, const uint8_t *SXT, int64_t ldsxt, void *dX,
+                                          int64_t lddx, float *dW, int64_t lddw, void *workspace,
+                                          int64_t workspace_bytes, void *stream);
+int64_t mpgemm_run_mxfp4_backward_workspace(int64_t M, int64_t N, int64_t K, int cu_count);
+
+/* ------------------------------------------------------- Newton-Schulz
+ *
+ * Orthogonalises `batch` matrices G (M x N, `type` MPGEMM_TYPE_F16 or _BF16,
+ * row stride ldg, matrix stride strideg, in elements): X = G / (|G|_F + eps),
+ * then `steps` times X <- a X + (b A + c A A) X with A = X X^T (X^T in the
+ * place of X where M > N), written to Y (`type`, ldy, stridey; Y may be G
+ * itself). coeffs: host pointer to a, b, c. Every factor of a product is held
+ * as a sum of two bf16 values (16 significant bits) and products are summed in
+ * fp32; the result is rounded once to `type`. A G of zeros gives zeros
+ * (eps > 0). 0 <= steps <= 100; M, N <= 65536; batch <= 65535. */
+mpgemm_status_t mpgemm_run_newton_schulz(mpgemm_handle_t h, int64_t batch, int64_t M, int64_t N, int type,
+                                         const void *G, int64_t ldg, int64_t strideg, int steps,
+                                         const float *coeffs, float eps, void *Y, int64_t ldy,
+                                         int64_t stridey, void *workspace, int64_t workspace_bytes,
+                                         void *stream);
+int64_t mpgemm_run_newton_schulz_workspace(int64_t batch, int64_t M, int64_t N);
+
 /* Measurement aid: a plain streaming read of `bytes` bytes at `src` (device
  * memory, 16-byte aligned, bytes a multiple of 16) with 16-byte loads,
  * loads_per_lane (1, 2, 4 or 8) per lane, all issued before any is combined.

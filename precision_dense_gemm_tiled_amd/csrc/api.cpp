@@ -10,20 +10,10 @@
 #include <cstring>
 #include <new>
 
+#include "handle.h"
 #include "mpgemm_internal.h"
 
-struct mpgemm_ctx {
-    int device;
-    int cu_count;
-    int forced_tile_cfg;   // -1: heuristic; else a TileCfg index (MPGEMM_TILE_CFG)
-    int forced_w4a16_cfg;  // -1: heuristic; else a W4A16Cfg index (MPGEMM_W4A16_CFG)
-    int streamk_mode;      // mpg::StreamKMode (MPGEMM_STREAMK=0/1 forces it off/on)
-    // One device buffer of partial sums, used by the weight-only path's K
-    // split and by stream-K tile GEMMs (calls sharing a handle are serialized
-    // by the caller), and the stream-K arrival counters (zero between calls).
-    mpg::W4A16Workspace ws;
-    mpg::TileWorkspace tile_ws;
-};
+using mpg::DeviceGuard;
 
 namespace {
 
@@ -79,25 +69,6 @@ constexpr int64_t kWorkspaceBytes = int64_t(128) << 20;
 constexpr int64_t kSplitPartialFloats = int64_t(8) << 20;
 // Stream-K arrival counters: one per split tile (at most two waves of tiles).
 constexpr int kStreamKFlags = 16384;
-
-// Makes the handle's device current for the duration of a call and restores
-// the caller's current device afterwards.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = false;
-    explicit DeviceGuard(int device) {
-        if (hipGetDevice(&prev) != hipSuccess) {
-            prev = -1;
-            return;
-        }
-        ok = prev == device || hipSetDevice(device) == hipSuccess;
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev)
-            (void)hipSetDevice(prev);
-    }
-};
 
 // The low-rank branch of a W4A4 call: U (fp32, M x rank) and the up-projection.
 struct LowRankArgs {

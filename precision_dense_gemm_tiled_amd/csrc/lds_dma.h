@@ -53,4 +53,11 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// Between a wavefront's LDS writes and its own lanes' reads of what other lanes
+// wrote (or back): the wavefront's LDS operations are done, and the compiler
+// keeps memory operations on their side.
+__device__ __forceinline__ void wave_lds_fence() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
 }  // namespace mpg

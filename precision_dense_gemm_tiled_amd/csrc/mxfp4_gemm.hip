@@ -1,0 +1,603 @@
+// MXFP4 product C = A B^T + bias on gfx950's scaled matrix instructions.
+//
+// C[m][n] = sum over blocks of 2^(sa - 127 + sb - 127) * (sum of 32 products
+// of e2m1 values). v_mfma_scale_f32_32x32x64_f8f6f4 (and 16x16x128) take one
+// block of 32 codes (16 bytes) and its scale byte per lane for each operand,
+// so the 16-byte chunks of the stored rows are the fragments and the stored
+// e8m0 bytes the scales: nothing is unpacked. Lane l supplies row l % 32 (16)
+// and block l / 32 (16) of a step; which blocks of K make up a step is free,
+// as long as both operands agree. A lane therefore takes four consecutive
+// blocks over four steps, whose scale bytes are one word, the step selecting
+// the byte.
+//
+// Two kernels:
+//   tile    operands through LDS (compute and L2 bandwidth bound)
+//   skinny  M <= 64: operands straight from memory into the matrix unit's
+//           registers, K over the wavefronts of a workgroup (bound by reading
+//           B once); with M <= 16 the activations may be quantised in it
+#include "mxfp4.h"
+#include "mxfp4_device.h"
+#include "lds_dma.h"
+
+namespace mpg {
+
+typedef int mx_i32x4 __attribute__((ext_vector_type(4)));
+typedef int mx_i32x8 __attribute__((ext_vector_type(8)));
+typedef float mx_f32x4 __attribute__((ext_vector_type(4)));
+typedef float mx_f32x16 __attribute__((ext_vector_type(16)));
+
+// 16 bytes of zeros: the source of blocks past a row's end.
+__device__ const u32x4 kMxZeros = {0, 0, 0, 0};
+
+__device__ __forceinline__ mx_i32x8 mx_widen(mx_i32x4 v) { return mx_i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+// One step with byte S of the scale words. The operand format 4 is e2m1.
+template <int S>
+__device__ __forceinline__ mx_f32x16 mx_mfma32(mx_i32x4 x, mx_i32x4 y, mx_f32x16 c, int sx, int sy) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_widen(x), mx_widen(y), c, 4, 4, S, sx, S, sy);
+}
+template <int S>
+__device__ __forceinline__ mx_f32x4 mx_mfma16(mx_i32x4 x, mx_i32x4 y, mx_f32x4 c, int sx, int sy) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_widen(x), mx_widen(y), c, 4, 4, S, sx, S, sy);
+}
+
+// Consecutive workgroups go to the 8 XCDs in turn, each with its own L2: give
+// every XCD a contiguous range of tiles, walked in groups of 8 tile rows.
+__device__ __forceinline__ void mx_tile_of(int bid, int nblk, int tiles_m, int tiles_n, int &tm, int &tn) {
+    int logical = bid;
+    if (nblk >= 8) {
+        const int xcd = bid % 8, base = nblk / 8, rem = nblk % 8;
+        logical = xcd * base + (xcd < rem ? xcd : rem) + bid / 8;
+    }
+    constexpr int GROUP = 8;
+    const int group = logical / (GROUP * tiles_n);
+    const int first = group * GROUP;
+    const int rows = tiles_m - first < GROUP ? tiles_m - first : GROUP;
+    const int in = logical - group * GROUP * tiles_n;
+    tm = first + in % rows;
+    tn = in / rows;
+}
+
+// Scale word of blocks blk .. blk + 3 with the bytes of blocks >= nb cleared
+// (their codes are read as zeros, and a stray 255 would make them NaN).
+__device__ __forceinline__ int mx_mask_scales(int w, int blk, int nb) {
+    const int left = nb - blk;
+    return left >= 4 ? w : (left <= 0 ? 0 : (int)((uint32_t)w & ((1u << (8 * left)) - 1u)));
+}
+
+template <typename T>
+__device__ __forceinline__ float mx_bias(const void *bias, int n) {
+    return bias ? (float)((const T *)bias)[n] : 0.f;
+}
+
+// ------------------------------------------------------------------ tile
+
+// BM x BN output tile, WGM x WGN wavefronts, stages of 8 blocks of K (128
+// bytes per row) in an NS-deep LDS ring filled with direct-to-LDS loads.
+// 16-byte chunk c of LDS row r sits at c ^ swz(r), which keeps the fragment
+// reads (one chunk column over 32 rows) free of bank conflicts. At step s of a
+// stage, lane half h reads chunk 4 h + s.
+//
+// Scales: 16 bytes per row, two stages' worth, in a two-slot ring of their
+// own; each lane reads the word of its row, stage and half once per stage.
+template <int BM, int BN, int WGM, int WGN, int NS>
+struct MxTile {
+    static constexpr int NW = WGM * WGN, NT = 64 * NW;
+    static constexpr int WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32;
+    static constexpr int BKB = 128, CPR = 8, RS = NT / CPR;
+    static constexpr int A_PER_T = BM / RS, B_PER_T = BN / RS, NL = A_PER_T + B_PER_T;
+    static constexpr int STAGE = (BM + BN) * BKB, SCALES = (BM + BN) * 16;
+    static constexpr int LDS_BYTES = NS * STAGE + 2 * SCALES;
+    static constexpr int SROUNDS = (BM + BN + NT - 1) / NT;
+    static_assert(RS % 16 == 0 && BM % RS == 0 && BN % RS == 0 && (BM + BN) % 64 == 0 && BM % 64 == 0, "staging");
+    static_assert(NS >= 2 && LDS_BYTES <= 160 * 1024 && (NS - 2) * NL < 64, "ring");
+
+    static __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+
+    template <int S>
+    static __device__ __forceinline__ void read_frags(const uint8_t *As, int wm0, int wn0, int lane,
+                                                      mx_i32x4 (&a)[TM], mx_i32x4 (&b)[TN]) {
+        const uint8_t *Bs = As + BM * BKB;
+        const int c = 4 * (lane >> 5) + S;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int r = wm0 + i * 32 + (lane & 31);
+            a[i] = *reinterpret_cast<const mx_i32x4 *>(As + r * BKB + ((c ^ swz(r)) * 16));
+        }
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int r = wn0 + j * 32 + (lane & 31);
+            b[j] = *reinterpret_cast<const mx_i32x4 *>(Bs + r * BKB + ((c ^ swz(r)) * 16));
+        }
+    }
+
+    // Operands swapped, so each accumulator block is the transpose of its C
+    // block: register r of lane l holds row l % 32, column
+    // 8 (r / 4) + 4 (l / 32) + r % 4.
+    template <int S, int LO = 0, int HI = TM * TN>
+    static __device__ __forceinline__ void mfmas(const mx_i32x4 (&a)[TM], const mx_i32x4 (&b)[TN],
+                                                 const int (&sa)[TM], const int (&sb)[TN],
+                                                 mx_f32x16 (&acc)[TM][TN]) {
+#pragma unroll
+        for (int f = LO; f < HI; ++f)
+            acc[f / TN][f % TN] = mx_mfma32<S>(b[f % TN], a[f / TN], acc[f / TN][f % TN], sb[f % TN], sa[f / TN]);
+    }
+
+    // Stages [e0, e1) of 8 blocks; only the last stage of a row may be partial.
+    static __device__ __forceinline__ void mainloop(const MxGemm &p, uint8_t *smem, int row0, int col0, int e0,
+                                                    int e1, int tid, int lane, int wave,
+                                                    mx_f32x16 (&acc)[TM][TN]) {
+        const int wm0 = (wave / WGN) * WTM, wn0 = (wave % WGN) * WTN;
+        const int nb = p.nb, last = (nb + 7) / 8 - 1;
+        const int r0 = tid / CPR, cg = (tid % CPR) ^ swz(r0);
+        const uint8_t *Ab = p.a + (int64_t)row0 * p.lda, *Bb = p.b + (int64_t)col0 * p.ldb;
+        const uint8_t *SAb = p.sa + (int64_t)row0 * p.ldsa, *SBb = p.sb + (int64_t)col0 * p.ldsb;
+        const int a_rows = p.M - row0, b_rows = p.N - col0;
+        // (rows past the matrix repeat its last row: their outputs are not stored)
+        uint32_t off[NL], soff[SROUNDS];
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const bool isa = i < A_PER_T;
+            const int rows = isa ? a_rows : b_rows;
+            int r = r0 + (isa ? i : i - A_PER_T) * RS;
+            r = r < rows ? r : rows - 1;
+            off[i] = (uint32_t)r * (uint32_t)(isa ? p.lda : p.ldb) + cg * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < SROUNDS; ++i) {
+            const int t = i * NT + tid;
+            const bool isa = t < BM;
+            const int rows = isa ? a_rows : b_rows;
+            int r = isa ? t : t - BM;
+            r = r < rows ? r : rows - 1;
+            soff[i] = (uint32_t)r * (uint32_t)(isa ? p.ldsa : p.ldsb);
+        }
+        const int wrow = wave * (64 / CPR);
+        uint8_t *sc = smem + NS * STAGE;
+
+        // every call issues NL loads: stages past the last re-read it
+        auto dma_stage = [&](int e) {
+            const int kt = e < last ? e : last;
+            const bool in = kt * 8 + cg < nb;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const bool isa = i < A_PER_T;
+                const uint8_t *src = (isa ? Ab : Bb) + (int64_t)kt * BKB + off[i];
+                if (kt == last)
+                    src = in ? src : reinterpret_cast<const uint8_t *>(&kMxZeros);
+                dma16(src, smem + (e % NS) * STAGE + (isa ? 0 : BM * BKB) +
+                               (wrow + (isa ? i : i - A_PER_T) * RS) * BKB);
+            }
+        };
+        // scale bytes of stages 2 q and 2 q + 1 (a chunk that starts inside the row)
+        auto dma_scales = [&](int q) {
+            const int qc = 2 * q <= last ? q : last / 2;
+#pragma unroll
+            for (int i = 0; i < SROUNDS; ++i)
+                if ((i + 1) * NT <= BM + BN || i * NT + wave * 64 < BM + BN)
+                    dma16((i * NT + wave * 64 < BM ? SAb : SBb) + soff[i] + 16 * qc,
+                          sc + (q & 1) * SCALES + (i * NT + wave * 64) * 16);
+        };
+        auto read_scales = [&](int e, int (&sa)[TM], int (&sb)[TN]) {
+            const uint8_t *s = sc + ((e >> 1) & 1) * SCALES + 8 * (e & 1) + 4 * (lane >> 5);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                sa[i] = *reinterpret_cast<const int *>(s + (wm0 + i * 32 + (lane & 31)) * 16);
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                sb[j] = *reinterpret_cast<const int *>(s + (BM + wn0 + j * 32 + (lane & 31)) * 16);
+            if (e >= last) {
+                const int blk = 8 * last + 4 * (lane >> 5);
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    sa[i] = mx_mask_scales(sa[i], blk, nb);
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    sb[j] = mx_mask_scales(sb[j], blk, nb);
+            }
+        };
+
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = mx_f32x16{};
+
+        mx_i32x4 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
+        int sa[TM], sb[TN], na[TM], nbs[TN];
+        // Loads retire in order and the scales of a pair are issued ahead of
+        // its stages, so the wait that proves a stage has landed proves its
+        // scales too. (A slice may start at an odd stage: both pairs then.)
+        dma_scales(e0 >> 1);
+        if (e0 & 1)
+            dma_scales((e0 >> 1) + 1);
+#pragma unroll
+        for (int e = 0; e < NS - 1; ++e)
+            dma_stage(e0 + e);
+        wait_vm_lds<(NS - 2) * NL>();
+        lds_barrier();
+        read_frags<0>(smem + (e0 % NS) * STAGE, wm0, wn0, lane, fa0, fb0);
+        read_scales(e0, sa, sb);
+
+        // Stage e: the loads of stage e + NS - 1 go into the slot that stage
+        // e - 1 has left; each step's fragments are read during the step
+        // before; after the first quarter of the last step's products the
+        // barrier publishes stage e + 1, whose first fragments and scales are
+        // read under the rest.
+        constexpr int NMF = TM * TN, KA = NMF >= 4 ? NMF / 4 : 1;
+        for (int e = e0; e < e1; ++e) {
+            const uint8_t *S = smem + (e % NS) * STAGE;
+            __builtin_amdgcn_sched_barrier(0);
+            // the next pair's scales, into the slot of the pair before this one
+            if ((e & 1) == 0)
+                dma_scales((e >> 1) + 1);
+            dma_stage(e + NS - 1);
+            read_frags<1>(S, wm0, wn0, lane, fa1, fb1);
+            mfmas<0>(fa0, fb0, sa, sb, acc);
+            __builtin_amdgcn_sched_barrier(0);
+            read_frags<2>(S, wm0, wn0, lane, fa0, fb0);
+            mfmas<1>(fa1, fb1, sa, sb, acc);
+            __builtin_amdgcn_sched_barrier(0);
+            read_frags<3>(S, wm0, wn0, lane, fa1, fb1);
+            mfmas<2>(fa0, fb0, sa, sb, acc);
+            __builtin_amdgcn_sched_barrier(0);
+            mfmas<3, 0, KA>(fa1, fb1, sa, sb, acc);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vm_lds<(NS - 2) * NL>();
+            lds_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            read_frags<0>(smem + ((e + 1) % NS) * STAGE, wm0, wn0, lane, fa0, fb0);
+            read_scales(e + 1, na, nbs);
+            mfmas<3, KA, NMF>(fa1, fb1, sa, sb, acc);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                sa[i] = na[i];
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                sb[j] = nbs[j];
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        wait_vm_lds<0>();
+    }
+
+    // C through LDS: each wavefront writes 32 rows of its outputs (four
+    // consecutive columns per lane) into its own region and reads whole row
+    // segments back for 16-byte stores. Chunk c of row r sits at
+    // c ^ (r % chunks per row).
+    template <typename OUT>
+    static __device__ __forceinline__ void epilogue(const MxGemm &p, uint8_t *smem, int row0, int col0, int lane,
+                                                    int wave, const mx_f32x16 (&acc)[TM][TN]) {
+        constexpr int RB = WTN * (int)sizeof(OUT), CPW = RB / 16;
+        constexpr int EPC = 16 / (int)sizeof(OUT);   // outputs per chunk
+        static_assert(NW * 32 * RB <= LDS_BYTES && (CPW & (CPW - 1)) == 0 && CPW >= 4, "epilogue staging");
+        const int wm0 = (wave / WGN) * WTM, wn0 = (wave % WGN) * WTN;
+        uint8_t *region = smem + wave * 32 * RB;
+        OUT *C = reinterpret_cast<OUT *>(p.c);
+        const bool vec = (reinterpret_cast<uintptr_t>(C) & 15) == 0 && (p.ldc * sizeof(OUT)) % 16 == 0;
+        __syncthreads();   // every wavefront is past its last fragment read
+        typedef OUT out4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int rl = lane & 31;
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int cl = 32 * j + 8 * g + 4 * (lane >> 5);
+                    out4 v;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const int n = col0 + wn0 + cl + d;
+                        v[d] = (OUT)(acc[i][j][4 * g + d] + mx_bias<OUT>(p.bias, n < p.N ? n : p.N - 1));
+                    }
+                    const int c = cl / EPC;
+                    *reinterpret_cast<out4 *>(region + rl * RB + ((c ^ (rl & (CPW - 1))) * 16) +
+                                              (cl % EPC) * (int)sizeof(OUT)) = v;
+                }
+            wave_lds_fence();
+#pragma unroll
+            for (int q = 0; q < 32 * CPW / 64; ++q) {
+                const int f = q * 64 + lane;
+                const int r = f / CPW, c = f % CPW;
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(region + r * RB + ((c ^ (r & (CPW - 1))) * 16));
+                const int row = row0 + wm0 + i * 32 + r, col = col0 + wn0 + c * EPC;
+                if (row < p.M) {
+                    OUT *dst = C + (int64_t)row * p.ldc + col;
+                    if (vec && col + EPC <= p.N) {
+                        // non-temporal: C is not read back here
+                        __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(dst));
+                    } else {
+#pragma unroll
+                        for (int d = 0; d < EPC; ++d)
+                            if (col + d < p.N) {
+                                if constexpr (sizeof(OUT) == 4)
+                                    reinterpret_cast<uint32_t *>(dst)[d] = v[d];
+                                else
+                                    reinterpret_cast<uint16_t *>(dst)[d] = (uint16_t)(v[d / 2] >> (16 * (d % 2)));
+                            }
+                    }
+                }
+            }
+            wave_lds_fence();
+        }
+    }
+};
+
+// OUT: the result's type; with K split over gridDim.y, slice y writes its fp32
+// sums to rows y M ... of p.c (no bias) and mx_join_kernel adds them.
+template <typename OUT, int BM, int BN, int WGM, int WGN, int NS>
+__global__ __launch_bounds__(64 * WGM * WGN) void mx_tile_kernel(MxGemm p, int tiles_m, int tiles_n, int slice) {
+    typedef MxTile<BM, BN, WGM, WGN, NS> MT;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[MT::LDS_BYTES];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    mx_tile_of(blockIdx.x, gridDim.x, tiles_m, tiles_n, tm, tn);
+    const int stages = (p.nb + 7) / 8;
+    const int e0 = blockIdx.y * slice, e1 = min(e0 + slice, stages);
+    mx_f32x16 acc[MT::TM][MT::TN];
+    MT::mainloop(p, smem, tm * BM, tn * BN, e0, e1, tid, lane, wave, acc);
+    if (gridDim.y > 1)
+        p.c = (float *)p.c + (int64_t)blockIdx.y * p.M * p.ldc;
+    MT::template epilogue<OUT>(p, smem, tm * BM, tn * BN, lane, wave, acc);
+}
+
+// C = sum of ks slices of M x N fp32 partial results (row stride ldp) + bias,
+// in the order of the slices. ks = 0: the bias alone (K = 0).
+template <typename OUT>
+__global__ __launch_bounds__(256) void mx_join_kernel(const float *part, int64_t ldp, int ks, MxGemm p) {
+    const int64_t total = (int64_t)p.M * p.N;
+    for (int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x; f < total; f += (int64_t)gridDim.x * 256) {
+        const int m = (int)(f / p.N), n = (int)(f - (int64_t)m * p.N);
+        float s = 0.f;
+        for (int k = 0; k < ks; ++k)
+            s += part[((int64_t)k * p.M + m) * ldp + n];
+        ((OUT *)p.c)[(int64_t)m * p.ldc + n] = (OUT)(s + mx_bias<OUT>(p.bias, n));
+    }
+}
+
+// ------------------------------------------------------------------ skinny
+
+// 16 MF rows x 16 NF columns per workgroup, K in groups of 16 blocks dealt out
+// to the 8 wavefronts in turn. In a group, lane quarter q takes blocks
+// 4 q ... 4 q + 3 (64 contiguous bytes of its row, and one word of scales), one
+// per step. The wavefronts' sums are joined in LDS in the order of the
+// wavefronts. FUSED (MF = 1): a lane quantises the 32 activations of its block
+// in registers; rows past M are zero.
+template <typename T, int MF, int NF, bool FUSED, bool VEC>
+__global__ __launch_bounds__(512) void mx_skinny_kernel(MxGemm p, MxSkinnyX px) {
+    constexpr int NW = 8;
+    __shared__ float red[NW][MF * NF][4][64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int q = lane >> 4, r = lane & 15;
+    const int n0 = blockIdx.x * 16 * NF;
+    const int nb = p.nb, groups = (nb + 15) / 16;
+
+    const uint8_t *bq[NF], *bs[NF];
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+        const int n = min(n0 + 16 * j + r, p.N - 1);
+        bq[j] = p.b + (int64_t)n * p.ldb + 64 * q;
+        bs[j] = p.sb + (int64_t)n * p.ldsb + 4 * q;
+    }
+    const uint8_t *aq[MF], *as[MF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+        const int m = min(16 * i + r, p.M - 1);
+        aq[i] = FUSED ? nullptr : p.a + (int64_t)m * p.lda + 64 * q;
+        as[i] = FUSED ? nullptr : p.sa + (int64_t)m * p.ldsa + 4 * q;
+    }
+    const T *x = (const T *)px.x + (int64_t)min(r, p.M - 1) * px.ldx;
+
+    mx_f32x4 acc[MF][NF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            acc[i][j] = mx_f32x4{};
+
+    for (int g = wave; g < groups; g += NW) {
+        const int blk = 16 * g + 4 * q;   // first of this lane's four blocks
+        mx_i32x4 b[NF][4], a[MF][4];
+        int sb[NF], sa[MF];
+        auto load4 = [&](const uint8_t *row, mx_i32x4 (&v)[4]) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                v[s] = blk + s < nb ? *reinterpret_cast<const mx_i32x4 *>(row + (int64_t)g * 256 + 16 * s)
+                                    : mx_i32x4{0, 0, 0, 0};
+        };
+        auto load_scales = [&](const uint8_t *row) {
+            return blk < nb ? mx_mask_scales(*reinterpret_cast<const int *>(row + 16 * g), blk, nb) : 0;
+        };
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            load4(bq[j], b[j]);
+            sb[j] = load_scales(bs[j]);
+        }
+        if constexpr (FUSED) {
+            uint32_t word = 0;
+            const bool live = r < p.M;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                uint32_t u[4][MxPack<T>::WORDS8];
+                uint32_t am = 0;
+#pragma unroll
+                for (int o = 0; o < 4; ++o) {
+                    mx_load8<T, VEC>(x, 32 * (blk + s) + 8 * o, live ? px.K : 0, u[o]);
+                    am = max(am, mx_amax8<T>(u[o]));
+                }
+                const uint32_t sc = mx_scale_of(am);
+#pragma unroll
+                for (int o = 0; o < 4; ++o)
+                    a[0][s][o] = (int)mx_pack8<T>(u[o], sc);
+                word |= sc << (8 * s);
+            }
+            sa[0] = (int)word;
+        } else {
+#pragma unroll
+            for (int i = 0; i < MF; ++i) {
+                load4(aq[i], a[i]);
+                sa[i] = load_scales(as[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                acc[i][j] = mx_mfma16<0>(a[i][0], b[j][0], acc[i][j], sa[i], sb[j]);
+                acc[i][j] = mx_mfma16<1>(a[i][1], b[j][1], acc[i][j], sa[i], sb[j]);
+                acc[i][j] = mx_mfma16<2>(a[i][2], b[j][2], acc[i][j], sa[i], sb[j]);
+                acc[i][j] = mx_mfma16<3>(a[i][3], b[j][3], acc[i][j], sa[i], sb[j]);
+            }
+    }
+    // register d of lane l: row 4 (l / 16) + d, column l % 16 of the block
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                red[wave][i * NF + j][d][lane] = acc[i][j][d];
+    __syncthreads();
+    for (int f = tid; f < MF * NF * 256; f += 512) {
+        // consecutive threads take consecutive columns
+        const int col = f % (16 * NF), row = f / (16 * NF);
+        const int i = row / 16, j = col / 16, d = row % 4, l = (row % 16) / 4 * 16 + col % 16;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            s += red[w][i * NF + j][d][l];
+        const int n = n0 + col;
+        if (row < p.M && n < p.N)
+            ((T *)p.c)[(int64_t)row * p.ldc + n] = (T)(s + mx_bias<T>(p.bias, n));
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+struct MxCfg { int BM, BN; };
+static const MxCfg kMxCfg[] = {{256, 256}, {256, 128}, {128, 128}, {64, 64}};
+
+MxPlan plan_mx(int64_t M, int64_t N, int64_t nb, int cu_count) {
+    MxPlan pl = {MX_TILE, 0, 1, 0, 0};
+    if (nb == 0) {
+        pl.kind = MX_EMPTY;
+        return pl;
+    }
+    if (M <= 64) {
+        pl.kind = MX_SKINNY;
+        pl.cfg = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
+        return pl;
+    }
+    auto tiles = [&](int c) {
+        return ((M + kMxCfg[c].BM - 1) / kMxCfg[c].BM) * ((N + kMxCfg[c].BN - 1) / kMxCfg[c].BN);
+    };
+    pl.cfg = 3;
+    for (int c = 0; c < 3; ++c)
+        if (tiles(c) >= cu_count) {
+            pl.cfg = c;
+            break;
+        }
+    const int64_t stages = (nb + 7) / 8, t = tiles(pl.cfg);
+    pl.slice = (int)stages;
+    // too few tiles for the chip and a long K: split it
+    if (t * 2 <= cu_count && stages >= 8) {
+        int64_t ks = cu_count / t;
+        if (ks > stages / 4)
+            ks = stages / 4;
+        if (ks > 16)
+            ks = 16;
+        if (ks > 1) {
+            pl.slice = (int)((stages + ks - 1) / ks);
+            pl.ks = (int)((stages + pl.slice - 1) / pl.slice);
+            if (pl.ks > 1)
+                pl.partial_bytes = pl.ks * M * ((N + 3) / 4 * 4) * 4;
+        }
+    }
+    return pl;
+}
+
+bool mx_fuses(const MxPlan &plan, int64_t M) { return plan.kind == MX_SKINNY && M <= 16; }
+
+template <typename OUT, int BM, int BN, int WGM, int WGN, int NS>
+static void tile_one(const MxGemm &p, const MxPlan &plan, hipStream_t stream) {
+    const int tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
+    hipLaunchKernelGGL((mx_tile_kernel<OUT, BM, BN, WGM, WGN, NS>), dim3((unsigned)(tm * tn), plan.ks),
+                       dim3(64 * WGM * WGN), 0, stream, p, tm, tn, plan.slice);
+}
+
+template <typename OUT>
+static void tile_cfg(const MxGemm &p, const MxPlan &plan, hipStream_t stream) {
+    switch (plan.cfg) {
+    case 0: tile_one<OUT, 256, 256, 2, 2, 2>(p, plan, stream); break;
+    case 1: tile_one<OUT, 256, 128, 2, 2, 3>(p, plan, stream); break;
+    case 2: tile_one<OUT, 128, 128, 2, 2, 2>(p, plan, stream); break;
+    default: tile_one<OUT, 64, 64, 2, 2, 3>(p, plan, stream); break;
+    }
+}
+
+template <typename OUT>
+static void join(const float *part, int64_t ldp, int ks, const MxGemm &p, hipStream_t stream) {
+    const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
+    hipLaunchKernelGGL((mx_join_kernel<OUT>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, stream,
+                       part, ldp, ks, p);
+}
+
+template <typename T>
+static hipError_t gemm_type(const MxGemm &p, const MxPlan &plan, float *partial, hipStream_t stream) {
+    if (plan.kind == MX_EMPTY) {
+        join<T>(nullptr, 0, 0, p, stream);
+    } else if (plan.kind == MX_SKINNY) {
+        const MxSkinnyX px = {};
+        if (plan.cfg == 1)
+            hipLaunchKernelGGL((mx_skinny_kernel<T, 1, 1, false, true>), dim3((p.N + 15) / 16), dim3(512), 0, stream, p, px);
+        else if (plan.cfg == 2)
+            hipLaunchKernelGGL((mx_skinny_kernel<T, 2, 1, false, true>), dim3((p.N + 15) / 16), dim3(512), 0, stream, p, px);
+        else
+            hipLaunchKernelGGL((mx_skinny_kernel<T, 4, 1, false, true>), dim3((p.N + 15) / 16), dim3(512), 0, stream, p, px);
+    } else if (plan.ks > 1) {
+        MxGemm s = p;
+        s.c = partial;
+        s.ldc = (p.N + 3) / 4 * 4;
+        s.bias = nullptr;
+        tile_cfg<float>(s, plan, stream);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+        join<T>(partial, s.ldc, plan.ks, p, stream);
+    } else {
+        tile_cfg<T>(p, plan, stream);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_mx_gemm(int type, const MxGemm &p, const MxPlan &plan, float *partial, hipStream_t stream) {
+    switch (type) {
+    case MPGEMM_TYPE_F16: return gemm_type<_Float16>(p, plan, partial, stream);
+    case MPGEMM_TYPE_BF16: return gemm_type<__bf16>(p, plan, partial, stream);
+    default: return gemm_type<float>(p, plan, partial, stream);
+    }
+}
+
+template <typename T>
+static hipError_t gemm_x_type(const MxGemm &p, const MxSkinnyX &px, hipStream_t stream) {
+    const bool vec = (reinterpret_cast<uintptr_t>(px.x) & 15) == 0 && (px.ldx * sizeof(T)) % 16 == 0;
+    if (vec)
+        hipLaunchKernelGGL((mx_skinny_kernel<T, 1, 1, true, true>), dim3((p.N + 15) / 16), dim3(512), 0, stream, p, px);
+    else
+        hipLaunchKernelGGL((mx_skinny_kernel<T, 1, 1, true, false>), dim3((p.N + 15) / 16), dim3(512), 0, stream, p, px);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx_gemm_x(int type, const MxGemm &p, const MxSkinnyX &px, const MxPlan &plan, hipStream_t stream) {
+    if (!mx_fuses(plan, p.M))
+        return hipErrorInvalidValue;
+    switch (type) {
+    case MPGEMM_TYPE_F16: return gemm_x_type<_Float16>(p, px, stream);
+    case MPGEMM_TYPE_BF16: return gemm_x_type<__bf16>(p, px, stream);
+    default: return gemm_x_type<float>(p, px, stream);
+    }
+}
+
+}  // namespace mpg
