@@ -518,193 +518,90 @@ def gemm_w4a4_lowrank(A, B, K, sx, sw, X, LD, LU, bias=None, out=None, handle=No
 # (R x 16 nb, nb = ceil(K / 32) blocks) and scales (R x nb), both with row
 # strides that are multiples of 16 bytes. The scales that these calls return
 # are views of rows padded to 16 bytes.
+#
+# The calls are short enough for the host's share to count, so their checks,
+# allocations and the C-ABI call are compiled (csrc/torch_calls.cpp); a call on
+# another stream is the same call with that stream made current, so that the
+# allocator hands out no memory which another stream still uses, and takes none
+# back before this one is done.
 
-_mx_types = None
-_cu_counts = {}
-
-
-def _mx_type(dtype, name, f32=True):
-    global _mx_types
-    if _mx_types is None:
-        import torch
-        _mx_types = {torch.float16: MPGEMM_TYPE_F16, torch.bfloat16: MPGEMM_TYPE_BF16, torch.float32: MPGEMM_TYPE_F32}
-    t = _mx_types.get(dtype)
-    if t is None or (t == MPGEMM_TYPE_F32 and not f32):
-        raise TypeError(f"{name}: expected float16, bfloat16{' or float32' if f32 else ''}, got {dtype}")
-    return t
+calls_path = os.path.join(_HERE, "_torch_calls.so")
+_calls = None
 
 
-def _cus(device):
-    n = _cu_counts.get(device.index)
-    if n is None:
-        import torch
-        n = _cu_counts[device.index] = torch.cuda.get_device_properties(device).multi_processor_count
-    return n
+def _load_calls():
+    global _calls
+    import importlib.machinery
+    import importlib.util
+
+    import torch  # noqa: F401  (the extension's libraries)
+    lib()
+    if not os.path.exists(calls_path):
+        raise RuntimeError(f"{calls_path} is not built; run `python -m precision_dense_gemm_tiled_amd.build`")
+    loader = importlib.machinery.ExtensionFileLoader("_torch_calls", calls_path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_torch_calls", loader))
+    loader.exec_module(module)
+    _calls = module
+    return module
 
 
-def _held(q, s, K, name, device):
-    """Row strides (bytes) of codes and scales of rows of K elements."""
+def _cu_count(index):
     import torch
-    ldq, lds = _rows(q, torch.uint8, f"{name} codes"), _rows(s, torch.uint8, f"{name} scales")
-    nb = (K + 31) // 32
-    if q.shape[1] != 16 * nb or s.shape[1] != nb or s.shape[0] != q.shape[0]:
-        raise ValueError(f"{name}: {tuple(q.shape)} codes and {tuple(s.shape)} scales for rows of {K} elements")
-    if q.device != device or s.device != device:
-        raise ValueError(f"{name}: not on {device}")
-    # (one row, or scales held without a row stride: the stride is not used)
-    return ldq, lds if s.shape[0] > 1 else (lds + 15) // 16 * 16
+    return torch.cuda.get_device_properties(index).multi_processor_count
 
 
-def _mx_bias(bias, n, dtype, device):
-    if bias is None:
-        return None
-    if bias.dtype != dtype or bias.shape != (n,) or not bias.is_contiguous() or bias.device != device:
-        raise ValueError(f"bias: expected {n} contiguous {dtype} values on {device}")
-    return bias.data_ptr()
-
-
-def _mx_out(out, shape, dtype, device, name="out"):
-    """The result (new, or the caller's) and its row stride."""
+def _on(stream, t):
+    """Context that makes `stream` (a torch stream or a raw one) current on t's device."""
     import torch
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device), max(shape[1], 1)
-    if tuple(out.shape) != tuple(shape) or out.device != device:
-        raise ValueError(f"{name}: expected {tuple(shape)} on {device}, got {tuple(out.shape)} on {out.device}")
-    return out, _rows(out, dtype, name)
-
-
-def _held_empty(rows, K, device):
-    import torch
-    nb = (K + 31) // 32
-    return (torch.empty((rows, 16 * nb), dtype=torch.uint8, device=device),
-            torch.empty((rows, (nb + 15) // 16 * 16), dtype=torch.uint8, device=device)[:, :nb])
-
-
-def _on(stream, device):
-    """(raw stream, context): new tensors of a call on `stream` are allocated
-    for that stream, so that the allocator hands out no memory which another
-    stream still uses, and takes none back before this one is done."""
-    import contextlib
-
-    import torch
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream, None
-    raw = getattr(stream, "cuda_stream", stream)
-    s = stream if isinstance(stream, torch.cuda.Stream) else (
-        torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device))
-    stack = contextlib.ExitStack()
-    stack.enter_context(torch.cuda.stream(s))
-    return raw, stack
-
-
-def _mx_call(stream, device, handle, body):
-    """body(raw stream, handle), with new tensors allocated for the stream."""
-    raw, ctx = _on(stream, device)
-    h = default_handle(device.index) if handle is None else handle
-    if ctx is None:
-        return body(raw, h)
-    with ctx:
-        return body(raw, h)
-
-
-def _scratch(nbytes, device, what):
-    import torch
-    if nbytes < 0:
-        raise MpgemmError(MPGEMM_ERR_UNSUPPORTED, what)
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = getattr(stream, "cuda_stream", stream)
+        stream = torch.cuda.ExternalStream(raw, device=t.device) if raw else torch.cuda.default_stream(t.device)
+    return torch.cuda.stream(stream)
 
 
 def quantize_mxfp4(X, handle=None, stream=None):
     """MXFP4 form of X (M x K, fp16, bf16 or fp32) along its rows: codes
     (M x 16 nb) and scales (M x nb)."""
-    t = _mx_type(X.dtype, "X")
-    ldx = _rows(X, X.dtype, "X")
-    M, K = X.shape
-
-    def body(s, h):
-        q, sc = _held_empty(M, K, X.device)
-        _check(mpgemm_quantize_mxfp4(h, M, K, t, X.data_ptr(), ldx, q.data_ptr(), q.stride(0), sc.data_ptr(),
-                                     sc.stride(0), None, 0, None, 0, s), "mpgemm_quantize_mxfp4")
-        return q, sc
-    return _mx_call(stream, X.device, handle, body)
+    if stream is not None:
+        with _on(stream, X):
+            return quantize_mxfp4(X, handle)
+    return (_calls or _load_calls()).quantize(X, False, handle)
 
 
 def quantize_mxfp4_both(X, handle=None, stream=None):
     """MXFP4 forms of X (M x K) and of X^T (K x M) in one pass over X: codes and
     scales of X, then of X^T."""
-    t = _mx_type(X.dtype, "X")
-    ldx = _rows(X, X.dtype, "X")
-    M, K = X.shape
-
-    def body(s, h):
-        q, sc = _held_empty(M, K, X.device)
-        qt, sct = _held_empty(K, M, X.device)
-        _check(mpgemm_quantize_mxfp4(h, M, K, t, X.data_ptr(), ldx, q.data_ptr(), q.stride(0), sc.data_ptr(),
-                                     sc.stride(0), qt.data_ptr(), qt.stride(0), sct.data_ptr(), sct.stride(0), s),
-               "mpgemm_quantize_mxfp4")
-        return q, sc, qt, sct
-    return _mx_call(stream, X.device, handle, body)
+    if stream is not None:
+        with _on(stream, X):
+            return quantize_mxfp4_both(X, handle)
+    return (_calls or _load_calls()).quantize(X, True, handle)
 
 
 def dequantize_mxfp4(q, s, K, dtype=None, out=None, handle=None, stream=None):
     """The values (M x K) that codes and scales stand for, in fp16, bf16 or fp32
     (the default)."""
-    import torch
-    dtype = (torch.float32 if out is None else out.dtype) if dtype is None else dtype
-    t = _mx_type(dtype, "dtype")
-    ldq, lds = _held(q, s, K, "q", q.device)
-
-    def body(st, h):
-        Y, ldy = _mx_out(out, (q.shape[0], K), dtype, q.device)
-        _check(mpgemm_dequantize_mxfp4(h, q.shape[0], K, q.data_ptr(), ldq, s.data_ptr(), lds, t, Y.data_ptr(), ldy,
-                                       st), "mpgemm_dequantize_mxfp4")
-        return Y
-    return _mx_call(stream, q.device, handle, body)
+    if stream is not None:
+        with _on(stream, q):
+            return dequantize_mxfp4(q, s, K, dtype, out, handle)
+    return (_calls or _load_calls()).dequantize(q, s, K, dtype, out, handle)
 
 
 def gemm_mxfp4(Aq, As, Bq, Bs, K, bias=None, dtype=None, out=None, handle=None, stream=None):
     """C = A @ B.T + bias with both operands held in MXFP4 (rows of K elements);
     C and bias in fp16, bf16 or fp32 (the default)."""
-    import torch
-    dtype = (torch.float32 if out is None else out.dtype) if dtype is None else dtype
-    t = _mx_type(dtype, "dtype")
-    dev = Aq.device
-    lda, ldsa = _held(Aq, As, K, "A", dev)
-    ldb, ldsb = _held(Bq, Bs, K, "B", dev)
-    M, N = Aq.shape[0], Bq.shape[0]
-    b = _mx_bias(bias, N, dtype, dev)
-
-    def body(s, h):
-        C, ldc = _mx_out(out, (M, N), dtype, dev)
-        n = mpgemm_run_mxfp4_workspace(M, N, K, _cus(dev))
-        ws = _scratch(n, dev, "mpgemm_run_mxfp4")
-        _check(mpgemm_run_mxfp4(h, M, N, K, Aq.data_ptr(), lda, As.data_ptr(), ldsa, Bq.data_ptr(), ldb,
-                                Bs.data_ptr(), ldsb, b, t, C.data_ptr(), ldc, None if ws is None else ws.data_ptr(),
-                                n, s), "mpgemm_run_mxfp4")
-        return C
-    return _mx_call(stream, dev, handle, body)
+    if stream is not None:
+        with _on(stream, Aq):
+            return gemm_mxfp4(Aq, As, Bq, Bs, K, bias, dtype, out, handle)
+    return (_calls or _load_calls()).gemm(Aq, As, Bq, Bs, K, bias, dtype, out, handle)
 
 
 def gemm_mxfp4_dyn(X, Wq, Ws, bias=None, out=None, handle=None, stream=None):
     """Y = MX(X) @ W.T + bias: X (M x K, fp16, bf16 or fp32) is quantised along
     its rows in the call, W (N x K) is held in MXFP4; Y and bias in X's type."""
-    t = _mx_type(X.dtype, "X")
-    dev = X.device
-    ldx = _rows(X, X.dtype, "X")
-    M, K = X.shape
-    ldw, ldsw = _held(Wq, Ws, K, "W", dev)
-    N = Wq.shape[0]
-    b = _mx_bias(bias, N, X.dtype, dev)
-
-    def body(s, h):
-        Y, ldy = _mx_out(out, (M, N), X.dtype, dev)
-        n = mpgemm_run_mxfp4_dyn_workspace(M, N, K, _cus(dev))
-        ws = _scratch(n, dev, "mpgemm_run_mxfp4_dyn")
-        _check(mpgemm_run_mxfp4_dyn(h, M, N, K, t, X.data_ptr(), ldx, Wq.data_ptr(), ldw, Ws.data_ptr(), ldsw, b,
-                                    Y.data_ptr(), ldy, None if ws is None else ws.data_ptr(), n, s),
-               "mpgemm_run_mxfp4_dyn")
-        return Y
-    return _mx_call(stream, dev, handle, body)
+    if stream is not None:
+        with _on(stream, X):
+            return gemm_mxfp4_dyn(X, Wq, Ws, bias, out, handle)
+    return (_calls or _load_calls()).dyn(X, Wq, Ws, bias, out, handle)
 
 
 def gemm_mxfp4_backward(dY, WTq, WTs, XTq, XTs, need_dx=True, need_dw=True, handle=None, stream=None):
@@ -712,35 +609,10 @@ def gemm_mxfp4_backward(dY, WTq, WTs, XTq, XTs, need_dx=True, need_dw=True, hand
     axes in the call: dX = MX(dY) @ W (M x K, dY's type) and dW = MX(dY.T) @ X
     (N x K, fp32). W^T (K x N) and X^T (K x M) are held in MXFP4. A gradient
     that is not needed is None (its operand may be None too)."""
-    import torch
-    t = _mx_type(dY.dtype, "dY")
-    dev = dY.device
-    lddy = _rows(dY, dY.dtype, "dY")
-    M, N = dY.shape
-    if not (need_dx or need_dw):
-        return None, None
-    ldwt = ldswt = ldxt = ldsxt = 0
-    if need_dx:
-        ldwt, ldswt = _held(WTq, WTs, N, "W^T", dev)
-    if need_dw:
-        ldxt, ldsxt = _held(XTq, XTs, M, "X^T", dev)
-    K = (WTq if need_dx else XTq).shape[0]
-    if need_dx and need_dw and XTq.shape[0] != K:
-        raise ValueError("W^T and X^T disagree on K")
-
-    def body(s, h):
-        dX = torch.empty((M, K), dtype=dY.dtype, device=dev) if need_dx else None
-        dW = torch.empty((N, K), dtype=torch.float32, device=dev) if need_dw else None
-        n = mpgemm_run_mxfp4_backward_workspace(M, N, K, _cus(dev))
-        ws = _scratch(n, dev, "mpgemm_run_mxfp4_backward")
-        _check(mpgemm_run_mxfp4_backward(
-            h, M, N, K, t, dY.data_ptr(), lddy, WTq.data_ptr() if need_dx else None, ldwt,
-            WTs.data_ptr() if need_dx else None, ldswt, XTq.data_ptr() if need_dw else None, ldxt,
-            XTs.data_ptr() if need_dw else None, ldsxt, dX.data_ptr() if need_dx else None, max(K, 1),
-            dW.data_ptr() if need_dw else None, max(K, 1), None if ws is None else ws.data_ptr(), n, s),
-            "mpgemm_run_mxfp4_backward")
-        return dX, dW
-    return _mx_call(stream, dev, handle, body)
+    if stream is not None:
+        with _on(stream, dY):
+            return gemm_mxfp4_backward(dY, WTq, WTs, XTq, XTs, need_dx, need_dw, handle)
+    return (_calls or _load_calls()).backward(dY, WTq, WTs, XTq, XTs, need_dx, need_dw, handle)
 
 
 def newton_schulz(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out=None, handle=None, stream=None):
@@ -748,31 +620,7 @@ def newton_schulz(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out=No
     or bf16: X = G / (|G| + eps), then `steps` times X <- a X + (b A + c A A) X
     with A = X X^T (on the smaller side), in products of fp32 quality. `out` may
     be G itself."""
-    import torch
-    t = _mx_type(G.dtype, "G", f32=False)
-    if G.dim() not in (2, 3):
-        raise ValueError("G: expected a matrix or a batch of matrices")
-    if len(coeffs) != 3:
-        raise ValueError("coeffs: expected three numbers")
-    dev = G.device
-    B = 1 if G.dim() == 2 else G.shape[0]
-    M, N = G.shape[-2:]
-
-    def strides(x, name):
-        m = x if x.dim() == 2 else (x[0] if B else x.new_empty((M, N)))
-        return _rows(m, G.dtype, name), x.stride(0) if x.dim() == 3 and B > 1 else 0
-
-    ldg, sg = strides(G, "G")
-
-    def body(s, h):
-        Y = torch.empty(G.shape, dtype=G.dtype, device=dev) if out is None else out
-        if Y.shape != G.shape or Y.device != dev:
-            raise ValueError(f"out: expected {tuple(G.shape)} on {dev}")
-        ldy, sy = strides(Y, "out")
-        n = mpgemm_run_newton_schulz_workspace(B, M, N)
-        ws = _scratch(n, dev, "mpgemm_run_newton_schulz")
-        _check(mpgemm_run_newton_schulz(h, B, M, N, t, G.data_ptr(), ldg, sg, steps, coeffs, eps, Y.data_ptr(), ldy,
-                                        sy, None if ws is None else ws.data_ptr(), n, s),
-               "mpgemm_run_newton_schulz")
-        return Y
-    return _mx_call(stream, dev, handle, body)
+    if stream is not None:
+        with _on(stream, G):
+            return newton_schulz(G, steps, coeffs, eps, out, handle)
+    return (_calls or _load_calls()).newton_schulz(G, steps, coeffs, eps, out, handle)

@@ -2,20 +2,25 @@
 
 Every source is compiled for gfx950 only, with packed-fp32 instruction
 selection disabled (-packed-fp32-ops), then linked into one shared library in
-this package directory, next to the Python binding that loads it.
+this package directory, next to the Python binding that loads it. The compiled
+torch-facing calls (host code only) become a second one beside it.
 """
 import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmpgemm.so")
+CALLS = os.path.join(HERE, "_torch_calls.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 SOURCES = ["api.cpp", "gemm_tile.hip", "w4a16.hip", "quantize.hip", "noalloc.hip", "stream_read.hip", "lowrank.hip",
            "api_mxfp4.cpp", "mxfp4_quantize.hip", "mxfp4_gemm.hip", "newton_schulz.hip"]
+TORCH_SOURCE = "torch_calls.cpp"
 
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -23,28 +28,51 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
 
-def build(verbose: bool = False, jobs: int = 4) -> str:
+def _torch_flags():
+    """Compile and link flags of the torch-facing calls."""
+    import torch
+    from torch.utils import cpp_extension
+    inc = cpp_extension.include_paths() + ["/opt/rocm/include", sysconfig.get_path("include")]
+    comp = ["-w"] + [f for i in inc for f in ("-isystem", i)] \
+        + [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1"]
+    link = ["-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu",
+            "-ltorch_python", "-L", HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    return comp, link
+
+
+def build(verbose: bool = False, jobs: int = 6) -> str:
     objdir = os.path.join(ROOT, "_build", "mpgemm")
     os.makedirs(objdir, exist_ok=True)
+    torch_comp, torch_link = _torch_flags()
 
     def compile_one(src):
         obj = os.path.join(objdir, src + ".o")
-        cmd = [HIPCC] + FLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
+        if src == TORCH_SOURCE:   # (host code: no kernels in it)
+            cmd = [CXX, "-O2", "-std=c++17", "-fPIC"] + torch_comp + ["-I", os.path.join(ROOT, "include")]
+        else:
+            cmd = [HIPCC] + FLAGS
+        cmd = cmd + ["-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"hipcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"compiling {src} failed:\n{r.stdout}\n{r.stderr}")
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
+        *objs, torch_obj = ex.map(compile_one, SOURCES + [TORCH_SOURCE])
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    tmp = CALLS + ".tmp"
+    cmd = [CXX, "-shared", "-o", tmp, torch_obj] + torch_link
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, CALLS)
     return LIB
 
 
