@@ -346,7 +346,7 @@ mpgemm_status_t mpgemm_run_newton_schulz(mpgemm_handle_t h, int64_t batch, int64
         return MPGEMM_ERR_HIP;
     const float zero[3] = {0.f, 0.f, 0.f};
     const float *k = coeffs ? coeffs : zero;
-    const mpg::NewtonSchulz p{G, Y, ldg, strideg, ldy, stridey, (int)batch, (int)M, (int)N, steps, k[0], k[1], k[2], eps};
+    const mpg::NewtonSchulz p{G, Y, ldg, strideg, ldy, stridey, (int)batch, (int)M, (int)N, steps, k[0], k[1], k[2], eps, h->cu_count};
     return status_of(mpg::launch_newton_schulz(type, p, workspace, static_cast<hipStream_t>(stream)));
 }
 

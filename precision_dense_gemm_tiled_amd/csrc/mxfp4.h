@@ -68,6 +68,7 @@ struct NewtonSchulz {
     int batch, M, N;
     int steps;
     float a, b, c, eps;
+    int cus;   // CUs of the device
 };
 int64_t newton_schulz_bytes(int64_t batch, int64_t M, int64_t N);
 hipError_t launch_newton_schulz(int type, const NewtonSchulz &p, void *workspace, hipStream_t stream);

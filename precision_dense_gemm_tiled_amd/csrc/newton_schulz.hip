@@ -1,24 +1,33 @@
 // Newton-Schulz orthogonalisation of a batch of matrices:
-//   X = G / (|G|_F + eps), then `steps` times
-//   A = X X^T,  P = b A + c A A,  X <- a X + P X
+//   X = G / (|G|_F + eps), then `steps` times X <- Q X with Q = a I + b A + c A A, A = X X^T
 // on the smaller side (X is m x n with m <= n, G or its transpose).
 //
-// Every product is of fp32 quality at the bf16 matrix rate: each factor is held
-// as the sum of two bf16 values, h + l (h = bf16(x), l = bf16(x - h): 16
-// significant bits with the full range of fp32), and a product is
-// h h + h l + l h with fp32 sums; l l is below the rounding of the sum. One
-// bf16 (or fp16) value per factor is not enough: the polynomial multiplies the
-// small singular values by about a at every step (485 times in all with the
-// usual coefficients), and their rounding errors with them. Measured against
-// 64 bits on gradients of rank 64 plus noise, 1024 x 256: 2.3e-2 with one bf16
-// value, 3e-3 with one fp16 value, 2e-4 (the output's own rounding, fp16) with
-// two.
+// Every Q is a polynomial of A, so all of them commute and the iteration needs
+// X at its ends only:
+//   A = X X^T;   per step: Q = a I + b A + c A A,  T = Q A,  A <- Q T,  W <- Q W;   X <- W X.
+// Per step that is four symmetric m x m products (the tiles on and below the
+// diagonal, the others mirrored), 4 m^3 flop, against m^2 n + m^3 + 2 m^2 n for
+// forming A and Q X anew: the same for a square matrix, less than a third at n = 4 m
+// (8192 x 2048: 2264 -> 893 us together with the single-part X below). What it
+// costs is accuracy: an error of A in the direction of a small singular value
+// grows by about a^2 per step, as that eigenvalue of A does, and A has to be formed
+// anew from X once it is no longer small; see group_length.
 //
-// Layout: X is needed with n contiguous (A = X X^T contracts over n) and with m
-// contiguous (P X contracts over m), so both are stored; A and P are symmetric
-// and only the tiles on and below the diagonal are computed, the others
-// mirrored. Rows and columns are padded with zeros to multiples of 64, which
-// the products keep zero.
+// Every product is of fp32 quality at the fp16 matrix rate: a factor is held as
+// the sum of two fp16 values of a scaled matrix, h = fp16(2^e x), l = fp16(2^e x - h):
+// 22 significant bits, and a product is h h + h l + l h with fp32 sums; l l is below
+// the rounding of the sum. The exponents e put each matrix's spectral norm, which
+// bounds its entries, at about 2^13 of fp16's 2^16. They come from bounds that
+// follow from |singular values of X| <= 1 and the polynomial, and are found per
+// matrix on the GPU (ns_norm_kernel), so any coefficients and any |G| against eps
+// work. G itself (fp16 or bf16) needs one part: scaled by a power of two it is an
+// fp16 matrix exactly, but for entries below 2^-26 |G|. So the first A is one
+// product and the first W X two.
+//
+// Measured against 64 bits before the output's rounding (rms 1.7e-3 of the norm for
+// bf16, 2.1e-4 for fp16), five steps: 4e-6 on gradients of rank 64 plus noise, 3e-5 on
+// rank 8 with noise of 1e-2 below it, in groups of three steps; 6e-5 and 1.7e-4 in one
+// group of five. Single fp16 values without the l part: 1.5e-3 and 3e-3.
 #include <cfloat>
 
 #include "mxfp4.h"
@@ -28,305 +37,505 @@ namespace mpg {
 
 typedef int ns_i32x4 __attribute__((ext_vector_type(4)));
 typedef float ns_f32x16 __attribute__((ext_vector_type(16)));
-typedef __bf16 ns_bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 ns_f16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t ns_u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t ns_u32x4 __attribute__((ext_vector_type(4)));
 
-// A matrix of h and l parts, rows of `ld` elements.
+// A matrix of one part (rows of `ld` fp16 values) or two (rows of `ld` / 64 lines of
+// 128 bytes, each 32 h and their 32 l: the 128 bytes that a stage of the products
+// takes from a row are one cache line).
 struct NsMat {
-    uint16_t *h, *l;
-    int64_t ld, stride;   // elements; stride between matrices of the batch
+    uint16_t *p;
+    int64_t ld, stride;   // in 16-bit values; stride between matrices of the batch
 };
 
-__device__ __forceinline__ uint16_t ns_bf16(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
-__device__ __forceinline__ float ns_f32(uint32_t h) { return __uint_as_float(h << 16); }
+__device__ __forceinline__ uint16_t ns_half(float x) { return __builtin_bit_cast(uint16_t, (_Float16)x); }
+__device__ __forceinline__ float ns_f32(uint32_t h) { return (float)__builtin_bit_cast(_Float16, (uint16_t)h); }
 
 // x as h | l << 16
 __device__ __forceinline__ uint32_t ns_split(float x) {
-    const uint16_t h = ns_bf16(x);
-    return h | ((uint32_t)ns_bf16(x - ns_f32(h)) << 16);
+    const uint16_t h = ns_half(x);
+    return h | ((uint32_t)ns_half(x - ns_f32(h)) << 16);
 }
 
-// Sum over the workgroup's 256 threads, in every thread, in a fixed order.
-__device__ __forceinline__ float ns_block_sum(float v, float *red) {
+// ------------------------------------------------------------ ends
+
+// 8 elements of a row from column c0 on, zeros past the row's end.
+template <typename T, bool VEC>
+__device__ __forceinline__ void ns_load8(const T *row, int c0, int cols, T (&v)[8]) {
+    if (VEC && c0 + 8 <= cols) {
+        const ns_u32x4 w = *reinterpret_cast<const ns_u32x4 *>(row + c0);
+        __builtin_memcpy(v, &w, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = c0 + i < cols ? row[c0 + i] : (T)0.f;
+    }
+}
+
+// Sum of squares of each 64 x 64 tile of G. In 64 bits: bf16 squares leave the
+// range of fp32 at both ends, and the pass is bound by memory.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(256) void ns_square_kernel(NewtonSchulz p, int batch0, double *sums) {
+    __shared__ double red[4];
+    const int tid = threadIdx.x;
+    const T *G = (const T *)p.g + (int64_t)(batch0 + blockIdx.z) * p.strideg;
+    const int r0 = blockIdx.y * 64 + tid / 8, c0 = blockIdx.x * 64 + (tid & 7) * 8;
+    double s = 0.;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (r0 + 32 * i < p.M) {
+            T v[8];
+            ns_load8<T, VEC>(G + (int64_t)(r0 + 32 * i) * p.ldg, c0, p.N, v);
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+                s += (double)(float)v[d] * (double)(float)v[d];
+        }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1)
-        v += __shfl_xor(v, o);
-    if ((threadIdx.x & 63) == 0)
-        red[threadIdx.x >> 6] = v;
+        s += __shfl_xor(s, o);
+    if ((tid & 63) == 0)
+        red[tid >> 6] = s;
     __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
+    if (tid == 0)
+        sums[((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// G (M x N) -> X (m x n, padded) and X^T, unscaled, and the sum of squares of
-// each 64 x 64 tile. FLIP: G is taller than wide, X = G^T.
-template <typename T, bool FLIP>
-__global__ __launch_bounds__(256) void ns_load_kernel(NewtonSchulz p, int batch0, NsMat X, NsMat XT, float *sums) {
-    __shared__ uint32_t tile[64][65];
-    __shared__ float red[4];
+// Per matrix: head[0] = the power of two that G is scaled by (NaN when |G| is not
+// finite, which makes the whole result NaN), head[1] = 1 / (|G| + eps); then for
+// each step the factors of the products' epilogues.
+enum { NS_Q_ACC, NS_Q_ADD, NS_Q_ONE, NS_T, NS_A, NS_W, NS_GRAM, NS_APPLY, NS_FACTORS };
+
+struct NsGroups {
+    int len, longer;   // groups of len + 1 steps, `longer` of them, then of len
+    __host__ __device__ bool starts(int k) const {
+        const int head = longer * (len + 1);
+        return k < head ? k % (len + 1) == 0 : (k - head) % len == 0;
+    }
+};
+
+// Exponent that takes a matrix of spectral norm `bound` to about 2^13.
+__device__ __forceinline__ int ns_exponent(float bound) {
+    if (!(bound > 0.f && bound < FLT_MAX))
+        return 0;
+    return 13 - (ilogbf(bound) + 1);
+}
+
+__global__ __launch_bounds__(256) void ns_norm_kernel(const double *sums, int tiles, NewtonSchulz p, NsGroups gr,
+                                                      float *head, float *factors) {
+    __shared__ double red[4];
+    __shared__ float top[4][5];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    double s = 0.;
+    for (int i = tid; i < tiles; i += 256)
+        s += sums[(int64_t)blockIdx.x * tiles + i];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        s += __shfl_xor(s, o);
+    if (lane == 0)
+        red[wave] = s;
+    __syncthreads();
+    const double norm = sqrt((red[0] + red[1]) + (red[2] + red[3]));
+    const double inv = 1. / (norm + (double)p.eps);
+    const bool finite = norm < DBL_MAX;   // (false for NaN)
+    const int e0 = finite && norm > 0. ? 12 - ilogb(norm) : 0;
+    const float up = finite ? (float)ldexp(1., e0 < 126 ? e0 : 126) : __builtin_nanf("");
+    const int ex0 = e0 < 126 ? e0 : 126;
+    if (tid == 0) {
+        head[2 * blockIdx.x] = up;
+        head[2 * blockIdx.x + 1] = (float)(inv < FLT_MAX ? inv : inv > 0. && norm == 0. && p.eps > 0.f ? FLT_MAX : inv);
+    }
+    // The singular values x of X lie in [0, r]. Thread t looks at x = r t / 255:
+    // the largest |Q|, |T| = |x^2 Q| and next r = |x Q|.
+    float r = finite ? (float)fmin(norm * inv, 1.) : 1.f;
+    double to_x = inv * ldexp(1., -ex0);   // stored X -> X
+    int ew = 0;
+    float wb = 1.f;
+    for (int k = 0; k < p.steps; ++k) {
+        const float x = r * ((float)tid * (1.f / 255.f)), x2 = x * x;
+        const float q = fabsf(p.a + x2 * (p.b + x2 * p.c));
+        float v[3] = {q, q * x2, q * x};
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1)
+#pragma unroll
+            for (int d = 0; d < 3; ++d)
+                v[d] = fmaxf(v[d], __shfl_xor(v[d], o));
+        __syncthreads();   // (the last step's values have been read)
+        if (lane == 0) {
+#pragma unroll
+            for (int d = 0; d < 3; ++d)
+                top[wave][d] = v[d];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int d = 0; d < 3; ++d)
+            v[d] = fmaxf(fmaxf(top[0][d], top[1][d]), fmaxf(top[2][d], top[3][d]));
+        // exponents of this step's matrices (every thread has the same)
+        const int ea = ns_exponent(r * r), eq = ns_exponent(v[0]), et = ns_exponent(v[1]), ea2 = ns_exponent(v[2] * v[2]);
+        const bool first = gr.starts(k), last = k + 1 == p.steps || gr.starts(k + 1);
+        wb = first ? v[0] : wb * v[0];
+        const int ew2 = first ? eq : ns_exponent(wb);
+        const int ex = k + 1 < p.steps ? ns_exponent(v[2]) : 0;
+        if (tid == 0) {
+            float *f = factors + ((int64_t)blockIdx.x * p.steps + k) * NS_FACTORS;
+            auto two = [](int e) { return ldexp(1., e); };
+            f[NS_Q_ACC] = (float)(p.c * two(eq - 2 * ea));
+            f[NS_Q_ADD] = (float)(p.b * two(eq - ea));
+            f[NS_Q_ONE] = (float)(p.a * two(eq));
+            f[NS_T] = (float)two(et - eq - ea);
+            f[NS_A] = (float)two(ea2 - eq - et);
+            f[NS_W] = (float)two(ew2 - eq - ew);
+            f[NS_GRAM] = (float)(to_x * to_x * two(ea));
+            f[NS_APPLY] = (float)(to_x * two(ex - ew2));
+        }
+        ew = ew2;
+        if (last)
+            to_x = ldexp(1., -ex);
+        r = v[2];
+    }
+}
+
+// G (M x N), scaled, as X (m x n, padded) and X^T. FLIP: G is taller than wide, X = G^T.
+template <typename T, bool FLIP, bool VEC>
+__global__ __launch_bounds__(256) void ns_load_kernel(NewtonSchulz p, int batch0, const float *head, NsMat X, NsMat XT) {
+    __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];
     const int tid = threadIdx.x;
     const T *G = (const T *)p.g + (int64_t)(batch0 + blockIdx.z) * p.strideg;
     const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
+    const float up = head[2 * blockIdx.z];
     const NsMat own = FLIP ? XT : X, other = FLIP ? X : XT;   // own: rows as G's
-    const int64_t ob = (int64_t)blockIdx.z * own.stride, tb = (int64_t)blockIdx.z * other.stride;
-    float sq = 0.f;
+    const int g = tid & 7;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int rl = i * 4 + tid / 64, cl = tid & 63;
-        const int row = r0 + rl, col = c0 + cl;
-        const float x = row < p.M && col < p.N ? (float)G[(int64_t)row * p.ldg + col] : 0.f;
-        sq += x * x;
-        const uint32_t w = ns_split(x);
-        own.h[ob + (int64_t)row * own.ld + col] = (uint16_t)w;
-        own.l[ob + (int64_t)row * own.ld + col] = (uint16_t)(w >> 16);
-        tile[rl][cl] = w;
+    for (int i = 0; i < 2; ++i) {
+        const int rl = tid / 8 + 32 * i;
+        uint16_t h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (r0 + rl < p.M) {
+            T v[8];
+            ns_load8<T, VEC>(G + (int64_t)(r0 + rl) * p.ldg, c0 + 8 * g, p.N, v);
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+                h[d] = ns_half((float)v[d] * up);
+        }
+        ns_u32x4 w;
+        __builtin_memcpy(&w, h, 16);
+        *reinterpret_cast<ns_u32x4 *>(own.p + (int64_t)blockIdx.z * own.stride + (int64_t)(r0 + rl) * own.ld + c0 + 8 * g) = w;
+        *reinterpret_cast<ns_u32x4 *>(&tile[rl][8 * g]) = w;
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int cl = i * 4 + tid / 64, rl = tid & 63;
-        const uint32_t w = tile[rl][cl];
-        other.h[tb + (int64_t)(c0 + cl) * other.ld + r0 + rl] = (uint16_t)w;
-        other.l[tb + (int64_t)(c0 + cl) * other.ld + r0 + rl] = (uint16_t)(w >> 16);
-    }
-    const float s = ns_block_sum(sq, red);
-    if (tid == 0)
-        sums[((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = s;
-}
-
-// inv[z] = 1 / (sqrt(sum of the tiles' sums) + eps)
-__global__ __launch_bounds__(256) void ns_norm_kernel(const float *sums, int tiles, float eps, float *inv) {
-    __shared__ float red[4];
-    float s = 0.f;
-    for (int i = threadIdx.x; i < tiles; i += 256)
-        s += sums[(int64_t)blockIdx.x * tiles + i];
-    s = ns_block_sum(s, red);
-    if (threadIdx.x == 0) {
-        const float d = sqrtf(s) + eps;
-        inv[blockIdx.x] = d > 0.f ? fminf(1.f / d, FLT_MAX) : 1.f / d;   // (finite, so that zeros stay zeros)
+    for (int i = 0; i < 2; ++i) {
+        const int cl = (tid & 31) + 32 * i, rg = tid / 32;   // 8 rows of a column
+        uint16_t h[8];
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+            h[d] = tile[8 * rg + d][cl];
+        ns_u32x4 w;
+        __builtin_memcpy(&w, h, 16);
+        *reinterpret_cast<ns_u32x4 *>(other.p + (int64_t)blockIdx.z * other.stride + (int64_t)(c0 + cl) * other.ld + r0 + 8 * rg) = w;
     }
 }
 
-// Y = inv G (no steps)
+// Y = G / (|G| + eps) (no steps)
 template <typename T>
-__global__ __launch_bounds__(256) void ns_scale_kernel(NewtonSchulz p, int batch0, const float *inv) {
+__global__ __launch_bounds__(256) void ns_scale_kernel(NewtonSchulz p, int batch0, const float *head) {
     const int z = batch0 + blockIdx.z;
     const T *G = (const T *)p.g + (int64_t)z * p.strideg;
     T *Y = (T *)p.y + (int64_t)z * p.stridey;
     const int64_t total = (int64_t)p.M * p.N;
+    const float s = head[2 * blockIdx.z] != head[2 * blockIdx.z] ? head[2 * blockIdx.z] : head[2 * blockIdx.z + 1];
     for (int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x; f < total; f += (int64_t)gridDim.x * 256) {
         const int64_t r = f / p.N, c = f - r * p.N;
-        Y[r * p.ldy + c] = (T)((float)G[r * p.ldg + c] * inv[blockIdx.z]);
+        Y[r * p.ldy + c] = (T)((float)G[r * p.ldg + c] * s);
     }
 }
 
-enum { NS_GRAM = 0, NS_POLY = 1, NS_STEP = 2, NS_LAST = 3 };
+// ------------------------------------------------------------ products
 
-struct NsGemm {
-    NsMat a, b;        // operands, K contiguous
-    int M, N, K;       // padded to 64
-    NsMat add;         // POLY: A; STEP, LAST: X (the old iterate)
-    NsMat out, outt;   // result and its transpose (STEP: X and X^T)
-    float ka, kc;      // result = ka * add + kc * (a b^T)
-    const float *inv;  // the first step's factors: GRAM scales by inv^2, STEP and LAST by inv; or null
+// out = f[0] a b^T (+ f[add] add + f[one] I)
+struct NsJob {
+    NsMat a, b;       // operands, K contiguous
+    NsMat add, out, outt;
+    int factor;       // index of the epilogue's factor among the step's
 };
 
-// C tile of 128 x 128 per workgroup, four wavefronts of 64 x 64, stages of 32 of
-// K (64 bytes per row and part) in a two-slot LDS ring. 16-byte chunk c of LDS
-// row r at c ^ swz(r).
-template <typename T, int MODE>
-__global__ __launch_bounds__(256) void ns_gemm_kernel(NsGemm p, NewtonSchulz q, int batch0, int tiles_m,
-                                                      int tiles_n) {
-    constexpr int BT = 128, BKB = 64, CPR = 4, RS = 64, PART = BT * BKB, STAGE = 4 * PART;
-    constexpr int PITCH = 65;
-    constexpr int LDS = 2 * STAGE > 4 * 64 * PITCH * 4 ? 2 * STAGE : 4 * 64 * PITCH * 4;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[LDS];
+struct NsGemm {
+    NsJob job[2];
+    int jobs, nz;
+    int M, N, K;      // padded to 64
+    int tiles_m, tiles;
+    const float *factors;   // of this step, NS_FACTORS each, `fstride` floats between matrices
+    int64_t fstride;
+};
+
+// Results: NS_SYM a symmetric matrix (tiles on and below the diagonal, mirrored),
+// NS_POLY the same with the multiples of `add` and of the identity, NS_X a matrix
+// and its transpose, NS_OUT the caller's Y.
+enum { NS_SYM, NS_POLY, NS_X, NS_OUT };
+
+// PA, PB: parts of the operands. C tile of 2 WT x 2 WT per workgroup, four
+// wavefronts of WT x WT, stages of KS of K in an LDS ring of NS slots. 16-byte chunk c
+// of LDS row r sits at c ^ swz(r), which keeps the fragment reads free of bank
+// conflicts.
+template <int PA, int PB, int WT, int KS, int NS>
+struct NsTile {
+    static constexpr int BT = 2 * WT, TB = WT / 32;
+    static constexpr int RBA = 2 * PA * KS, RBB = 2 * PB * KS;        // bytes of a row and stage
+    static constexpr int CA = RBA / 16, CB = RBB / 16;                // chunks
+    static constexpr int RSA = 256 / CA, RSB = 256 / CB;              // rows of a round of loads
+    static constexpr int RA = BT / RSA, RB = BT / RSB, NL = RA + RB;  // rounds
+    static constexpr int A_BYTES = BT * RBA, STAGE = A_BYTES + BT * RBB;
+    static constexpr int PITCH = WT + 1, EPI = 4 * WT * PITCH * 4;
+    static constexpr int LDS = NS * STAGE > EPI ? NS * STAGE : EPI;
+    static_assert(LDS <= 160 * 1024 && NS >= 2 && (NS - 2) * NL < 64, "ring");
+
+    template <int CHUNKS>
+    static __device__ __forceinline__ int swz(int row) {
+        return CHUNKS == 4 ? ((row >> 1) & 3) ^ ((row >> 3) & 1) : (row & 7) ^ ((row >> 3) & 1);
+    }
+    // chunk of step s (16 of K), half q of the lanes, part l
+    template <int PARTS>
+    static __device__ __forceinline__ int chunk(int s, int q, int l) {
+        return PARTS == 1 ? 2 * s + q : 8 * (s / 2) + 4 * l + 2 * (s % 2) + q;
+    }
+};
+
+// 8 columns of a two-part row from column c0 (a multiple of 8) on.
+__device__ __forceinline__ int64_t ns_column(int c0) { return (int64_t)(c0 / 32) * 64 + c0 % 32; }
+
+// 8 words h | l << 16 into the row.
+__device__ __forceinline__ void ns_store8(uint16_t *row, int c0, const uint32_t (&u)[8]) {
+    ns_u32x4 h, l;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        h[d] = __builtin_amdgcn_perm(u[2 * d + 1], u[2 * d], 0x05040100u);
+        l[d] = __builtin_amdgcn_perm(u[2 * d + 1], u[2 * d], 0x07060302u);
+    }
+    ns_u32x4 *to = reinterpret_cast<ns_u32x4 *>(row + ns_column(c0));
+    to[0] = h;
+    to[4] = l;
+}
+
+template <typename T, int MODE, int PA, int PB, int WT, int KS, int NS>
+__global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz q, int batch0) {
+    typedef NsTile<PA, PB, WT, KS, NS> S;
+    constexpr bool SYM = MODE == NS_SYM || MODE == NS_POLY;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[S::LDS];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    constexpr bool SYM = MODE == NS_GRAM || MODE == NS_POLY;
+    // consecutive workgroups go to the 8 XCDs in turn, each with its own L2: give
+    // every XCD a contiguous range of (matrix, product, tile)
+    int bid = blockIdx.x;
+    {
+        const int n = gridDim.x, xcd = bid % 8, base = n / 8, rem = n % 8;
+        bid = xcd * base + (xcd < rem ? xcd : rem) + bid / 8;
+    }
+    const int t = bid % p.tiles, jz = bid / p.tiles;
+    const int jn = jz % p.jobs;
+    const int64_t z = jz / p.jobs;
+    const NsJob &job = p.job[jn];
     int tm, tn;
     if (SYM) {   // lower triangle: tile t is (tm, tn), tn <= tm
-        tm = (int)((sqrtf(8.f * blockIdx.x + 1.f) - 1.f) * 0.5f);
-        while ((tm + 1) * (tm + 2) / 2 <= (int)blockIdx.x)
+        tm = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
+        while ((tm + 1) * (tm + 2) / 2 <= t)
             ++tm;
-        while (tm * (tm + 1) / 2 > (int)blockIdx.x)
+        while (tm * (tm + 1) / 2 > t)
             --tm;
-        tn = blockIdx.x - tm * (tm + 1) / 2;
+        tn = t - tm * (tm + 1) / 2;
     } else {
-        tm = blockIdx.x % tiles_m;
-        tn = blockIdx.x / tiles_m;
+        tm = t % p.tiles_m;
+        tn = t / p.tiles_m;
     }
-    const int row0 = tm * BT, col0 = tn * BT;
-    const int64_t z = blockIdx.z;
-    auto swz = [](int row) { return ((row >> 1) & 3) ^ ((row >> 3) & 1); };
+    const int row0 = tm * S::BT, col0 = tn * S::BT;
 
-    const int r0 = tid / CPR, cg = (tid % CPR) ^ swz(r0);
-    const uint8_t *base[4] = {(const uint8_t *)(p.a.h + z * p.a.stride), (const uint8_t *)(p.a.l + z * p.a.stride),
-                              (const uint8_t *)(p.b.h + z * p.b.stride), (const uint8_t *)(p.b.l + z * p.b.stride)};
-    int64_t off[4];   // rows row0 + r0 (+ 64), col0 + r0 (+ 64)
+    // (rows past the padding repeat the last: not stored)
+    const uint8_t *srca[S::RA], *srcb[S::RB];
+    {
+        const int ra = tid / S::CA, ca = (tid % S::CA) ^ S::template swz<S::CA>(ra);
+        const int rb = tid / S::CB, cb = (tid % S::CB) ^ S::template swz<S::CB>(rb);
+        const uint16_t *pa = job.a.p + z * job.a.stride, *pb = job.b.p + z * job.b.stride;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool isa = i < 2;
-        int r = (isa ? row0 : col0) + r0 + (i & 1) * RS;
-        r = min(r, (isa ? p.M : p.N) - 1);   // (rows past the padding repeat: not stored)
-        off[i] = (int64_t)r * (isa ? p.a.ld : p.b.ld) * 2 + cg * 16;
+        for (int i = 0; i < S::RA; ++i)
+            srca[i] = reinterpret_cast<const uint8_t *>(pa + (int64_t)min(row0 + ra + i * S::RSA, p.M - 1) * job.a.ld) + ca * 16;
+#pragma unroll
+        for (int i = 0; i < S::RB; ++i)
+            srcb[i] = reinterpret_cast<const uint8_t *>(pb + (int64_t)min(col0 + rb + i * S::RSB, p.N - 1) * job.b.ld) + cb * 16;
     }
-    const int KT = p.K / 32;
+    const int KT = p.K / KS;
+    // (every call issues NL loads: stages past the last re-read it)
     auto dma = [&](int e) {
         const int kt = min(e, KT - 1);
+        uint8_t *st = smem + (e % NS) * S::STAGE;
 #pragma unroll
-        for (int part = 0; part < 4; ++part)
+        for (int i = 0; i < S::RA; ++i)
+            dma16(srca[i] + (int64_t)kt * S::RBA, st + (wave * (64 / S::CA) + i * S::RSA) * S::RBA);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                dma16(base[part] + off[(part >> 1) * 2 + i] + (int64_t)kt * BKB,
-                      smem + (e & 1) * STAGE + part * PART + (wave * 16 + i * RS) * BKB);
+        for (int i = 0; i < S::RB; ++i)
+            dma16(srcb[i] + (int64_t)kt * S::RBB, st + S::A_BYTES + (wave * (64 / S::CB) + i * S::RSB) * S::RBB);
     };
 
-    const int wm0 = (wave >> 1) * 64, wn0 = (wave & 1) * 64;
-    ns_f32x16 acc[2][2];
+    const int wm0 = (wave >> 1) * WT, wn0 = (wave & 1) * WT;
+    ns_f32x16 acc[S::TB][S::TB];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < S::TB; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < S::TB; ++j)
             acc[i][j] = ns_f32x16{};
-    dma(0);
+    typedef ns_i32x4 Frags[PA + PB][S::TB];   // h and l of A, of B
+    auto read = [&](int e, int s, Frags &f) {
+        const uint8_t *st = smem + (e % NS) * S::STAGE;
+#pragma unroll
+        for (int k = 0; k < S::TB; ++k) {
+            const int ra = wm0 + k * 32 + (lane & 31), rb = wn0 + k * 32 + (lane & 31);
+#pragma unroll
+            for (int l = 0; l < PA; ++l)
+                f[l][k] = *reinterpret_cast<const ns_i32x4 *>(
+                    st + ra * S::RBA + ((S::template chunk<PA>(s, lane >> 5, l) ^ S::template swz<S::CA>(ra)) * 16));
+#pragma unroll
+            for (int l = 0; l < PB; ++l)
+                f[PA + l][k] = *reinterpret_cast<const ns_i32x4 *>(
+                    st + S::A_BYTES + rb * S::RBB + ((S::template chunk<PB>(s, lane >> 5, l) ^ S::template swz<S::CB>(rb)) * 16));
+        }
+    };
+    // products lo ... hi - 1 of a step: l h, h l, h h of each block
+    constexpr int BLOCKS = S::TB * S::TB, TERMS = PA + PB - 1, NMF = BLOCKS * TERMS;
+    auto mfmas = [&](const Frags &f, int lo, int hi) {
+#pragma unroll
+        for (int n = lo; n < hi; ++n) {
+            const int term = n / BLOCKS, i = n % BLOCKS / S::TB, j = n % S::TB;
+            const bool last = term == TERMS - 1;
+            const int x = !last && PA == 2 && term == 0 ? 1 : 0, y = !last && x == 0 ? PA + 1 : PA;
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(ns_f16x8, f[x][i]),
+                                                               __builtin_bit_cast(ns_f16x8, f[y][j]), acc[i][j], 0, 0, 0);
+        }
+    };
+
+    Frags f[2];
+#pragma unroll
+    for (int e = 0; e < NS - 1; ++e)
+        dma(e);
+    wait_vm_lds<(NS - 2) * S::NL>();
+    lds_barrier();
+    read(0, 0, f[0]);
+    // Stage e: the loads of stage e + NS - 1 go into the slot that stage e - 1 has
+    // left; each step's fragments are read during the step before; after the first
+    // products of the last step the barrier publishes stage e + 1, whose first
+    // fragments are read under the rest.
+    constexpr int SUB = KS / 16, KA = NMF >= 4 ? NMF / 4 : 1;
     for (int e = 0; e < KT; ++e) {
-        // this wavefront's loads of stage e have landed; the barrier makes them
-        // everybody's, and says that stage e - 1 has been read
-        wait_vm_lds<0>();
+        __builtin_amdgcn_sched_barrier(0);
+        dma(e + NS - 1);
+#pragma unroll
+        for (int s = 0; s < SUB - 1; ++s) {
+            read(e, s + 1, f[(s + 1) & 1]);
+            mfmas(f[s & 1], 0, NMF);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        mfmas(f[(SUB - 1) & 1], 0, KA);
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vm_lds<(NS - 2) * S::NL>();
         lds_barrier();
-        dma(e + 1);
-        const uint8_t *S = smem + (e & 1) * STAGE;
+        __builtin_amdgcn_sched_barrier(0);
+        read(e + 1, 0, f[0]);
+        mfmas(f[(SUB - 1) & 1], KA, NMF);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // Epilogue through LDS, a WT x WT block per wavefront: rows first (8 columns per
+    // lane, stored along rows), then columns (stored into the transpose).
+    constexpr int LPR = WT / 8, RPP = 64 / LPR, PASSES = WT / RPP;   // lanes per row, rows per pass
+    const int rb = row0 + wm0, cb = col0 + wn0;
+    const bool inside = rb < p.M && cb < p.N;   // (whole blocks: the padding is a multiple of WT)
+    const int lr = lane / LPR, lc = lane % LPR;
+    const float *fac = p.factors + z * p.fstride;
+    const float kp = fac[job.factor];
+    const float kadd = MODE == NS_POLY ? fac[NS_Q_ADD] : 0.f, kone = MODE == NS_POLY ? fac[NS_Q_ONE] : 0.f;
+    // (all of `add` on its way before the accumulators go through LDS)
+    constexpr int ADDS = MODE == NS_POLY ? PASSES : 1;
+    ns_u32x4 ah[ADDS], al[ADDS];
+    if constexpr (MODE == NS_POLY) {
+        if (inside) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int c = 2 * s + (lane >> 5);
-            ns_i32x4 f[4][2];
-#pragma unroll
-            for (int part = 0; part < 4; ++part)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = (part < 2 ? wm0 : wn0) + i * 32 + (lane & 31);
-                    f[part][i] = *reinterpret_cast<const ns_i32x4 *>(S + part * PART + r * BKB + ((c ^ swz(r)) * 16));
-                }
-            auto mf = [&](int x, int y) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            __builtin_bit_cast(ns_bf16x8, f[x][i]), __builtin_bit_cast(ns_bf16x8, f[y][j]),
-                            acc[i][j], 0, 0, 0);
-            };
-            mf(1, 2);
-            mf(0, 3);
-            mf(0, 2);
+            for (int i = 0; i < PASSES; ++i) {
+                const ns_u32x4 *from = reinterpret_cast<const ns_u32x4 *>(
+                    job.add.p + z * job.add.stride + (int64_t)(rb + i * RPP + lr) * job.add.ld + ns_column(cb + lc * 8));
+                ah[i] = from[0];
+                al[i] = from[4];
+            }
         }
     }
+    // (the ring's last loads have landed and every wavefront is past its last read)
     wait_vm_lds<0>();
     __syncthreads();
-
-    // Epilogue through LDS, a 64 x 64 block per wavefront: rows first (old
-    // values added, stored along rows), then columns (stored into the transpose).
-    uint32_t *w = reinterpret_cast<uint32_t *>(smem) + wave * 64 * PITCH;
+    if (!inside)
+        return;
+    uint32_t *w = reinterpret_cast<uint32_t *>(smem) + wave * WT * S::PITCH;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < S::TB; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < S::TB; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                w[(i * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4) * PITCH + j * 32 + (lane & 31)] =
+                w[(i * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4) * S::PITCH + j * 32 + (lane & 31)] =
                     __float_as_uint(acc[i][j][r]);
     wave_lds_fence();
-    const int rb = row0 + wm0, cb = col0 + wn0;
-    if (rb >= p.M || cb >= p.N)   // (whole 64 x 64 blocks: the padding's granularity)
-        return;
-    float kx = p.ka, kp = p.kc;
-    if (p.inv) {
-        const float s = p.inv[z];
-        if (MODE == NS_GRAM) {
-            kp = s;   // applied twice below: s * s may leave the range of fp32
-        } else {
-            kx *= s;
-            kp *= s;
-        }
-    }
-    const int lr = lane >> 4, lc = lane & 15;
-#pragma unroll 4
-    for (int i = 0; i < 16; ++i) {
-        const int rl = i * 4 + lr;
-        uint32_t *src = w + rl * PITCH + lc * 4;
-        float v[4];
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
-            v[d] = __uint_as_float(src[d]) * kp;
-        if (MODE == NS_GRAM && p.inv) {
+    for (int i = 0; i < PASSES; ++i) {
+        const int rl = i * RPP + lr;
+        uint32_t *from = w + rl * S::PITCH + lc * 8;
+        float v[8];
 #pragma unroll
-            for (int d = 0; d < 4; ++d)
-                v[d] *= kp;
-        }
-        const int row = rb + rl, col = cb + lc * 4;
-        if constexpr (MODE != NS_GRAM) {
-            const int64_t o = z * p.add.stride + (int64_t)row * p.add.ld + col;
-            const ns_u32x2 h = *reinterpret_cast<const ns_u32x2 *>(p.add.h + o);
-            const ns_u32x2 l = *reinterpret_cast<const ns_u32x2 *>(p.add.l + o);
+        for (int d = 0; d < 8; ++d)
+            v[d] = __uint_as_float(from[d]) * kp;
+        const int row = rb + rl, col = cb + lc * 8;
+        if constexpr (MODE == NS_POLY) {
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                const uint32_t hh = (h[d / 2] >> (16 * (d & 1))) & 0xFFFF, ll = (l[d / 2] >> (16 * (d & 1))) & 0xFFFF;
-                v[d] = __builtin_fmaf(kx, ns_f32(hh) + ns_f32(ll), v[d]);
+            for (int d = 0; d < 8; ++d) {
+                const uint32_t hh = (ah[i][d / 2] >> (16 * (d & 1))) & 0xFFFF, ll = (al[i][d / 2] >> (16 * (d & 1))) & 0xFFFF;
+                v[d] = __builtin_fmaf(kadd, ns_f32(hh) + ns_f32(ll), v[d]) + (row == col + d ? kone : 0.f);
             }
         }
-        if constexpr (MODE == NS_LAST) {
-#pragma unroll
-            for (int d = 0; d < 4; ++d)
-                src[d] = __float_as_uint(v[d]);
-            if (q.M <= q.N && row < q.M) {
-                T *Y = (T *)q.y + (batch0 + z) * q.stridey + (int64_t)row * q.ldy;
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    if (col + d < q.N)
-                        Y[col + d] = (T)v[d];
-            }
-        } else {
-            uint32_t t[4];
-#pragma unroll
-            for (int d = 0; d < 4; ++d)
-                src[d] = t[d] = ns_split(v[d]);
-            const int64_t o = z * p.out.stride + (int64_t)row * p.out.ld + col;
-            *reinterpret_cast<ns_u32x2 *>(p.out.h + o) =
-                ns_u32x2{(t[0] & 0xFFFF) | (t[1] << 16), (t[2] & 0xFFFF) | (t[3] << 16)};
-            *reinterpret_cast<ns_u32x2 *>(p.out.l + o) =
-                ns_u32x2{(t[0] >> 16) | (t[1] & 0xFFFF0000u), (t[2] >> 16) | (t[3] & 0xFFFF0000u)};
-        }
-    }
-    if (SYM && tm == tn)
-        return;   // the wavefronts of a diagonal tile store all of it along rows
-    if (MODE == NS_LAST && q.M <= q.N)
-        return;
-    wave_lds_fence();
-#pragma unroll 4
-    for (int i = 0; i < 16; ++i) {
-        const int cl = i * 4 + lr;
-        uint32_t t[4];
-#pragma unroll
-        for (int d = 0; d < 4; ++d)
-            t[d] = w[(lc * 4 + d) * PITCH + cl];
-        const int row = cb + cl, col = rb + lc * 4;   // of the transpose
-        if constexpr (MODE == NS_LAST) {
+        if constexpr (MODE == NS_OUT) {
+            // Y's rows are the product's: X's, or with M > N the rows of X^T
             if (row < q.M) {
-                T *Y = (T *)q.y + (batch0 + z) * q.stridey + (int64_t)row * q.ldy;
+                T *Y = (T *)q.y + (batch0 + z) * q.stridey + (int64_t)row * q.ldy + col;
+                T o[8];
 #pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    if (col + d < q.N)
-                        Y[col + d] = (T)__uint_as_float(t[d]);
+                for (int d = 0; d < 8; ++d)
+                    o[d] = (T)v[d];
+                if (col + 8 <= q.N && (reinterpret_cast<uintptr_t>(Y) & 15) == 0) {
+                    ns_u32x4 u;
+                    __builtin_memcpy(&u, o, 16);
+                    *reinterpret_cast<ns_u32x4 *>(Y) = u;
+                } else {
+#pragma unroll
+                    for (int d = 0; d < 8; ++d)
+                        if (col + d < q.N)
+                            Y[d] = o[d];
+                }
             }
         } else {
-            const int64_t o = z * p.outt.stride + (int64_t)row * p.outt.ld + col;
-            *reinterpret_cast<ns_u32x2 *>(p.outt.h + o) =
-                ns_u32x2{(t[0] & 0xFFFF) | (t[1] << 16), (t[2] & 0xFFFF) | (t[3] << 16)};
-            *reinterpret_cast<ns_u32x2 *>(p.outt.l + o) =
-                ns_u32x2{(t[0] >> 16) | (t[1] & 0xFFFF0000u), (t[2] >> 16) | (t[3] & 0xFFFF0000u)};
+            uint32_t u[8];
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+                from[d] = u[d] = ns_split(v[d]);
+            ns_store8(job.out.p + z * job.out.stride + (int64_t)row * job.out.ld, col, u);
         }
+    }
+    if (MODE == NS_OUT || (SYM && tm == tn))
+        return;   // (the wavefronts of a diagonal tile store all of it along rows)
+    wave_lds_fence();
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int cl = i * RPP + lr;
+        uint32_t u[8];
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+            u[d] = w[(lc * 8 + d) * S::PITCH + cl];
+        ns_store8(job.outt.p + z * job.outt.stride + (int64_t)(cb + cl) * job.outt.ld, rb + lc * 8, u);
     }
 }
+
+// ------------------------------------------------------------ host
 
 namespace {
 
@@ -337,6 +546,8 @@ struct NsPlan {
     int64_t tiles;
 };
 
+constexpr int kMaxSteps = 100;
+
 // Matrices are processed in chunks whose scratch stays below 4 GiB (one matrix
 // at least), which keeps the workspace of a long batch bounded.
 NsPlan ns_plan(int64_t batch, int64_t M, int64_t N) {
@@ -345,7 +556,7 @@ NsPlan ns_plan(int64_t batch, int64_t M, int64_t N) {
     pl.mp = (m + 63) / 64 * 64;
     pl.np = (n + 63) / 64 * 64;
     pl.tiles = (pl.mp / 64) * (pl.np / 64);
-    pl.per = 3 * pl.mp * pl.np * 4 + 2 * pl.mp * pl.mp * 4 + (pl.tiles + 1) * 4;
+    pl.per = 3 * pl.mp * pl.np * 4 + 5 * pl.mp * pl.mp * 4 + pl.tiles * 8 + 8 + kMaxSteps * NS_FACTORS * 4;
     const int64_t most = (int64_t)4 << 30;
     pl.chunk = most / pl.per;
     if (pl.chunk < 1)
@@ -353,6 +564,24 @@ NsPlan ns_plan(int64_t batch, int64_t M, int64_t N) {
     if (pl.chunk > batch)
         pl.chunk = batch;
     return pl;
+}
+
+// Steps between two A = X X^T. A's own rounding grows by a^2 a step in the
+// directions of small singular values, and reaches Q through b A. Against 64 bits
+// the result was off by up to 2^-23 a^(2 (L - 1)) of its norm after L steps (2.1e-3 for
+// L = 5, a = 3.4445 on rank 8 with noise of 1e-2 below it; 2e-4 on noise of the
+// signal's size). Kept below 1/8 of a half step of the output type: four steps for
+// bf16, three for fp16 with these coefficients, and five steps are three and two.
+int group_length(int type, float a) {
+    const double limit = type == MPGEMM_TYPE_F16 ? 0x1p-14 : 0x1p-11;
+    const double grow = (double)a * a > 1. ? (double)a * a : 1.;
+    double err = 0x1p-23;
+    int len = 1;
+    while (len < 8 && err * grow <= limit) {
+        err *= grow;
+        ++len;
+    }
+    return len;
 }
 
 }  // namespace
@@ -364,50 +593,150 @@ int64_t newton_schulz_bytes(int64_t batch, int64_t M, int64_t N) {
     return (pl.chunk * pl.per + 255) / 256 * 256;
 }
 
-template <typename T>
-static hipError_t ns_type(const NewtonSchulz &p, void *workspace, hipStream_t stream) {
+template <typename T, int MODE, int PA, int PB>
+static void ns_product(NsGemm g, const NewtonSchulz &p, int z0, int cus, hipStream_t stream) {
+    constexpr bool sym = MODE == NS_SYM || MODE == NS_POLY;
+    auto count = [&](int bt) {
+        const int64_t tm = (g.M + bt - 1) / bt, tn = (g.N + bt - 1) / bt;
+        return sym ? tm * (tm + 1) / 2 : tm * tn;
+    };
+    // 128 x 128 tiles load half the bytes per flop of 64 x 64 ones: taken where
+    // they are enough to give half of the CUs one.
+    const bool big = count(128) * g.jobs * g.nz * 2 >= cus;
+    const int bt = big ? 128 : 64;
+    g.tiles_m = (g.M + bt - 1) / bt;
+    g.tiles = (int)count(bt);
+    const dim3 grid((unsigned)((int64_t)g.tiles * g.jobs * g.nz));
+    constexpr int KS = PA + PB == 2 ? 64 : 32;
+    if (big && grid.x <= (unsigned)cus)
+        hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 64, KS, 4>), grid, dim3(256), 0, stream, g, p, z0);
+    else if (big)
+        hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 64, KS, 2>), grid, dim3(256), 0, stream, g, p, z0);
+    else
+        hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 32, KS, 4>), grid, dim3(256), 0, stream, g, p, z0);
+}
+
+template <typename T, bool VEC>
+static hipError_t ns_type(int type, const NewtonSchulz &p, void *workspace, hipStream_t stream) {
     const NsPlan pl = ns_plan(p.batch, p.M, p.N);
     const bool flip = p.M > p.N;
     const int mp = (int)pl.mp, np = (int)pl.np;
     const int64_t xs = pl.mp * pl.np, as = pl.mp * pl.mp;
     uint16_t *w = (uint16_t *)workspace;
-    auto mat = [&](int64_t ld, int64_t size) {
-        NsMat r = {w, w + pl.chunk * size, ld, size};
+    auto mat = [&](int64_t ld, int64_t size) {   // two parts
+        NsMat r = {w, 2 * ld, 2 * size};
         w += 2 * pl.chunk * size;
         return r;
     };
+    auto one = [](NsMat m) {   // one part in the same place
+        m.ld /= 2;
+        m.stride /= 2;
+        return m;
+    };
     const NsMat X = mat(np, xs);
-    NsMat XT[2];
-    XT[0] = mat(mp, xs);
-    XT[1] = mat(mp, xs);
-    const NsMat A = mat(mp, as), P = mat(mp, as);
-    float *sums = (float *)w, *inv = sums + pl.chunk * pl.tiles;
-    const int tm = (mp + 127) / 128, tn = (np + 127) / 128;
+    NsMat XT = mat(mp, xs), XT2 = mat(mp, xs);
+    const NsMat A = mat(mp, as), Tm = mat(mp, as);
+    NsMat Q = mat(mp, as), W = mat(mp, as), W2 = mat(mp, as);
+    double *sums = (double *)w;
+    float *head = (float *)(sums + pl.chunk * pl.tiles), *factors = head + 2 * pl.chunk;
+
+    const int most = group_length(type, p.a), groups = (p.steps + most - 1) / most;
+    NsGroups gr = {1, 0};
+    if (groups > 0) {
+        gr.len = p.steps / groups;
+        gr.longer = p.steps % groups;
+    }
 
     for (int64_t b0 = 0; b0 < p.batch; b0 += pl.chunk) {
-        const unsigned nz = (unsigned)(p.batch - b0 < pl.chunk ? p.batch - b0 : pl.chunk);
+        const int nz = (int)(p.batch - b0 < pl.chunk ? p.batch - b0 : pl.chunk);
         const int z0 = (int)b0;
-        if (flip)
-            hipLaunchKernelGGL((ns_load_kernel<T, true>), dim3(mp / 64, np / 64, nz), dim3(256), 0, stream, p, z0, X, XT[0], sums);
-        else
-            hipLaunchKernelGGL((ns_load_kernel<T, false>), dim3(np / 64, mp / 64, nz), dim3(256), 0, stream, p, z0, X, XT[0], sums);
-        hipLaunchKernelGGL(ns_norm_kernel, dim3(nz), dim3(256), 0, stream, sums, (int)pl.tiles, p.eps, inv);
+        hipLaunchKernelGGL((ns_square_kernel<T, VEC>), dim3((p.N + 63) / 64, (p.M + 63) / 64, nz), dim3(256), 0, stream, p, z0, sums);
+        hipLaunchKernelGGL(ns_norm_kernel, dim3(nz), dim3(256), 0, stream, sums, (int)pl.tiles, p, gr, head, factors);
         if (p.steps == 0) {
             const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
-            hipLaunchKernelGGL((ns_scale_kernel<T>), dim3((unsigned)(blocks < 4096 ? blocks : 4096), 1, nz), dim3(256), 0, stream, p, z0, inv);
+            hipLaunchKernelGGL((ns_scale_kernel<T>), dim3((unsigned)(blocks < 4096 ? blocks : 4096), 1, nz), dim3(256), 0, stream, p, z0, head);
+        } else if (flip) {
+            hipLaunchKernelGGL((ns_load_kernel<T, true, VEC>), dim3(mp / 64, np / 64, nz), dim3(256), 0, stream, p, z0, head, one(X), one(XT));
+        } else {
+            hipLaunchKernelGGL((ns_load_kernel<T, false, VEC>), dim3(np / 64, mp / 64, nz), dim3(256), 0, stream, p, z0, head, one(X), one(XT));
         }
         for (int s = 0; s < p.steps; ++s) {
-            const float *sc = s == 0 ? inv : nullptr;
-            const NsMat &xt = XT[s & 1], &xt2 = XT[(s + 1) & 1];
-            NsGemm g = {X, X, mp, mp, np, X, A, A, 0.f, 1.f, sc};
-            hipLaunchKernelGGL((ns_gemm_kernel<T, NS_GRAM>), dim3(tm * (tm + 1) / 2, 1, nz), dim3(256), 0, stream, g, p, z0, tm, tm);
-            g = {A, A, mp, mp, mp, A, P, P, p.b, p.c, nullptr};
-            hipLaunchKernelGGL((ns_gemm_kernel<T, NS_POLY>), dim3(tm * (tm + 1) / 2, 1, nz), dim3(256), 0, stream, g, p, z0, tm, tm);
-            g = {P, xt, mp, np, mp, X, X, xt2, p.a, 1.f, sc};
-            if (s + 1 < p.steps)
-                hipLaunchKernelGGL((ns_gemm_kernel<T, NS_STEP>), dim3(tm * tn, 1, nz), dim3(256), 0, stream, g, p, z0, tm, tn);
-            else
-                hipLaunchKernelGGL((ns_gemm_kernel<T, NS_LAST>), dim3(tm * tn, 1, nz), dim3(256), 0, stream, g, p, z0, tm, tn);
+            const bool first = gr.starts(s), last = s + 1 == p.steps, ends = last || gr.starts(s + 1);
+            NsGemm g = {};
+            g.jobs = 1;
+            g.nz = nz;
+            g.M = g.N = mp;
+            g.factors = factors + (int64_t)s * NS_FACTORS;
+            g.fstride = (int64_t)p.steps * NS_FACTORS;
+            if (first) {   // A = X X^T
+                g.K = np;
+                g.job[0] = {X, X, A, A, A, NS_GRAM};
+                if (s == 0) {
+                    g.job[0].a = g.job[0].b = one(X);
+                    ns_product<T, NS_SYM, 1, 1>(g, p, z0, p.cus, stream);
+                } else {
+                    ns_product<T, NS_SYM, 2, 2>(g, p, z0, p.cus, stream);
+                }
+            }
+            g.K = mp;
+            g.job[0] = {A, A, A, Q, Q, NS_Q_ACC};
+            ns_product<T, NS_POLY, 2, 2>(g, p, z0, p.cus, stream);
+            // T = Q A and W <- Q W, side by side (the first W is Q itself, the last T is not needed)
+            g.jobs = 0;
+            if (!ends)
+                g.job[g.jobs++] = {Q, A, A, Tm, Tm, NS_T};
+            if (!first)
+                g.job[g.jobs++] = {Q, W, W, W2, W2, NS_W};
+            if (g.jobs)
+                ns_product<T, NS_SYM, 2, 2>(g, p, z0, p.cus, stream);
+            if (!ends) {   // A <- Q T
+                g.jobs = 1;
+                g.job[0] = {Q, Tm, A, A, A, NS_A};
+                ns_product<T, NS_SYM, 2, 2>(g, p, z0, p.cus, stream);
+            }
+            if (first) {
+                const NsMat t = Q;
+                Q = W;
+                W = t;
+            } else {
+                const NsMat t = W;
+                W = W2;
+                W2 = t;
+            }
+            if (!ends)
+                continue;
+            // X <- W X; X^T is the operand whose rows run along the contracted axis
+            g.jobs = 1;
+            const bool exact = s + 1 <= gr.len + (gr.longer > 0);   // G's own X: one part
+            const NsMat xt = exact ? one(XT) : XT;
+            if (last && !flip) {
+                g.M = mp;
+                g.N = np;
+                g.job[0] = {W, xt, W, X, X, NS_APPLY};
+                if (exact)
+                    ns_product<T, NS_OUT, 2, 1>(g, p, z0, p.cus, stream);
+                else
+                    ns_product<T, NS_OUT, 2, 2>(g, p, z0, p.cus, stream);
+            } else if (last) {
+                g.M = np;
+                g.N = mp;
+                g.job[0] = {xt, W, W, X, X, NS_APPLY};
+                if (exact)
+                    ns_product<T, NS_OUT, 1, 2>(g, p, z0, p.cus, stream);
+                else
+                    ns_product<T, NS_OUT, 2, 2>(g, p, z0, p.cus, stream);
+            } else {
+                g.M = mp;
+                g.N = np;
+                g.job[0] = {W, xt, W, X, XT2, NS_APPLY};
+                if (exact)
+                    ns_product<T, NS_X, 2, 1>(g, p, z0, p.cus, stream);
+                else
+                    ns_product<T, NS_X, 2, 2>(g, p, z0, p.cus, stream);
+                const NsMat t = XT;
+                XT = XT2;
+                XT2 = t;
+            }
         }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
@@ -417,7 +746,11 @@ static hipError_t ns_type(const NewtonSchulz &p, void *workspace, hipStream_t st
 }
 
 hipError_t launch_newton_schulz(int type, const NewtonSchulz &p, void *workspace, hipStream_t stream) {
-    return type == MPGEMM_TYPE_F16 ? ns_type<_Float16>(p, workspace, stream) : ns_type<__bf16>(p, workspace, stream);
+    // (both types have 2 bytes)
+    const bool vec = (reinterpret_cast<uintptr_t>(p.g) & 15) == 0 && p.ldg % 8 == 0 && p.strideg % 8 == 0;
+    if (type == MPGEMM_TYPE_F16)
+        return vec ? ns_type<_Float16, true>(type, p, workspace, stream) : ns_type<_Float16, false>(type, p, workspace, stream);
+    return vec ? ns_type<__bf16, true>(type, p, workspace, stream) : ns_type<__bf16, false>(type, p, workspace, stream);
 }
 
 }  // namespace mpg
