@@ -7,9 +7,8 @@
 //   A = X X^T;   per step: Q = a I + b A + c A A,  T = Q A,  A <- Q T,  W <- Q W;   X <- W X.
 // Per step that is four symmetric m x m products (the tiles on and below the
 // diagonal, the others mirrored), 4 m^3 flop, against m^2 n + m^3 + 2 m^2 n for
-// forming A and Q X anew: the same for a square matrix, less than a third at n = 4 m
-// (8192 x 2048: 2264 -> 893 us together with the single-part X below). What it
-// costs is accuracy: an error of A in the direction of a small singular value
+// forming A and Q X anew: the same for a square matrix, less than a third at n = 4 m.
+// What it costs is accuracy: an error of A in the direction of a small singular value
 // grows by about a^2 per step, as that eigenvalue of A does, and A has to be formed
 // anew from X once it is no longer small; see group_length.
 //
@@ -124,8 +123,7 @@ __device__ __forceinline__ int ns_exponent(float bound) {
 __global__ __launch_bounds__(256) void ns_norm_kernel(const double *sums, int tiles, NewtonSchulz p, NsGroups gr,
                                                       float *head, float *factors) {
     __shared__ double red[4];
-    __shared__ float top[4][5];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
     double s = 0.;
     for (int i = tid; i < tiles; i += 256)
         s += sums[(int64_t)blockIdx.x * tiles + i];
@@ -133,64 +131,58 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(const double *sums, int ti
     for (int o = 32; o > 0; o >>= 1)
         s += __shfl_xor(s, o);
     if (lane == 0)
-        red[wave] = s;
+        red[tid >> 6] = s;
     __syncthreads();
+    if (tid >= 64)
+        return;
     const double norm = sqrt((red[0] + red[1]) + (red[2] + red[3]));
     const double inv = 1. / (norm + (double)p.eps);
     const bool finite = norm < DBL_MAX;   // (false for NaN)
-    const int e0 = finite && norm > 0. ? 12 - ilogb(norm) : 0;
-    const float up = finite ? (float)ldexp(1., e0 < 126 ? e0 : 126) : __builtin_nanf("");
-    const int ex0 = e0 < 126 ? e0 : 126;
-    if (tid == 0) {
-        head[2 * blockIdx.x] = up;
-        head[2 * blockIdx.x + 1] = (float)(inv < FLT_MAX ? inv : inv > 0. && norm == 0. && p.eps > 0.f ? FLT_MAX : inv);
+    const int ex0 = finite && norm > 0. ? min(12 - ilogb(norm), 126) : 0;
+    if (lane == 0) {
+        head[2 * blockIdx.x] = finite ? (float)ldexp(1., ex0) : __builtin_nanf("");
+        // (finite where eps > 0, so that zeros stay zeros)
+        head[2 * blockIdx.x + 1] = (float)(p.eps > 0.f ? fmin(inv, (double)FLT_MAX) : inv);
     }
-    // The singular values x of X lie in [0, r]. Thread t looks at x = r t / 255:
-    // the largest |Q|, |T| = |x^2 Q| and next r = |x Q|.
-    float r = finite ? (float)fmin(norm * inv, 1.) : 1.f;
-    double to_x = inv * ldexp(1., -ex0);   // stored X -> X
+    // The singular values x of X lie in [0, r]. Lane t looks at four x of [0, r]: the
+    // largest |Q|, |T| = |x^2 Q| and next r = |x Q|. The factors are products of
+    // powers of two with exponents in the range of a double.
+    auto two = [](int e) { return ldexp(1., e); };
+    float r = finite ? (float)fmin(norm * inv, 1.) : 1.f, wb = 1.f;
+    double to_x = inv * two(-ex0);   // stored X -> X
     int ew = 0;
-    float wb = 1.f;
     for (int k = 0; k < p.steps; ++k) {
-        const float x = r * ((float)tid * (1.f / 255.f)), x2 = x * x;
-        const float q = fabsf(p.a + x2 * (p.b + x2 * p.c));
-        float v[3] = {q, q * x2, q * x};
+        float v[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x = r * ((float)(4 * lane + i) * (1.f / 255.f)), x2 = x * x;
+            const float q = fabsf(p.a + x2 * (p.b + x2 * p.c));
+            v[0] = fmaxf(v[0], q);
+            v[1] = fmaxf(v[1], q * x2);
+            v[2] = fmaxf(v[2], q * x);
+        }
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1)
 #pragma unroll
             for (int d = 0; d < 3; ++d)
                 v[d] = fmaxf(v[d], __shfl_xor(v[d], o));
-        __syncthreads();   // (the last step's values have been read)
-        if (lane == 0) {
-#pragma unroll
-            for (int d = 0; d < 3; ++d)
-                top[wave][d] = v[d];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int d = 0; d < 3; ++d)
-            v[d] = fmaxf(fmaxf(top[0][d], top[1][d]), fmaxf(top[2][d], top[3][d]));
-        // exponents of this step's matrices (every thread has the same)
+        // exponents of this step's matrices
         const int ea = ns_exponent(r * r), eq = ns_exponent(v[0]), et = ns_exponent(v[1]), ea2 = ns_exponent(v[2] * v[2]);
         const bool first = gr.starts(k), last = k + 1 == p.steps || gr.starts(k + 1);
         wb = first ? v[0] : wb * v[0];
         const int ew2 = first ? eq : ns_exponent(wb);
         const int ex = k + 1 < p.steps ? ns_exponent(v[2]) : 0;
-        if (tid == 0) {
-            float *f = factors + ((int64_t)blockIdx.x * p.steps + k) * NS_FACTORS;
-            auto two = [](int e) { return ldexp(1., e); };
-            f[NS_Q_ACC] = (float)(p.c * two(eq - 2 * ea));
-            f[NS_Q_ADD] = (float)(p.b * two(eq - ea));
-            f[NS_Q_ONE] = (float)(p.a * two(eq));
-            f[NS_T] = (float)two(et - eq - ea);
-            f[NS_A] = (float)two(ea2 - eq - et);
-            f[NS_W] = (float)two(ew2 - eq - ew);
-            f[NS_GRAM] = (float)(to_x * to_x * two(ea));
-            f[NS_APPLY] = (float)(to_x * two(ex - ew2));
+        if (lane < NS_FACTORS) {
+            const double base = lane == NS_Q_ACC ? (double)p.c : lane == NS_Q_ADD ? (double)p.b : lane == NS_Q_ONE ? (double)p.a
+                                : lane == NS_GRAM ? to_x * to_x : lane == NS_APPLY ? to_x : 1.;
+            const int e = lane == NS_Q_ACC ? eq - 2 * ea : lane == NS_Q_ADD ? eq - ea : lane == NS_Q_ONE ? eq
+                          : lane == NS_T ? et - eq - ea : lane == NS_A ? ea2 - eq - et : lane == NS_W ? ew2 - eq - ew
+                          : lane == NS_GRAM ? ea : ex - ew2;
+            factors[((int64_t)blockIdx.x * p.steps + k) * NS_FACTORS + lane] = (float)(base * two(e));
         }
         ew = ew2;
         if (last)
-            to_x = ldexp(1., -ex);
+            to_x = two(-ex);
         r = v[2];
     }
 }
@@ -600,9 +592,11 @@ static void ns_product(NsGemm g, const NewtonSchulz &p, int z0, int cus, hipStre
         const int64_t tm = (g.M + bt - 1) / bt, tn = (g.N + bt - 1) / bt;
         return sym ? tm * (tm + 1) / 2 : tm * tn;
     };
-    // 128 x 128 tiles load half the bytes per flop of 64 x 64 ones: taken where
-    // they are enough to give half of the CUs one.
-    const bool big = count(128) * g.jobs * g.nz * 2 >= cus;
+    // 128 x 128 tiles load half the bytes per flop of 64 x 64 ones, which finish
+    // sooner where there are few: on 136 CUs (2048 x 2048, symmetric) 39 us against 38
+    // at K = 2048, 128 against 141 at K = 8192; on 192 CUs (12 x 512 x 512) 19 against 16.
+    const int64_t want = sym ? cus / 2 : cus;
+    const bool big = count(128) * g.jobs * g.nz >= want;
     const int bt = big ? 128 : 64;
     g.tiles_m = (g.M + bt - 1) / bt;
     g.tiles = (int)count(bt);
@@ -613,7 +607,7 @@ static void ns_product(NsGemm g, const NewtonSchulz &p, int z0, int cus, hipStre
     else if (big)
         hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 64, KS, 2>), grid, dim3(256), 0, stream, g, p, z0);
     else
-        hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 32, KS, 4>), grid, dim3(256), 0, stream, g, p, z0);
+        hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 32, KS, 3>), grid, dim3(256), 0, stream, g, p, z0);
 }
 
 template <typename T, bool VEC>
@@ -640,7 +634,10 @@ static hipError_t ns_type(int type, const NewtonSchulz &p, void *workspace, hipS
     double *sums = (double *)w;
     float *head = (float *)(sums + pl.chunk * pl.tiles), *factors = head + 2 * pl.chunk;
 
-    const int most = group_length(type, p.a), groups = (p.steps + most - 1) / most;
+    // Per step and m^3 flop: L steps in a group cost (3 n / m + 4 L - 3) / L products. For a
+    // square matrix that is 4 whatever L is, and single steps need fewer launches
+    // (12 x 512 x 512: 199 against 248 us).
+    const int most = pl.np * 4 >= pl.mp * 5 ? group_length(type, p.a) : 1, groups = (p.steps + most - 1) / most;
     NsGroups gr = {1, 0};
     if (groups > 0) {
         gr.len = p.steps / groups;
