@@ -80,15 +80,20 @@ __device__ __forceinline__ float mx_bias(const void *bias, int n) {
 //
 // Scales: 16 bytes per row, two stages' worth, in a two-slot ring of their
 // own; each lane reads the word of its row, stage and half once per stage.
+//
+// The main loop runs over pairs of stages and has no branch: with one (for the
+// scales of every other stage, or for the last stage's partial rows) the compiler
+// moved all of a stage's 64 matrix instructions past it, behind the wait for the next
+// stage.
 template <int BM, int BN, int WGM, int WGN, int NS>
 struct MxTile {
     static constexpr int NW = WGM * WGN, NT = 64 * NW;
     static constexpr int WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32;
     static constexpr int BKB = 128, CPR = 8, RS = NT / CPR;
     static constexpr int A_PER_T = BM / RS, B_PER_T = BN / RS, NL = A_PER_T + B_PER_T;
-    static constexpr int STAGE = (BM + BN) * BKB, SCALES = (BM + BN) * 16;
-    static constexpr int LDS_BYTES = NS * STAGE + 2 * SCALES;
     static constexpr int SROUNDS = (BM + BN + NT - 1) / NT;
+    static constexpr int STAGE = (BM + BN) * BKB, SCALES = SROUNDS * NT * 16;   // (whole rounds)
+    static constexpr int LDS_BYTES = NS * STAGE + 2 * SCALES;
     static_assert(RS % 16 == 0 && BM % RS == 0 && BN % RS == 0 && (BM + BN) % 64 == 0 && BM % 64 == 0, "staging");
     static_assert(NS >= 2 && LDS_BYTES <= 160 * 1024 && (NS - 2) * NL < 64, "ring");
 
@@ -123,7 +128,9 @@ struct MxTile {
             acc[f / TN][f % TN] = mx_mfma32<S>(b[f % TN], a[f / TN], acc[f / TN][f % TN], sb[f % TN], sa[f / TN]);
     }
 
-    // Stages [e0, e1) of 8 blocks; only the last stage of a row may be partial.
+    // Stages [e0, e1) of 8 blocks, e0 even; only the last stage of a row may be
+    // partial. The sums start from the bias.
+    template <typename OUT>
     static __device__ __forceinline__ void mainloop(const MxGemm &p, uint8_t *smem, int row0, int col0, int e0,
                                                     int e1, int tid, int lane, int wave,
                                                     mx_f32x16 (&acc)[TM][TN]) {
@@ -134,7 +141,8 @@ struct MxTile {
         const uint8_t *SAb = p.sa + (int64_t)row0 * p.ldsa, *SBb = p.sb + (int64_t)col0 * p.ldsb;
         const int a_rows = p.M - row0, b_rows = p.N - col0;
         // (rows past the matrix repeat its last row: their outputs are not stored)
-        uint32_t off[NL], soff[SROUNDS];
+        uint32_t off[NL];
+        const uint8_t *ssrc[SROUNDS];
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             const bool isa = i < A_PER_T;
@@ -145,12 +153,12 @@ struct MxTile {
         }
 #pragma unroll
         for (int i = 0; i < SROUNDS; ++i) {
-            const int t = i * NT + tid;
+            const int t = min(i * NT + tid, BM + BN - 1);
             const bool isa = t < BM;
             const int rows = isa ? a_rows : b_rows;
             int r = isa ? t : t - BM;
             r = r < rows ? r : rows - 1;
-            soff[i] = (uint32_t)r * (uint32_t)(isa ? p.ldsa : p.ldsb);
+            ssrc[i] = (isa ? SAb : SBb) + (uint32_t)r * (uint32_t)(isa ? p.ldsa : p.ldsb);
         }
         const int wrow = wave * (64 / CPR);
         uint8_t *sc = smem + NS * STAGE;
@@ -163,8 +171,7 @@ struct MxTile {
             for (int i = 0; i < NL; ++i) {
                 const bool isa = i < A_PER_T;
                 const uint8_t *src = (isa ? Ab : Bb) + (int64_t)kt * BKB + off[i];
-                if (kt == last)
-                    src = in ? src : reinterpret_cast<const uint8_t *>(&kMxZeros);
+                src = in ? src : reinterpret_cast<const uint8_t *>(&kMxZeros);
                 dma16(src, smem + (e % NS) * STAGE + (isa ? 0 : BM * BKB) +
                                (wrow + (isa ? i : i - A_PER_T) * RS) * BKB);
             }
@@ -174,62 +181,59 @@ struct MxTile {
             const int qc = 2 * q <= last ? q : last / 2;
 #pragma unroll
             for (int i = 0; i < SROUNDS; ++i)
-                if ((i + 1) * NT <= BM + BN || i * NT + wave * 64 < BM + BN)
-                    dma16((i * NT + wave * 64 < BM ? SAb : SBb) + soff[i] + 16 * qc,
-                          sc + (q & 1) * SCALES + (i * NT + wave * 64) * 16);
+                dma16(ssrc[i] + 16 * qc, sc + (q & 1) * SCALES + (i * NT + wave * 64) * 16);
         };
         auto read_scales = [&](int e, int (&sa)[TM], int (&sb)[TN]) {
             const uint8_t *s = sc + ((e >> 1) & 1) * SCALES + 8 * (e & 1) + 4 * (lane >> 5);
+            // (the bytes of blocks past the row's end are cleared: a stray 255 would be NaN)
+            const int left = nb - 8 * min(e, last) - 4 * (lane >> 5);
+            const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
 #pragma unroll
             for (int i = 0; i < TM; ++i)
-                sa[i] = *reinterpret_cast<const int *>(s + (wm0 + i * 32 + (lane & 31)) * 16);
+                sa[i] = *reinterpret_cast<const int *>(s + (wm0 + i * 32 + (lane & 31)) * 16) & keep;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
-                sb[j] = *reinterpret_cast<const int *>(s + (BM + wn0 + j * 32 + (lane & 31)) * 16);
-            if (e >= last) {
-                const int blk = 8 * last + 4 * (lane >> 5);
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-                    sa[i] = mx_mask_scales(sa[i], blk, nb);
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    sb[j] = mx_mask_scales(sb[j], blk, nb);
-            }
+                sb[j] = *reinterpret_cast<const int *>(s + (BM + wn0 + j * 32 + (lane & 31)) * 16) & keep;
         };
 
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+        for (int j = 0; j < TN; ++j) {
+            mx_f32x16 b = {};
+            if (p.bias) {
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
-                acc[i][j] = mx_f32x16{};
+                for (int r = 0; r < 16; ++r) {
+                    const int n = col0 + wn0 + 32 * j + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
+                    b[r] = (float)((const OUT *)p.bias)[n < p.N ? n : p.N - 1];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                acc[i][j] = b;
+        }
 
         mx_i32x4 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
-        int sa[TM], sb[TN], na[TM], nbs[TN];
-        // Loads retire in order and the scales of a pair are issued ahead of
-        // its stages, so the wait that proves a stage has landed proves its
-        // scales too. (A slice may start at an odd stage: both pairs then.)
+        int sa0[TM], sb0[TN], sa1[TM], sb1[TN];
+        // Loads retire in order and the scales of a pair are issued ahead of its
+        // stages, so the wait that proves a stage has landed proves its scales too.
         dma_scales(e0 >> 1);
-        if (e0 & 1)
-            dma_scales((e0 >> 1) + 1);
 #pragma unroll
         for (int e = 0; e < NS - 1; ++e)
             dma_stage(e0 + e);
         wait_vm_lds<(NS - 2) * NL>();
         lds_barrier();
         read_frags<0>(smem + (e0 % NS) * STAGE, wm0, wn0, lane, fa0, fb0);
-        read_scales(e0, sa, sb);
+        read_scales(e0, sa0, sb0);
 
         // Stage e: the loads of stage e + NS - 1 go into the slot that stage
-        // e - 1 has left; each step's fragments are read during the step
-        // before; after the first quarter of the last step's products the
-        // barrier publishes stage e + 1, whose first fragments and scales are
-        // read under the rest.
+        // e - 1 has left (before an even stage the next pair's scales, into the slot
+        // of the pair before this one); each step's fragments are read during the step
+        // before; after the first quarter of the last step's products the barrier
+        // publishes stage e + 1, whose first fragments and scales are read under the rest.
         constexpr int NMF = TM * TN, KA = NMF >= 4 ? NMF / 4 : 1;
-        for (int e = e0; e < e1; ++e) {
+        auto stage = [&](int e, bool even, const int (&sa)[TM], const int (&sb)[TN], int (&na)[TM], int (&nb2)[TN]) {
             const uint8_t *S = smem + (e % NS) * STAGE;
             __builtin_amdgcn_sched_barrier(0);
-            // the next pair's scales, into the slot of the pair before this one
-            if ((e & 1) == 0)
+            if (even)
                 dma_scales((e >> 1) + 1);
             dma_stage(e + NS - 1);
             read_frags<1>(S, wm0, wn0, lane, fa1, fb1);
@@ -247,16 +251,17 @@ struct MxTile {
             lds_barrier();
             __builtin_amdgcn_sched_barrier(0);
             read_frags<0>(smem + ((e + 1) % NS) * STAGE, wm0, wn0, lane, fa0, fb0);
-            read_scales(e + 1, na, nbs);
+            read_scales(e + 1, na, nb2);
             mfmas<3, KA, NMF>(fa1, fb1, sa, sb, acc);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-                sa[i] = na[i];
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                sb[j] = nbs[j];
             __builtin_amdgcn_sched_barrier(0);
+        };
+        int e = e0;
+        for (; e + 1 < e1; e += 2) {
+            stage(e, true, sa0, sb0, sa1, sb1);
+            stage(e + 1, false, sa1, sb1, sa0, sb0);
         }
+        if (e < e1)
+            stage(e, true, sa0, sb0, sa1, sb1);
         wait_vm_lds<0>();
     }
 
@@ -286,10 +291,8 @@ struct MxTile {
                     const int cl = 32 * j + 8 * g + 4 * (lane >> 5);
                     out4 v;
 #pragma unroll
-                    for (int d = 0; d < 4; ++d) {
-                        const int n = col0 + wn0 + cl + d;
-                        v[d] = (OUT)(acc[i][j][4 * g + d] + mx_bias<OUT>(p.bias, n < p.N ? n : p.N - 1));
-                    }
+                    for (int d = 0; d < 4; ++d)
+                        v[d] = (OUT)acc[i][j][4 * g + d];
                     const int c = cl / EPC;
                     *reinterpret_cast<out4 *>(region + rl * RB + ((c ^ (rl & (CPW - 1))) * 16) +
                                               (cl % EPC) * (int)sizeof(OUT)) = v;
@@ -336,7 +339,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_tile_kernel(MxGemm p, int t
     const int stages = (p.nb + 7) / 8;
     const int e0 = blockIdx.y * slice, e1 = min(e0 + slice, stages);
     mx_f32x16 acc[MT::TM][MT::TN];
-    MT::mainloop(p, smem, tm * BM, tn * BN, e0, e1, tid, lane, wave, acc);
+    MT::template mainloop<OUT>(p, smem, tm * BM, tn * BN, e0, e1, tid, lane, wave, acc);
     if (gridDim.y > 1)
         p.c = (float *)p.c + (int64_t)blockIdx.y * p.M * p.ldc;
     MT::template epilogue<OUT>(p, smem, tm * BM, tn * BN, lane, wave, acc);
@@ -509,7 +512,7 @@ MxPlan plan_mx(int64_t M, int64_t N, int64_t nb, int cu_count) {
         if (ks > 16)
             ks = 16;
         if (ks > 1) {
-            pl.slice = (int)((stages + ks - 1) / ks);
+            pl.slice = (int)((stages + ks - 1) / ks + 1) / 2 * 2;   // (a slice starts at an even stage)
             pl.ks = (int)((stages + pl.slice - 1) / pl.slice);
             if (pl.ks > 1)
                 pl.partial_bytes = pl.ks * M * ((N + 3) / 4 * 4) * 4;
