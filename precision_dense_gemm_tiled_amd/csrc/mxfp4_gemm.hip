@@ -24,7 +24,6 @@ namespace mpg {
 typedef int mx_i32x4 __attribute__((ext_vector_type(4)));
 typedef int mx_i32x8 __attribute__((ext_vector_type(8)));
 typedef float mx_f32x4 __attribute__((ext_vector_type(4)));
-typedef float mx_f32x16 __attribute__((ext_vector_type(16)));
 
 // 16 bytes of zeros: the source of blocks past a row's end.
 __device__ const u32x4 kMxZeros = {0, 0, 0, 0};
@@ -32,10 +31,6 @@ __device__ const u32x4 kMxZeros = {0, 0, 0, 0};
 __device__ __forceinline__ mx_i32x8 mx_widen(mx_i32x4 v) { return mx_i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
 // One step with byte S of the scale words. The operand format 4 is e2m1.
-template <int S>
-__device__ __forceinline__ mx_f32x16 mx_mfma32(mx_i32x4 x, mx_i32x4 y, mx_f32x16 c, int sx, int sy) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_widen(x), mx_widen(y), c, 4, 4, S, sx, S, sy);
-}
 template <int S>
 __device__ __forceinline__ mx_f32x4 mx_mfma16(mx_i32x4 x, mx_i32x4 y, mx_f32x4 c, int sx, int sy) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_widen(x), mx_widen(y), c, 4, 4, S, sx, S, sy);
@@ -75,57 +70,55 @@ __device__ __forceinline__ float mx_bias(const void *bias, int n) {
 // BM x BN output tile, WGM x WGN wavefronts, stages of 8 blocks of K (128
 // bytes per row) in an NS-deep LDS ring filled with direct-to-LDS loads.
 // 16-byte chunk c of LDS row r sits at c ^ swz(r), which keeps the fragment
-// reads (one chunk column over 32 rows) free of bank conflicts. At step s of a
-// stage, lane half h reads chunk 4 h + s.
+// reads (one chunk column over 16 rows) free of bank conflicts. At step s (of two)
+// of a stage, lane quarter q reads chunk 2 q + s.
 //
 // Scales: 16 bytes per row, two stages' worth, in a two-slot ring of their
-// own; each lane reads the word of its row, stage and half once per stage.
+// own; each lane reads the two bytes of its row, stage and quarter once per stage.
+//
+// The 16 x 16 x 128 shape: with random codes a stream of independent matrix
+// instructions alone runs at 7.2 PFLOP/s in it and at 6.5 in 32 x 32 x 64 (9.4 and 9.2 on
+// zeros: the clock follows the power, and this shape moves half the sums per product).
 //
 // The main loop runs over pairs of stages and has no branch: with one (for the
 // scales of every other stage, or for the last stage's partial rows) the compiler
-// moved all of a stage's 64 matrix instructions past it, behind the wait for the next
+// moved all of a stage's matrix instructions past it, behind the wait for the next
 // stage.
 template <int BM, int BN, int WGM, int WGN, int NS>
 struct MxTile {
     static constexpr int NW = WGM * WGN, NT = 64 * NW;
-    static constexpr int WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32;
+    static constexpr int WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 16, TN = WTN / 16, HM = TM / 2, HN = TN / 2;
     static constexpr int BKB = 128, CPR = 8, RS = NT / CPR;
     static constexpr int A_PER_T = BM / RS, B_PER_T = BN / RS, NL = A_PER_T + B_PER_T;
     static constexpr int SROUNDS = (BM + BN + NT - 1) / NT;
     static constexpr int STAGE = (BM + BN) * BKB, SCALES = SROUNDS * NT * 16;   // (whole rounds)
     static constexpr int LDS_BYTES = NS * STAGE + 2 * SCALES;
     static_assert(RS % 16 == 0 && BM % RS == 0 && BN % RS == 0 && (BM + BN) % 64 == 0 && BM % 64 == 0, "staging");
+    static_assert(TM % 2 == 0 && TN % 2 == 0, "quadrants");
     static_assert(NS >= 2 && LDS_BYTES <= 160 * 1024 && (NS - 2) * NL < 64, "ring");
 
     static __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
-    template <int S>
-    static __device__ __forceinline__ void read_frags(const uint8_t *As, int wm0, int wn0, int lane,
-                                                      mx_i32x4 (&a)[TM], mx_i32x4 (&b)[TN]) {
-        const uint8_t *Bs = As + BM * BKB;
-        const int c = 4 * (lane >> 5) + S;
+    // The fragments of half of the wavefront's rows (or columns) at a step.
+    template <int N>
+    static __device__ __forceinline__ void read_half(const uint8_t *rows, int first, int chunk, int lane, mx_i32x4 (&f)[N]) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int r = wm0 + i * 32 + (lane & 31);
-            a[i] = *reinterpret_cast<const mx_i32x4 *>(As + r * BKB + ((c ^ swz(r)) * 16));
-        }
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int r = wn0 + j * 32 + (lane & 31);
-            b[j] = *reinterpret_cast<const mx_i32x4 *>(Bs + r * BKB + ((c ^ swz(r)) * 16));
+        for (int i = 0; i < N; ++i) {
+            const int r = first + i * 16 + (lane & 15);
+            f[i] = *reinterpret_cast<const mx_i32x4 *>(rows + r * BKB + ((chunk ^ swz(r)) * 16));
         }
     }
 
-    // Operands swapped, so each accumulator block is the transpose of its C
-    // block: register r of lane l holds row l % 32, column
-    // 8 (r / 4) + 4 (l / 32) + r % 4.
-    template <int S, int LO = 0, int HI = TM * TN>
-    static __device__ __forceinline__ void mfmas(const mx_i32x4 (&a)[TM], const mx_i32x4 (&b)[TN],
-                                                 const int (&sa)[TM], const int (&sb)[TN],
-                                                 mx_f32x16 (&acc)[TM][TN]) {
+    // A quadrant of a step. Operands swapped, so each accumulator block is the
+    // transpose of its C block: register d of lane l holds row l % 16, column 4 (l / 16) + d.
+    template <int S>
+    static __device__ __forceinline__ void quadrant(const mx_i32x4 (&a)[HM], const mx_i32x4 (&b)[HN], const int (&sa)[TM],
+                                                    const int (&sb)[TN], int i0, int j0, mx_f32x4 (&acc)[TM][TN]) {
 #pragma unroll
-        for (int f = LO; f < HI; ++f)
-            acc[f / TN][f % TN] = mx_mfma32<S>(b[f % TN], a[f / TN], acc[f / TN][f % TN], sb[f % TN], sa[f / TN]);
+        for (int i = 0; i < HM; ++i)
+#pragma unroll
+            for (int j = 0; j < HN; ++j)
+                acc[i0 + i][j0 + j] = mx_mfma16<S>(b[j], a[i], acc[i0 + i][j0 + j], sb[j0 + j], sa[i0 + i]);
     }
 
     // Stages [e0, e1) of 8 blocks, e0 even; only the last stage of a row may be
@@ -133,8 +126,8 @@ struct MxTile {
     template <typename OUT>
     static __device__ __forceinline__ void mainloop(const MxGemm &p, uint8_t *smem, int row0, int col0, int e0,
                                                     int e1, int tid, int lane, int wave,
-                                                    mx_f32x16 (&acc)[TM][TN]) {
-        const int wm0 = (wave / WGN) * WTM, wn0 = (wave % WGN) * WTN;
+                                                    mx_f32x4 (&acc)[TM][TN]) {
+        const int wm0 = (wave / WGN) * WTM, wn0 = (wave % WGN) * WTN, quarter = lane >> 4;
         const int nb = p.nb, last = (nb + 7) / 8 - 1;
         const int r0 = tid / CPR, cg = (tid % CPR) ^ swz(r0);
         const uint8_t *Ab = p.a + (int64_t)row0 * p.lda, *Bb = p.b + (int64_t)col0 * p.ldb;
@@ -184,26 +177,26 @@ struct MxTile {
                 dma16(ssrc[i] + 16 * qc, sc + (q & 1) * SCALES + (i * NT + wave * 64) * 16);
         };
         auto read_scales = [&](int e, int (&sa)[TM], int (&sb)[TN]) {
-            const uint8_t *s = sc + ((e >> 1) & 1) * SCALES + 8 * (e & 1) + 4 * (lane >> 5);
+            const uint8_t *s = sc + ((e >> 1) & 1) * SCALES + 8 * (e & 1) + 2 * quarter;
             // (the bytes of blocks past the row's end are cleared: a stray 255 would be NaN)
-            const int left = nb - 8 * min(e, last) - 4 * (lane >> 5);
-            const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+            const int left = nb - 8 * min(e, last) - 2 * quarter;
+            const int keep = left >= 2 ? 0xFFFF : left == 1 ? 0xFF : 0;
 #pragma unroll
             for (int i = 0; i < TM; ++i)
-                sa[i] = *reinterpret_cast<const int *>(s + (wm0 + i * 32 + (lane & 31)) * 16) & keep;
+                sa[i] = *reinterpret_cast<const uint16_t *>(s + (wm0 + i * 16 + (lane & 15)) * 16) & keep;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
-                sb[j] = *reinterpret_cast<const int *>(s + (BM + wn0 + j * 32 + (lane & 31)) * 16) & keep;
+                sb[j] = *reinterpret_cast<const uint16_t *>(s + (BM + wn0 + j * 16 + (lane & 15)) * 16) & keep;
         };
 
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            mx_f32x16 b = {};
+            mx_f32x4 b = {};
             if (p.bias) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int n = col0 + wn0 + 32 * j + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
-                    b[r] = (float)((const OUT *)p.bias)[n < p.N ? n : p.N - 1];
+                for (int d = 0; d < 4; ++d) {
+                    const int n = col0 + wn0 + 16 * j + 4 * quarter + d;
+                    b[d] = (float)((const OUT *)p.bias)[n < p.N ? n : p.N - 1];
                 }
             }
 #pragma unroll
@@ -211,7 +204,7 @@ struct MxTile {
                 acc[i][j] = b;
         }
 
-        mx_i32x4 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
+        mx_i32x4 a0[2][HM], a1[HM], b0[2][HN], b1[HN];
         int sa0[TM], sb0[TN], sa1[TM], sb1[TN];
         // Loads retire in order and the scales of a pair are issued ahead of its
         // stages, so the wait that proves a stage has landed proves its scales too.
@@ -221,38 +214,51 @@ struct MxTile {
             dma_stage(e0 + e);
         wait_vm_lds<(NS - 2) * NL>();
         lds_barrier();
-        read_frags<0>(smem + (e0 % NS) * STAGE, wm0, wn0, lane, fa0, fb0);
+        read_half(smem + (e0 % NS) * STAGE, wm0, 2 * quarter, lane, a0[0]);
+        read_half(smem + (e0 % NS) * STAGE + BM * BKB, wn0, 2 * quarter, lane, b0[0]);
         read_scales(e0, sa0, sb0);
 
         // Stage e: the loads of stage e + NS - 1 go into the slot that stage
         // e - 1 has left (before an even stage the next pair's scales, into the slot
-        // of the pair before this one); each step's fragments are read during the step
-        // before; after the first quarter of the last step's products the barrier
-        // publishes stage e + 1, whose first fragments and scales are read under the rest.
-        constexpr int NMF = TM * TN, KA = NMF >= 4 ? NMF / 4 : 1;
+        // of the pair before this one). A step goes round its quadrants, each of which
+        // needs one new half of the fragments, read during the quadrant before; half way
+        // through the second step the barrier publishes stage e + 1, whose first halves
+        // and scales are read under the other two quadrants.
         auto stage = [&](int e, bool even, const int (&sa)[TM], const int (&sb)[TN], int (&na)[TM], int (&nb2)[TN]) {
-            const uint8_t *S = smem + (e % NS) * STAGE;
+            const uint8_t *A = smem + (e % NS) * STAGE, *B = A + BM * BKB;
+            const uint8_t *An = smem + ((e + 1) % NS) * STAGE, *Bn = An + BM * BKB;
+            const int c0 = 2 * quarter, c1 = c0 + 1;
             __builtin_amdgcn_sched_barrier(0);
             if (even)
                 dma_scales((e >> 1) + 1);
             dma_stage(e + NS - 1);
-            read_frags<1>(S, wm0, wn0, lane, fa1, fb1);
-            mfmas<0>(fa0, fb0, sa, sb, acc);
+            read_half(B, wn0 + HN * 16, c0, lane, b1);
+            quadrant<0>(a0[0], b0[0], sa, sb, 0, 0, acc);
             __builtin_amdgcn_sched_barrier(0);
-            read_frags<2>(S, wm0, wn0, lane, fa0, fb0);
-            mfmas<1>(fa1, fb1, sa, sb, acc);
+            read_half(A, wm0 + HM * 16, c0, lane, a1);
+            quadrant<0>(a0[0], b1, sa, sb, 0, HN, acc);
             __builtin_amdgcn_sched_barrier(0);
-            read_frags<3>(S, wm0, wn0, lane, fa1, fb1);
-            mfmas<2>(fa0, fb0, sa, sb, acc);
+            read_half(A, wm0, c1, lane, a0[1]);
+            quadrant<0>(a1, b1, sa, sb, HM, HN, acc);
             __builtin_amdgcn_sched_barrier(0);
-            mfmas<3, 0, KA>(fa1, fb1, sa, sb, acc);
+            read_half(B, wn0, c1, lane, b0[1]);
+            quadrant<0>(a1, b0[0], sa, sb, HM, 0, acc);
+            __builtin_amdgcn_sched_barrier(0);
+            read_half(B, wn0 + HN * 16, c1, lane, b1);
+            quadrant<1>(a0[1], b0[1], sa, sb, 0, 0, acc);
+            __builtin_amdgcn_sched_barrier(0);
+            read_half(A, wm0 + HM * 16, c1, lane, a1);
+            quadrant<1>(a0[1], b1, sa, sb, 0, HN, acc);
             __builtin_amdgcn_sched_barrier(0);
             wait_vm_lds<(NS - 2) * NL>();
             lds_barrier();
             __builtin_amdgcn_sched_barrier(0);
-            read_frags<0>(smem + ((e + 1) % NS) * STAGE, wm0, wn0, lane, fa0, fb0);
+            read_half(An, wm0, c0, lane, a0[0]);
             read_scales(e + 1, na, nb2);
-            mfmas<3, KA, NMF>(fa1, fb1, sa, sb, acc);
+            quadrant<1>(a1, b1, sa, sb, HM, HN, acc);
+            __builtin_amdgcn_sched_barrier(0);
+            read_half(Bn, wn0, c0, lane, b0[0]);
+            quadrant<1>(a1, b0[1], sa, sb, HM, 0, acc);
             __builtin_amdgcn_sched_barrier(0);
         };
         int e = e0;
@@ -271,7 +277,7 @@ struct MxTile {
     // c ^ (r % chunks per row).
     template <typename OUT>
     static __device__ __forceinline__ void epilogue(const MxGemm &p, uint8_t *smem, int row0, int col0, int lane,
-                                                    int wave, const mx_f32x16 (&acc)[TM][TN]) {
+                                                    int wave, const mx_f32x4 (&acc)[TM][TN]) {
         constexpr int RB = WTN * (int)sizeof(OUT), CPW = RB / 16;
         constexpr int EPC = 16 / (int)sizeof(OUT);   // outputs per chunk
         static_assert(NW * 32 * RB <= LDS_BYTES && (CPW & (CPW - 1)) == 0 && CPW >= 4, "epilogue staging");
@@ -282,19 +288,17 @@ struct MxTile {
         __syncthreads();   // every wavefront is past its last fragment read
         typedef OUT out4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int rl = lane & 31;
+        for (int i = 0; i < TM; i += 2) {
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int cl = 32 * j + 8 * g + 4 * (lane >> 5);
+                for (int j = 0; j < TN; ++j) {
+                    const int rl = 16 * h + (lane & 15), cl = 16 * j + 4 * (lane >> 4);
                     out4 v;
 #pragma unroll
                     for (int d = 0; d < 4; ++d)
-                        v[d] = (OUT)acc[i][j][4 * g + d];
-                    const int c = cl / EPC;
-                    *reinterpret_cast<out4 *>(region + rl * RB + ((c ^ (rl & (CPW - 1))) * 16) +
+                        v[d] = (OUT)acc[i + h][j][d];
+                    *reinterpret_cast<out4 *>(region + rl * RB + (((cl / EPC) ^ (rl & (CPW - 1))) * 16) +
                                               (cl % EPC) * (int)sizeof(OUT)) = v;
                 }
             wave_lds_fence();
@@ -303,7 +307,7 @@ struct MxTile {
                 const int f = q * 64 + lane;
                 const int r = f / CPW, c = f % CPW;
                 const u32x4 v = *reinterpret_cast<const u32x4 *>(region + r * RB + ((c ^ (r & (CPW - 1))) * 16));
-                const int row = row0 + wm0 + i * 32 + r, col = col0 + wn0 + c * EPC;
+                const int row = row0 + wm0 + i * 16 + r, col = col0 + wn0 + c * EPC;
                 if (row < p.M) {
                     OUT *dst = C + (int64_t)row * p.ldc + col;
                     if (vec && col + EPC <= p.N) {
@@ -338,7 +342,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mx_tile_kernel(MxGemm p, int t
     mx_tile_of(blockIdx.x, gridDim.x, tiles_m, tiles_n, tm, tn);
     const int stages = (p.nb + 7) / 8;
     const int e0 = blockIdx.y * slice, e1 = min(e0 + slice, stages);
-    mx_f32x16 acc[MT::TM][MT::TN];
+    mx_f32x4 acc[MT::TM][MT::TN];
     MT::template mainloop<OUT>(p, smem, tm * BM, tn * BN, e0, e1, tid, lane, wave, acc);
     if (gridDim.y > 1)
         p.c = (float *)p.c + (int64_t)blockIdx.y * p.M * p.ldc;
