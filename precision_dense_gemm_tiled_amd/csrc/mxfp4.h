@@ -49,10 +49,11 @@ struct MxSkinnyX {
 enum MxKind { MX_SKINNY = 0, MX_TILE = 1, MX_EMPTY = 2 };
 struct MxPlan {
     int kind;
-    int cfg;       // skinny: rows of 16 per workgroup; tile: index of the tile table
+    int cfg;       // skinny: blocks of 16 rows; tile: index of the tile table
     int ks;        // K slices (tile kernel): fp32 partial results in the workspace when > 1
     int slice;     // stages of 8 blocks per slice
     int64_t partial_bytes;
+    int cus;       // CUs of the device
 };
 // `fused`: A is quantised in the kernel if the plan is MX_SKINNY with M <= 16.
 MxPlan plan_mx(int64_t M, int64_t N, int64_t nb, int cu_count);

@@ -53,13 +53,6 @@ __device__ __forceinline__ void mx_tile_of(int bid, int nblk, int tiles_m, int t
     tn = in / rows;
 }
 
-// Scale word of blocks blk .. blk + 3 with the bytes of blocks >= nb cleared
-// (their codes are read as zeros, and a stray 255 would make them NaN).
-__device__ __forceinline__ int mx_mask_scales(int w, int blk, int nb) {
-    const int left = nb - blk;
-    return left >= 4 ? w : (left <= 0 ? 0 : (int)((uint32_t)w & ((1u << (8 * left)) - 1u)));
-}
-
 template <typename T>
 __device__ __forceinline__ float mx_bias(const void *bias, int n) {
     return bias ? (float)((const T *)bias)[n] : 0.f;
@@ -366,11 +359,24 @@ __global__ __launch_bounds__(256) void mx_join_kernel(const float *part, int64_t
 // ------------------------------------------------------------------ skinny
 
 // 16 MF rows x 16 NF columns per workgroup, K in groups of 16 blocks dealt out
-// to the 8 wavefronts in turn. In a group, lane quarter q takes blocks
-// 4 q ... 4 q + 3 (64 contiguous bytes of its row, and one word of scales), one
-// per step. The wavefronts' sums are joined in LDS in the order of the
-// wavefronts. FUSED (MF = 1): a lane quantises the 32 activations of its block
-// in registers; rows past M are zero.
+// to the 8 wavefronts in turn. At step s of a group, lane quarter q takes block
+// 4 s + q, so that a load instruction reads 64 contiguous bytes of each of 16 rows; the
+// scale bytes of its four blocks are picked from the row's 16. B of the next group is on
+// its way during a group. The wavefronts' sums are joined in LDS in the order of the
+// wavefronts. FUSED (MF = 1): a lane quantises the 32 activations of its block in
+// registers; rows past M are zero.
+
+// Bytes 4 s + quarter of a row's 16 scale bytes as byte s of a word, those of blocks
+// >= left (blocks of the row from the group's first one on) cleared: their codes
+// are read as zeros, and a stray 255 would make them NaN.
+__device__ __forceinline__ int mx_pick_scales(u32x4 w, int quarter, int left) {
+    const uint32_t sel = (uint32_t)quarter + ((uint32_t)(quarter + 4) << 8);
+    const uint32_t lo = __builtin_amdgcn_perm(w[1], w[0], sel), hi = __builtin_amdgcn_perm(w[3], w[2], sel);
+    const uint32_t v = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+    const int n = (left - quarter + 3) >> 2;   // of this quarter's four blocks inside the row
+    return n >= 4 ? (int)v : n <= 0 ? 0 : (int)(v & ((1u << (8 * n)) - 1u));
+}
+
 template <typename T, int MF, int NF, bool FUSED, bool VEC>
 __global__ __launch_bounds__(512) void mx_skinny_kernel(MxGemm p, MxSkinnyX px) {
     constexpr int NW = 8;
@@ -381,21 +387,37 @@ __global__ __launch_bounds__(512) void mx_skinny_kernel(MxGemm p, MxSkinnyX px) 
     const int n0 = blockIdx.x * 16 * NF;
     const int nb = p.nb, groups = (nb + 15) / 16;
 
-    const uint8_t *bq[NF], *bs[NF];
+    // The four blocks and the scales of one group of a row.
+    struct Rows {
+        mx_i32x4 v[4];
+        u32x4 s;
+    };
+    const uint8_t *bq[NF], *bs[NF], *aq[MF], *as[MF];
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
         const int n = min(n0 + 16 * j + r, p.N - 1);
-        bq[j] = p.b + (int64_t)n * p.ldb + 64 * q;
-        bs[j] = p.sb + (int64_t)n * p.ldsb + 4 * q;
+        bq[j] = p.b + (int64_t)n * p.ldb + 16 * q;
+        bs[j] = p.sb + (int64_t)n * p.ldsb;
     }
-    const uint8_t *aq[MF], *as[MF];
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
         const int m = min(16 * i + r, p.M - 1);
-        aq[i] = FUSED ? nullptr : p.a + (int64_t)m * p.lda + 64 * q;
-        as[i] = FUSED ? nullptr : p.sa + (int64_t)m * p.ldsa + 4 * q;
+        aq[i] = FUSED ? nullptr : p.a + (int64_t)m * p.lda + 16 * q;
+        as[i] = FUSED ? nullptr : p.sa + (int64_t)m * p.ldsa;
     }
-    const T *x = (const T *)px.x + (int64_t)min(r, p.M - 1) * px.ldx;
+    auto load = [&](const uint8_t *row, const uint8_t *scales, int g, Rows &x) {
+        if (16 * g + 16 <= nb) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                x.v[s] = *reinterpret_cast<const mx_i32x4 *>(row + (int64_t)g * 256 + 64 * s);
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                x.v[s] = 16 * g + 4 * s + q < nb ? *reinterpret_cast<const mx_i32x4 *>(row + (int64_t)g * 256 + 64 * s)
+                                                 : mx_i32x4{0, 0, 0, 0};
+        }
+        x.s = *reinterpret_cast<const u32x4 *>(scales + 16 * g);
+    };
 
     mx_f32x4 acc[MF][NF];
 #pragma unroll
@@ -404,59 +426,85 @@ __global__ __launch_bounds__(512) void mx_skinny_kernel(MxGemm p, MxSkinnyX px) 
         for (int j = 0; j < NF; ++j)
             acc[i][j] = mx_f32x4{};
 
+    Rows b[NF], bn[NF];
+    if (wave < groups) {
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            load(bq[j], bs[j], wave, b[j]);
+    }
     for (int g = wave; g < groups; g += NW) {
-        const int blk = 16 * g + 4 * q;   // first of this lane's four blocks
-        mx_i32x4 b[NF][4], a[MF][4];
-        int sb[NF], sa[MF];
-        auto load4 = [&](const uint8_t *row, mx_i32x4 (&v)[4]) {
+        const int left = nb - 16 * g;
+        Rows a[MF];
+        int sa[MF];
+        if constexpr (!FUSED) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-                v[s] = blk + s < nb ? *reinterpret_cast<const mx_i32x4 *>(row + (int64_t)g * 256 + 16 * s)
-                                    : mx_i32x4{0, 0, 0, 0};
-        };
-        auto load_scales = [&](const uint8_t *row) {
-            return blk < nb ? mx_mask_scales(*reinterpret_cast<const int *>(row + 16 * g), blk, nb) : 0;
-        };
+            for (int i = 0; i < MF; ++i)
+                load(aq[i], as[i], g, a[i]);
+        }
+        if (g + NW < groups) {
 #pragma unroll
-        for (int j = 0; j < NF; ++j) {
-            load4(bq[j], b[j]);
-            sb[j] = load_scales(bs[j]);
+            for (int j = 0; j < NF; ++j)
+                load(bq[j], bs[j], g + NW, bn[j]);
         }
         if constexpr (FUSED) {
             uint32_t word = 0;
-            const bool live = r < p.M;
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
+                const int k0 = 32 * (16 * g + 4 * s + q);
+                const T *x = (const T *)px.x + (int64_t)r * px.ldx;   // (read where r < M)
                 uint32_t u[4][MxPack<T>::WORDS8];
+#pragma unroll
+                for (int o = 0; o < 4; ++o)
+#pragma unroll
+                    for (int d = 0; d < MxPack<T>::WORDS8; ++d)
+                        u[o][d] = 0;
+                if (r < p.M) {
+                    if (VEC && k0 + 32 <= px.K) {
+#pragma unroll
+                        for (int o = 0; o < 4; ++o)
+#pragma unroll
+                            for (int d = 0; d < MxPack<T>::WORDS8; d += 4) {
+                                const u32x4 w = *reinterpret_cast<const u32x4 *>((const uint32_t *)(x + k0 + 8 * o) + d);
+                                u[o][d] = w[0], u[o][d + 1] = w[1], u[o][d + 2] = w[2], u[o][d + 3] = w[3];
+                            }
+                    } else if (k0 < px.K) {
+#pragma unroll
+                        for (int o = 0; o < 4; ++o)
+                            mx_load8<T, false>(x, k0 + 8 * o, px.K, u[o]);
+                    }
+                }
                 uint32_t am = 0;
 #pragma unroll
-                for (int o = 0; o < 4; ++o) {
-                    mx_load8<T, VEC>(x, 32 * (blk + s) + 8 * o, live ? px.K : 0, u[o]);
+                for (int o = 0; o < 4; ++o)
                     am = max(am, mx_amax8<T>(u[o]));
-                }
                 const uint32_t sc = mx_scale_of(am);
 #pragma unroll
                 for (int o = 0; o < 4; ++o)
-                    a[0][s][o] = (int)mx_pack8<T>(u[o], sc);
+                    a[0].v[s][o] = (int)mx_pack8<T>(u[o], sc);
                 word |= sc << (8 * s);
             }
             sa[0] = (int)word;
         } else {
 #pragma unroll
-            for (int i = 0; i < MF; ++i) {
-                load4(aq[i], a[i]);
-                sa[i] = load_scales(as[i]);
-            }
+            for (int i = 0; i < MF; ++i)
+                sa[i] = mx_pick_scales(a[i].s, q, left);
         }
+        int sb[NF];
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            sb[j] = mx_pick_scales(b[j].s, q, left);
 #pragma unroll
         for (int i = 0; i < MF; ++i)
 #pragma unroll
             for (int j = 0; j < NF; ++j) {
-                acc[i][j] = mx_mfma16<0>(a[i][0], b[j][0], acc[i][j], sa[i], sb[j]);
-                acc[i][j] = mx_mfma16<1>(a[i][1], b[j][1], acc[i][j], sa[i], sb[j]);
-                acc[i][j] = mx_mfma16<2>(a[i][2], b[j][2], acc[i][j], sa[i], sb[j]);
-                acc[i][j] = mx_mfma16<3>(a[i][3], b[j][3], acc[i][j], sa[i], sb[j]);
+                acc[i][j] = mx_mfma16<0>(a[i].v[0], b[j].v[0], acc[i][j], sa[i], sb[j]);
+                acc[i][j] = mx_mfma16<1>(a[i].v[1], b[j].v[1], acc[i][j], sa[i], sb[j]);
+                acc[i][j] = mx_mfma16<2>(a[i].v[2], b[j].v[2], acc[i][j], sa[i], sb[j]);
+                acc[i][j] = mx_mfma16<3>(a[i].v[3], b[j].v[3], acc[i][j], sa[i], sb[j]);
             }
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            b[j] = bn[j];
     }
     // register d of lane l: row 4 (l / 16) + d, column l % 16 of the block
 #pragma unroll
@@ -490,7 +538,7 @@ struct MxCfg { int BM, BN; double cost; };
 static const MxCfg kMxCfg[] = {{256, 256, 4.0}, {128, 128, 1.25}, {64, 64, 0.5}};
 
 MxPlan plan_mx(int64_t M, int64_t N, int64_t nb, int cu_count) {
-    MxPlan pl = {MX_TILE, 0, 1, 0, 0};
+    MxPlan pl = {MX_TILE, 0, 1, 0, 0, cu_count};
     if (nb == 0) {
         pl.kind = MX_EMPTY;
         return pl;
@@ -555,18 +603,29 @@ static void join(const float *part, int64_t ldp, int ks, const MxGemm &p, hipStr
                        part, ldp, ks, p);
 }
 
+// 32 columns per workgroup once that still gives every CU one: the activations are
+// then read, and in the fused form quantised, half as often.
+template <typename T, int MF, bool FUSED, bool VEC>
+static void skinny_one(const MxGemm &p, const MxSkinnyX &px, int cus, hipStream_t stream) {
+    if (p.N >= 32 * cus)
+        hipLaunchKernelGGL((mx_skinny_kernel<T, MF, 2, FUSED, VEC>), dim3((p.N + 31) / 32), dim3(512), 0, stream, p, px);
+    else
+        hipLaunchKernelGGL((mx_skinny_kernel<T, MF, 1, FUSED, VEC>), dim3((p.N + 15) / 16), dim3(512), 0, stream, p, px);
+}
+
 template <typename T>
 static hipError_t gemm_type(const MxGemm &p, const MxPlan &plan, float *partial, hipStream_t stream) {
+    const int cus = plan.cus;
     if (plan.kind == MX_EMPTY) {
         join<T>(nullptr, 0, 0, p, stream);
     } else if (plan.kind == MX_SKINNY) {
         const MxSkinnyX px = {};
         if (plan.cfg == 1)
-            hipLaunchKernelGGL((mx_skinny_kernel<T, 1, 1, false, true>), dim3((p.N + 15) / 16), dim3(512), 0, stream, p, px);
+            skinny_one<T, 1, false, true>(p, px, cus, stream);
         else if (plan.cfg == 2)
-            hipLaunchKernelGGL((mx_skinny_kernel<T, 2, 1, false, true>), dim3((p.N + 15) / 16), dim3(512), 0, stream, p, px);
+            skinny_one<T, 2, false, true>(p, px, cus, stream);
         else
-            hipLaunchKernelGGL((mx_skinny_kernel<T, 4, 1, false, true>), dim3((p.N + 15) / 16), dim3(512), 0, stream, p, px);
+            skinny_one<T, 4, false, true>(p, px, cus, stream);
     } else if (plan.ks > 1) {
         MxGemm s = p;
         s.c = partial;
@@ -592,22 +651,22 @@ hipError_t launch_mx_gemm(int type, const MxGemm &p, const MxPlan &plan, float *
 }
 
 template <typename T>
-static hipError_t gemm_x_type(const MxGemm &p, const MxSkinnyX &px, hipStream_t stream) {
+static hipError_t gemm_x_type(const MxGemm &p, const MxSkinnyX &px, int cus, hipStream_t stream) {
     const bool vec = (reinterpret_cast<uintptr_t>(px.x) & 15) == 0 && (px.ldx * sizeof(T)) % 16 == 0;
     if (vec)
-        hipLaunchKernelGGL((mx_skinny_kernel<T, 1, 1, true, true>), dim3((p.N + 15) / 16), dim3(512), 0, stream, p, px);
+        skinny_one<T, 1, true, true>(p, px, cus, stream);
     else
-        hipLaunchKernelGGL((mx_skinny_kernel<T, 1, 1, true, false>), dim3((p.N + 15) / 16), dim3(512), 0, stream, p, px);
+        skinny_one<T, 1, true, false>(p, px, cus, stream);
     return hipGetLastError();
 }
 
-hipError_t launch_mx_gemm_x(int type, const MxGemm &p, const MxSkinnyX &px, const MxPlan &plan, hipStream_t stream) {
+hipError_t launch_mx_gemm_x(int type, const MxGemm &p, const MxSkinnyX &x, const MxPlan &plan, hipStream_t stream) {
     if (!mx_fuses(plan, p.M))
         return hipErrorInvalidValue;
     switch (type) {
-    case MPGEMM_TYPE_F16: return gemm_x_type<_Float16>(p, px, stream);
-    case MPGEMM_TYPE_BF16: return gemm_x_type<__bf16>(p, px, stream);
-    default: return gemm_x_type<float>(p, px, stream);
+    case MPGEMM_TYPE_F16: return gemm_x_type<_Float16>(p, x, plan.cus, stream);
+    case MPGEMM_TYPE_BF16: return gemm_x_type<__bf16>(p, x, plan.cus, stream);
+    default: return gemm_x_type<float>(p, x, plan.cus, stream);
     }
 }
 
