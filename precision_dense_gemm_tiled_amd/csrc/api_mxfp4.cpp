@@ -186,7 +186,7 @@ int64_t mpgemm_run_mxfp4_dyn_workspace(int64_t M, int64_t N, int64_t K, int cu_c
     const int64_t partial = mpgemm_run_mxfp4_workspace(M, N, K, cu_count);
     if (partial < 0 || M == 0 || N == 0 || K == 0)
         return partial;
-    if (mpg::mx_fuses(mpg::plan_mx(M, N, blocks_of(K), cu_count), M))
+    if (mpg::mx_fuses(mpg::plan_mx(M, N, blocks_of(K), cu_count), M, blocks_of(K)))
         return 0;
     return round_up(Held(M, K).bytes, 256) + partial;
 }
@@ -213,7 +213,7 @@ mpgemm_status_t mpgemm_run_mxfp4_dyn(mpgemm_handle_t h, int64_t M, int64_t N, in
     if (!h)
         return MPGEMM_ERR_INVALID_ARG;
     const mpg::MxPlan plan = mpg::plan_mx(M, N, blocks_of(K), h->cu_count);
-    const bool fused = mpg::mx_fuses(plan, M);
+    const bool fused = mpg::mx_fuses(plan, M, blocks_of(K));
     const Held a(M, K);
     const int64_t a_bytes = fused || K == 0 ? 0 : round_up(a.bytes, 256);
     st = check_workspace(workspace, workspace_bytes, a_bytes + plan.partial_bytes);
@@ -226,7 +226,7 @@ mpgemm_status_t mpgemm_run_mxfp4_dyn(mpgemm_handle_t h, int64_t M, int64_t N, in
     uint8_t *q = static_cast<uint8_t *>(workspace);
     const mpg::MxGemm p = product(M, N, K, q, a.ldq, q + a.q_bytes, a.lds, W, ldw, SW, ldsw, bias, Y, ldy);
     if (fused) {
-        const mpg::MxSkinnyX x{X, ldx, (int)K};
+        const mpg::MxSkinnyX x{X, ldx, (int)K, 0};
         return status_of(mpg::launch_mx_gemm_x(type, p, x, plan, s));
     }
     if (K > 0) {

@@ -43,6 +43,7 @@ struct MxSkinnyX {
     const void *x;
     int64_t ldx;
     int K;
+    int rlog;   // set by the launcher: log2 of the rows held per block, at least M
 };
 
 // What a product runs, decided from the sizes alone.
@@ -55,9 +56,9 @@ struct MxPlan {
     int64_t partial_bytes;
     int cus;       // CUs of the device
 };
-// `fused`: A is quantised in the kernel if the plan is MX_SKINNY with M <= 16.
 MxPlan plan_mx(int64_t M, int64_t N, int64_t nb, int cu_count);
-bool mx_fuses(const MxPlan &plan, int64_t M);
+// Whether the product quantises the activations itself.
+bool mx_fuses(const MxPlan &plan, int64_t M, int64_t nb);
 hipError_t launch_mx_gemm(int type, const MxGemm &p, const MxPlan &plan, float *partial, hipStream_t stream);
 hipError_t launch_mx_gemm_x(int type, const MxGemm &p, const MxSkinnyX &x, const MxPlan &plan, hipStream_t stream);
 

@@ -366,6 +366,8 @@ __global__ __launch_bounds__(256) void mx_join_kernel(const float *part, int64_t
 // wavefronts. FUSED (MF = 1): a lane quantises the 32 activations of its block in
 // registers; rows past M are zero.
 
+constexpr int MX_FUSE_PIECES = 4;
+
 // Bytes 4 s + quarter of a row's 16 scale bytes as byte s of a word, those of blocks
 // >= left (blocks of the row from the group's first one on) cleared: their codes
 // are read as zeros, and a stray 255 would make them NaN.
@@ -380,12 +382,16 @@ __device__ __forceinline__ int mx_pick_scales(u32x4 w, int quarter, int left) {
 template <typename T, int MF, int NF, bool FUSED, bool VEC>
 __global__ __launch_bounds__(512) void mx_skinny_kernel(MxGemm p, MxSkinnyX px) {
     constexpr int NW = 8;
-    __shared__ float red[NW][MF * NF][4][64];
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    float (*red)[MF * NF][4][64] = reinterpret_cast<float (*)[MF * NF][4][64]>(smem);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, r = lane & 15;
     const int n0 = blockIdx.x * 16 * NF;
     const int nb = p.nb, groups = (nb + 15) / 16;
+    uint8_t *codes = smem + sizeof(float) * NW * MF * NF * 256;   // FUSED: 16 bytes per block and row
+    uint8_t *scales = codes + ((size_t)(groups * 16) << (px.rlog + 4));   // a word per group, quarter and row
+    const int rmask = (1 << px.rlog) - 1;
 
     // The four blocks and the scales of one group of a row.
     struct Rows {
@@ -432,6 +438,33 @@ __global__ __launch_bounds__(512) void mx_skinny_kernel(MxGemm p, MxSkinnyX px) 
         for (int j = 0; j < NF; ++j)
             load(bq[j], bs[j], wave, b[j]);
     }
+    if constexpr (FUSED) {
+        // pieces of 8 elements, of whole groups: at most MX_FUSE_PIECES per thread, all loaded first
+        const int per_row = groups * 64;
+        uint32_t u[MX_FUSE_PIECES][MxPack<T>::WORDS8];
+#pragma unroll
+        for (int i = 0; i < MX_FUSE_PIECES; ++i) {
+            const int f = i * 512 + tid, row = f / per_row;
+            if (row < p.M)
+                mx_load8<T, VEC>((const T *)px.x + (int64_t)row * px.ldx, (f - row * per_row) * 8, px.K, u[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < MX_FUSE_PIECES; ++i) {
+            const int f = i * 512 + tid, row = f / per_row, piece = f - row * per_row, blk = piece >> 2;
+            if (row >= p.M)
+                break;
+            uint32_t am = mx_amax8<T>(u[i]);
+            am = max(am, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)am, 0xB1, 0xF, 0xF, false));
+            am = max(am, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)am, 0x4E, 0xF, 0xF, false));
+            const uint32_t sc = mx_scale_of(am);
+            *reinterpret_cast<uint32_t *>(codes + ((((size_t)blk << px.rlog) + ((row ^ blk) & rmask)) * 16 + (piece & 3) * 4)) =
+                mx_pack8<T>(u[i], sc);
+            // block 16 g + 4 s + quarter: byte s of its word
+            if ((piece & 3) == 0)
+                scales[(((size_t)((blk >> 4) * 4 + (blk & 3)) << px.rlog) + row) * 4 + ((blk >> 2) & 3)] = (uint8_t)sc;
+        }
+        __syncthreads();
+    }
     for (int g = wave; g < groups; g += NW) {
         const int left = nb - 16 * g;
         Rows a[MF];
@@ -447,43 +480,13 @@ __global__ __launch_bounds__(512) void mx_skinny_kernel(MxGemm p, MxSkinnyX px) 
                 load(bq[j], bs[j], g + NW, bn[j]);
         }
         if constexpr (FUSED) {
-            uint32_t word = 0;
+            // (rows past M repeat others: their outputs are not stored)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const int k0 = 32 * (16 * g + 4 * s + q);
-                const T *x = (const T *)px.x + (int64_t)r * px.ldx;   // (read where r < M)
-                uint32_t u[4][MxPack<T>::WORDS8];
-#pragma unroll
-                for (int o = 0; o < 4; ++o)
-#pragma unroll
-                    for (int d = 0; d < MxPack<T>::WORDS8; ++d)
-                        u[o][d] = 0;
-                if (r < p.M) {
-                    if (VEC && k0 + 32 <= px.K) {
-#pragma unroll
-                        for (int o = 0; o < 4; ++o)
-#pragma unroll
-                            for (int d = 0; d < MxPack<T>::WORDS8; d += 4) {
-                                const u32x4 w = *reinterpret_cast<const u32x4 *>((const uint32_t *)(x + k0 + 8 * o) + d);
-                                u[o][d] = w[0], u[o][d + 1] = w[1], u[o][d + 2] = w[2], u[o][d + 3] = w[3];
-                            }
-                    } else if (k0 < px.K) {
-#pragma unroll
-                        for (int o = 0; o < 4; ++o)
-                            mx_load8<T, false>(x, k0 + 8 * o, px.K, u[o]);
-                    }
-                }
-                uint32_t am = 0;
-#pragma unroll
-                for (int o = 0; o < 4; ++o)
-                    am = max(am, mx_amax8<T>(u[o]));
-                const uint32_t sc = mx_scale_of(am);
-#pragma unroll
-                for (int o = 0; o < 4; ++o)
-                    a[0].v[s][o] = (int)mx_pack8<T>(u[o], sc);
-                word |= sc << (8 * s);
+                const int blk = 16 * g + 4 * s + q;
+                a[0].v[s] = *reinterpret_cast<const mx_i32x4 *>(codes + (((size_t)blk << px.rlog) + ((r ^ blk) & rmask)) * 16);
             }
-            sa[0] = (int)word;
+            sa[0] = *reinterpret_cast<const int *>(scales + (((size_t)(4 * g + q) << px.rlog) + (r & rmask)) * 4);
         } else {
 #pragma unroll
             for (int i = 0; i < MF; ++i)
@@ -578,7 +581,18 @@ MxPlan plan_mx(int64_t M, int64_t N, int64_t nb, int cu_count) {
     return pl;
 }
 
-bool mx_fuses(const MxPlan &plan, int64_t M) { return plan.kind == MX_SKINNY && M <= 16; }
+static int mx_rlog(int64_t M) { return M <= 1 ? 0 : M <= 2 ? 1 : M <= 4 ? 2 : M <= 8 ? 3 : 4; }
+
+// LDS bytes of quantised activations: codes and scale words of whole groups.
+static unsigned mx_fused_bytes(int64_t nb, int rlog) { return (unsigned)(((nb + 15) / 16 * (4096 + 256)) >> (4 - rlog)); }
+
+// Few activations: every workgroup quantises all of them. Fused and with a launch of
+// the quantisation kernel before (us, other weights each call): 1 x 4096 x 4096 5.0 and 7.3,
+// 4 x 4096 x 4096 6.0 and 7.8, 1 x 8192 x 8192 11.6 and 12.3; 16 x 4096 x 4096 10.6 and 8.1, 16 x 8192 x 8192
+// 25 and 14.
+bool mx_fuses(const MxPlan &plan, int64_t M, int64_t nb) {
+    return plan.kind == MX_SKINNY && M <= 16 && M * ((nb + 15) / 16) <= MX_FUSE_PIECES * 512 / 64;
+}
 
 template <typename OUT, int BM, int BN, int WGM, int WGN, int NS>
 static void tile_one(const MxGemm &p, const MxPlan &plan, hipStream_t stream) {
@@ -607,10 +621,11 @@ static void join(const float *part, int64_t ldp, int ks, const MxGemm &p, hipStr
 // then read, and in the fused form quantised, half as often.
 template <typename T, int MF, bool FUSED, bool VEC>
 static void skinny_one(const MxGemm &p, const MxSkinnyX &px, int cus, hipStream_t stream) {
+    const unsigned fused = FUSED ? mx_fused_bytes(p.nb, px.rlog) : 0;
     if (p.N >= 32 * cus)
-        hipLaunchKernelGGL((mx_skinny_kernel<T, MF, 2, FUSED, VEC>), dim3((p.N + 31) / 32), dim3(512), 0, stream, p, px);
+        hipLaunchKernelGGL((mx_skinny_kernel<T, MF, 2, FUSED, VEC>), dim3((p.N + 31) / 32), dim3(512), MF * 16384 + fused, stream, p, px);
     else
-        hipLaunchKernelGGL((mx_skinny_kernel<T, MF, 1, FUSED, VEC>), dim3((p.N + 15) / 16), dim3(512), 0, stream, p, px);
+        hipLaunchKernelGGL((mx_skinny_kernel<T, MF, 1, FUSED, VEC>), dim3((p.N + 15) / 16), dim3(512), MF * 8192 + fused, stream, p, px);
 }
 
 template <typename T>
@@ -660,9 +675,11 @@ static hipError_t gemm_x_type(const MxGemm &p, const MxSkinnyX &px, int cus, hip
     return hipGetLastError();
 }
 
-hipError_t launch_mx_gemm_x(int type, const MxGemm &p, const MxSkinnyX &x, const MxPlan &plan, hipStream_t stream) {
-    if (!mx_fuses(plan, p.M))
+hipError_t launch_mx_gemm_x(int type, const MxGemm &p, const MxSkinnyX &px, const MxPlan &plan, hipStream_t stream) {
+    if (!mx_fuses(plan, p.M, p.nb))
         return hipErrorInvalidValue;
+    MxSkinnyX x = px;
+    x.rlog = mx_rlog(p.M);
     switch (type) {
     case MPGEMM_TYPE_F16: return gemm_x_type<_Float16>(p, x, plan.cus, stream);
     case MPGEMM_TYPE_BF16: return gemm_x_type<__bf16>(p, x, plan.cus, stream);
