@@ -152,11 +152,34 @@ __device__ __forceinline__ void mx_columns(const uint32_t (&v)[32], uint32_t (&b
     }
 }
 
-// The value of one code: e2m1 magnitudes are {0, 1, 2, 3, 4, 6, 8, 12} / 2.
-__device__ __forceinline__ float mx_value(uint32_t code, float scale, uint32_t b) {
-    const uint32_t twice = (uint32_t)(0xC8643210u >> (4 * (code & 7))) & 15u;
-    const float v = (float)twice * 0.5f * scale;
-    return b == 255 ? __builtin_nanf("") : ((code & 8) ? -v : v);
+// Values of byte SEL of w (two codes) as words: one of a 2-byte type, two of fp32.
+// The conversion reads the scale's exponent field only, 0 as 2^-127.
+template <typename T, int SEL>
+__device__ __forceinline__ void mx_values2(uint32_t w, float s, uint32_t *v) {
+    if constexpr (__is_same(T, _Float16)) {
+        v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, SEL));
+    } else if constexpr (__is_same(T, __bf16)) {
+        v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, SEL));
+    } else {
+        const auto f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, SEL);
+        v[0] = __float_as_uint(f[0]);
+        v[1] = __float_as_uint(f[1]);
+    }
+}
+
+// 8 codes and their scale byte -> 8 values; a scale of 255 makes them NaN.
+template <typename T>
+__device__ __forceinline__ void mx_unpack8(uint32_t w, uint32_t b, uint32_t (&v)[MxPack<T>::WORDS8]) {
+    constexpr int W2 = MxPack<T>::WORDS8 / 4;
+    constexpr uint32_t NAN_WORD = __is_same(T, _Float16) ? 0x7E007E00u : __is_same(T, __bf16) ? 0x7FC07FC0u : 0x7FC00000u;
+    const float s = __uint_as_float(b << 23);
+    mx_values2<T, 0>(w, s, v);
+    mx_values2<T, 1>(w, s, v + W2);
+    mx_values2<T, 2>(w, s, v + 2 * W2);
+    mx_values2<T, 3>(w, s, v + 3 * W2);
+#pragma unroll
+    for (int d = 0; d < MxPack<T>::WORDS8; ++d)
+        v[d] = b == 255 ? NAN_WORD : v[d];
 }
 
 }  // namespace mpg

@@ -379,9 +379,10 @@ __device__ __forceinline__ int mx_pick_scales(u32x4 w, int quarter, int left) {
     return n >= 4 ? (int)v : n <= 0 ? 0 : (int)(v & ((1u << (8 * n)) - 1u));
 }
 
-template <typename T, int MF, int NF, bool FUSED, bool VEC>
+template <typename T, int MF, int NF, int PIECES, bool VEC>
 __global__ __launch_bounds__(512) void mx_skinny_kernel(MxGemm p, MxSkinnyX px) {
     constexpr int NW = 8;
+    constexpr bool FUSED = PIECES > 0;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     float (*red)[MF * NF][4][64] = reinterpret_cast<float (*)[MF * NF][4][64]>(smem);
     const int tid = threadIdx.x, lane = tid & 63;
@@ -402,26 +403,21 @@ __global__ __launch_bounds__(512) void mx_skinny_kernel(MxGemm p, MxSkinnyX px) 
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
         const int n = min(n0 + 16 * j + r, p.N - 1);
-        bq[j] = p.b + (int64_t)n * p.ldb + 16 * q;
+        bq[j] = p.b + (int64_t)n * p.ldb;
         bs[j] = p.sb + (int64_t)n * p.ldsb;
     }
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
         const int m = min(16 * i + r, p.M - 1);
-        aq[i] = FUSED ? nullptr : p.a + (int64_t)m * p.lda + 16 * q;
+        aq[i] = FUSED ? nullptr : p.a + (int64_t)m * p.lda;
         as[i] = FUSED ? nullptr : p.sa + (int64_t)m * p.ldsa;
     }
+    // (No branches: a wait for all loads would stand behind each. Blocks past the row's
+    // end are its last one again, under a scale of 0; A's codes are cleared too.)
     auto load = [&](const uint8_t *row, const uint8_t *scales, int g, Rows &x) {
-        if (16 * g + 16 <= nb) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-                x.v[s] = *reinterpret_cast<const mx_i32x4 *>(row + (int64_t)g * 256 + 64 * s);
-        } else {
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-                x.v[s] = 16 * g + 4 * s + q < nb ? *reinterpret_cast<const mx_i32x4 *>(row + (int64_t)g * 256 + 64 * s)
-                                                 : mx_i32x4{0, 0, 0, 0};
-        }
+        for (int s = 0; s < 4; ++s)
+            x.v[s] = *reinterpret_cast<const mx_i32x4 *>(row + (int64_t)min(16 * g + 4 * s + q, nb - 1) * 16);
         x.s = *reinterpret_cast<const u32x4 *>(scales + 16 * g);
     };
 
@@ -433,35 +429,46 @@ __global__ __launch_bounds__(512) void mx_skinny_kernel(MxGemm p, MxSkinnyX px) 
             acc[i][j] = mx_f32x4{};
 
     Rows b[NF], bn[NF];
-    if (wave < groups) {
+    auto first_group = [&]() {
+        if (wave < groups) {
 #pragma unroll
-        for (int j = 0; j < NF; ++j)
-            load(bq[j], bs[j], wave, b[j]);
-    }
-    if constexpr (FUSED) {
-        // pieces of 8 elements, of whole groups: at most MX_FUSE_PIECES per thread, all loaded first
-        const int per_row = groups * 64;
-        uint32_t u[MX_FUSE_PIECES][MxPack<T>::WORDS8];
-#pragma unroll
-        for (int i = 0; i < MX_FUSE_PIECES; ++i) {
-            const int f = i * 512 + tid, row = f / per_row;
-            if (row < p.M)
-                mx_load8<T, VEC>((const T *)px.x + (int64_t)row * px.ldx, (f - row * per_row) * 8, px.K, u[i]);
+            for (int j = 0; j < NF; ++j)
+                load(bq[j], bs[j], wave, b[j]);
         }
+    };
+    if constexpr (!FUSED) {
+        first_group();
+    } else {
+        // pieces of 8 elements, of whole groups; VEC: K is a multiple of 8
+        const int per_row = groups * 64;
+        uint32_t u[PIECES][MxPack<T>::WORDS8];
 #pragma unroll
-        for (int i = 0; i < MX_FUSE_PIECES; ++i) {
+        for (int i = 0; i < PIECES; ++i) {
+            const int f = i * 512 + tid, row = f / per_row, k0 = (f - row * per_row) * 8;
+            const T *x = (const T *)px.x + (int64_t)min(row, p.M - 1) * px.ldx;
+            if constexpr (VEC) {
+                mx_load8<T, true>(x, min(k0, px.K - 8), px.K, u[i]);
+#pragma unroll
+                for (int d = 0; d < MxPack<T>::WORDS8; ++d)
+                    u[i][d] = k0 < px.K ? u[i][d] : 0;
+            } else {
+                mx_load8<T, false>(x, k0, px.K, u[i]);
+            }
+        }
+        first_group();   // (behind the activations: loads return in order)
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
             const int f = i * 512 + tid, row = f / per_row, piece = f - row * per_row, blk = piece >> 2;
-            if (row >= p.M)
-                break;
             uint32_t am = mx_amax8<T>(u[i]);
             am = max(am, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)am, 0xB1, 0xF, 0xF, false));
             am = max(am, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)am, 0x4E, 0xF, 0xF, false));
-            const uint32_t sc = mx_scale_of(am);
-            *reinterpret_cast<uint32_t *>(codes + ((((size_t)blk << px.rlog) + ((row ^ blk) & rmask)) * 16 + (piece & 3) * 4)) =
-                mx_pack8<T>(u[i], sc);
-            // block 16 g + 4 s + quarter: byte s of its word
-            if ((piece & 3) == 0)
-                scales[(((size_t)((blk >> 4) * 4 + (blk & 3)) << px.rlog) + row) * 4 + ((blk >> 2) & 3)] = (uint8_t)sc;
+            const uint32_t sc = mx_scale_of(am), w = mx_pack8<T>(u[i], sc);
+            if (row < p.M) {
+                *reinterpret_cast<uint32_t *>(codes + ((((size_t)blk << px.rlog) + ((row ^ blk) & rmask)) * 16 + (piece & 3) * 4)) = w;
+                // block 16 g + 4 s + quarter: byte s of its word
+                if ((piece & 3) == 0)
+                    scales[(((size_t)((blk >> 4) * 4 + (blk & 3)) << px.rlog) + row) * 4 + ((blk >> 2) & 3)] = (uint8_t)sc;
+            }
         }
         __syncthreads();
     }
@@ -489,8 +496,12 @@ __global__ __launch_bounds__(512) void mx_skinny_kernel(MxGemm p, MxSkinnyX px) 
             sa[0] = *reinterpret_cast<const int *>(scales + (((size_t)(4 * g + q) << px.rlog) + (r & rmask)) * 4);
         } else {
 #pragma unroll
-            for (int i = 0; i < MF; ++i)
+            for (int i = 0; i < MF; ++i) {
                 sa[i] = mx_pick_scales(a[i].s, q, left);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    a[i].v[s] = 4 * s + q < left ? a[i].v[s] : mx_i32x4{0, 0, 0, 0};
+            }
         }
         int sb[NF];
 #pragma unroll
@@ -619,13 +630,13 @@ static void join(const float *part, int64_t ldp, int ks, const MxGemm &p, hipStr
 
 // 32 columns per workgroup once that still gives every CU one: the activations are
 // then read, and in the fused form quantised, half as often.
-template <typename T, int MF, bool FUSED, bool VEC>
+template <typename T, int MF, int PIECES, bool VEC>
 static void skinny_one(const MxGemm &p, const MxSkinnyX &px, int cus, hipStream_t stream) {
-    const unsigned fused = FUSED ? mx_fused_bytes(p.nb, px.rlog) : 0;
+    const unsigned fused = PIECES > 0 ? mx_fused_bytes(p.nb, px.rlog) : 0;
     if (p.N >= 32 * cus)
-        hipLaunchKernelGGL((mx_skinny_kernel<T, MF, 2, FUSED, VEC>), dim3((p.N + 31) / 32), dim3(512), MF * 16384 + fused, stream, p, px);
+        hipLaunchKernelGGL((mx_skinny_kernel<T, MF, 2, PIECES, VEC>), dim3((p.N + 31) / 32), dim3(512), MF * 16384 + fused, stream, p, px);
     else
-        hipLaunchKernelGGL((mx_skinny_kernel<T, MF, 1, FUSED, VEC>), dim3((p.N + 15) / 16), dim3(512), MF * 8192 + fused, stream, p, px);
+        hipLaunchKernelGGL((mx_skinny_kernel<T, MF, 1, PIECES, VEC>), dim3((p.N + 15) / 16), dim3(512), MF * 8192 + fused, stream, p, px);
 }
 
 template <typename T>
@@ -636,11 +647,11 @@ static hipError_t gemm_type(const MxGemm &p, const MxPlan &plan, float *partial,
     } else if (plan.kind == MX_SKINNY) {
         const MxSkinnyX px = {};
         if (plan.cfg == 1)
-            skinny_one<T, 1, false, true>(p, px, cus, stream);
+            skinny_one<T, 1, 0, true>(p, px, cus, stream);
         else if (plan.cfg == 2)
-            skinny_one<T, 2, false, true>(p, px, cus, stream);
+            skinny_one<T, 2, 0, true>(p, px, cus, stream);
         else
-            skinny_one<T, 4, false, true>(p, px, cus, stream);
+            skinny_one<T, 4, 0, true>(p, px, cus, stream);
     } else if (plan.ks > 1) {
         MxGemm s = p;
         s.c = partial;
@@ -667,11 +678,13 @@ hipError_t launch_mx_gemm(int type, const MxGemm &p, const MxPlan &plan, float *
 
 template <typename T>
 static hipError_t gemm_x_type(const MxGemm &p, const MxSkinnyX &px, int cus, hipStream_t stream) {
-    const bool vec = (reinterpret_cast<uintptr_t>(px.x) & 15) == 0 && (px.ldx * sizeof(T)) % 16 == 0;
-    if (vec)
-        skinny_one<T, 1, true, true>(p, px, cus, stream);
+    const bool vec = (reinterpret_cast<uintptr_t>(px.x) & 15) == 0 && (px.ldx * sizeof(T)) % 16 == 0 && px.K % 8 == 0;
+    if (!vec)
+        skinny_one<T, 1, MX_FUSE_PIECES, false>(p, px, cus, stream);
+    else if (p.M * ((p.nb + 15) / 16) * 64 <= 512)
+        skinny_one<T, 1, 1, true>(p, px, cus, stream);
     else
-        skinny_one<T, 1, true, false>(p, px, cus, stream);
+        skinny_one<T, 1, MX_FUSE_PIECES, true>(p, px, cus, stream);
     return hipGetLastError();
 }
 

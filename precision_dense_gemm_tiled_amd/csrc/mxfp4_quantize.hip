@@ -19,28 +19,52 @@
 
 namespace mpg {
 
+// Threads of a workgroup over (rows, pieces of 8 elements): 2^tlog of the 256 side by
+// side along a row. A thread takes 4 rows, all loaded before the first is worked on, where
+// that leaves 8 workgroups per CU, else one. (One piece per thread found by a 64-bit
+// division: 12.3 us for the values of 4096 x 4096 in bf16, this 8.0.)
+struct MxSpread {
+    int tlog;
+    bool four;
+    dim3 grid;
+    MxSpread(int64_t M, int64_t pieces) {
+        for (tlog = 2; tlog < 8 && (1 << tlog) < pieces; ++tlog)
+            ;
+        const int64_t across = (pieces + (1 << tlog) - 1) >> tlog, per = 256 >> tlog;
+        four = (M + per * 4 - 1) / (per * 4) * across >= 2048;
+        const int64_t rows = four ? per * 4 : per;
+        grid = dim3((unsigned)((M + rows - 1) / rows), (unsigned)across);
+    }
+};
+
 // Rows only: a lane owns 8 consecutive elements (one 16-byte load where the
 // rows are 16-byte aligned and the type has 2 bytes), a block is 4 lanes, whose
 // maximum is taken with two DPP moves; each lane stores its 8 codes as one
-// word, the block's first lane the scale. Grid-stride over (row, 8 elements).
-template <typename T, bool VEC>
-__global__ __launch_bounds__(256) void mx_quantize_rows_kernel(MxQuantize p, int lanes_per_row, int64_t total) {
-    for (int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x; f < total; f += (int64_t)gridDim.x * 256) {
-        const int row = (int)(f / lanes_per_row);
-        const int k0 = (int)(f - (int64_t)row * lanes_per_row) * 8;
-        const T *x = (const T *)p.x + (int64_t)row * p.ldx;
-        uint32_t u[MxPack<T>::WORDS8];
-        mx_load8<T, VEC>(x, k0, p.K, u);
-        uint32_t am = mx_amax8<T>(u);
-        // the four lanes of a block are in one DPP quad (lanes_per_row % 4 == 0
-        // and 256 % 4 == 0) and take part together
+// word, the block's first lane the scale.
+template <typename T, bool VEC, int ROWS>
+__global__ __launch_bounds__(256) void mx_quantize_rows_kernel(MxQuantize p, int tlog, int pieces) {
+    const int piece = (int)(blockIdx.y << tlog) + (threadIdx.x & ((1 << tlog) - 1)), k0 = piece * 8;
+    const int step = 256 >> tlog, row0 = (int)blockIdx.x * step * ROWS + (threadIdx.x >> tlog);
+    if (piece >= pieces)   // (whole blocks: pieces is a multiple of 4)
+        return;
+    uint32_t u[ROWS][MxPack<T>::WORDS8];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+        if (row0 + i * step < p.M)
+            mx_load8<T, VEC>((const T *)p.x + (int64_t)(row0 + i * step) * p.ldx, k0, p.K, u[i]);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int row = row0 + i * step;
+        if (row >= p.M)
+            return;
+        uint32_t am = mx_amax8<T>(u[i]);
+        // the four lanes of a block are in one DPP quad and take part together
         am = max(am, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)am, 0xB1, 0xF, 0xF, false));
         am = max(am, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)am, 0x4E, 0xF, 0xF, false));
         const uint32_t b = mx_scale_of(am);
-        const uint32_t w = mx_pack8<T>(u, b);
-        *reinterpret_cast<uint32_t *>(p.q + (int64_t)row * p.ldq + k0 / 2) = w;
+        *reinterpret_cast<uint32_t *>(p.q + (int64_t)row * p.ldq + piece * 4) = mx_pack8<T>(u[i], b);
         if ((threadIdx.x & 3) == 0)
-            p.s[(int64_t)row * p.lds + k0 / 32] = (uint8_t)b;
+            p.s[(int64_t)row * p.lds + piece / 4] = (uint8_t)b;
     }
 }
 
@@ -136,29 +160,41 @@ __global__ __launch_bounds__(256) void mx_quantize_both_kernel(MxQuantize p, int
     }
 }
 
-// A lane turns 8 codes (one word) into 8 values.
-template <typename T, bool VEC>
-__global__ __launch_bounds__(256) void mx_dequantize_kernel(MxDequantize p, int lanes_per_row, int64_t total) {
-    for (int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x; f < total; f += (int64_t)gridDim.x * 256) {
-        const int row = (int)(f / lanes_per_row);
-        const int k0 = (int)(f - (int64_t)row * lanes_per_row) * 8;
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(p.q + (int64_t)row * p.ldq + k0 / 2);
-        const uint32_t b = p.s[(int64_t)row * p.lds + k0 / 32];
-        const float s = __uint_as_float(b ? b << 23 : 0x00400000u);   // 2^(b - 127); b = 255: made NaN below
-        T *y = (T *)p.y + (int64_t)row * p.ldy;
-        T v[8];
+// A lane turns 8 codes (one word) into 8 values; threads as for the rows above.
+template <typename T, bool VEC, int ROWS>
+__global__ __launch_bounds__(256) void mx_dequantize_kernel(MxDequantize p, int tlog, int pieces) {
+    const int piece = (int)(blockIdx.y << tlog) + (threadIdx.x & ((1 << tlog) - 1)), k0 = piece * 8;
+    const int step = 256 >> tlog, row0 = (int)blockIdx.x * step * ROWS + (threadIdx.x >> tlog);
+    if (piece >= pieces)
+        return;
+    uint32_t w[ROWS], b[ROWS];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = (T)mx_value((w >> (4 * i)) & 15, s, b);
+    for (int i = 0; i < ROWS; ++i) {
+        const int row = row0 + i * step;
+        w[i] = row < p.M ? *reinterpret_cast<const uint32_t *>(p.q + (int64_t)row * p.ldq + piece * 4) : 0;
+        b[i] = row < p.M ? p.s[(int64_t)row * p.lds + piece / 4] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int row = row0 + i * step;
+        if (row >= p.M)
+            return;
+        T *y = (T *)p.y + (int64_t)row * p.ldy;
+        uint32_t v[MxPack<T>::WORDS8];
+        mx_unpack8<T>(w[i], b[i], v);
         if (VEC && k0 + 8 <= p.K) {
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-                *reinterpret_cast<u32x4 *>((uint8_t *)(y + k0) + 16 * i) = reinterpret_cast<const u32x4 *>(v)[i];
+            for (int d = 0; d < MxPack<T>::WORDS8; d += 4)
+                *reinterpret_cast<u32x4 *>((uint32_t *)(y + k0) + d) = u32x4{v[d], v[d + 1], v[d + 2], v[d + 3]};
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (k0 + i < p.K)
-                    y[k0 + i] = v[i];
+            for (int d = 0; d < 8; ++d)
+                if (k0 + d < p.K) {
+                    if constexpr (sizeof(T) == 4)
+                        reinterpret_cast<uint32_t *>(y)[k0 + d] = v[d];
+                    else
+                        reinterpret_cast<uint16_t *>(y)[k0 + d] = (uint16_t)(v[d / 2] >> (16 * (d & 1)));
+                }
         }
     }
 }
@@ -167,14 +203,16 @@ template <typename T>
 static hipError_t quantize_type(const MxQuantize &p, hipStream_t stream) {
     const bool vec = (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && (p.ldx * sizeof(T)) % 16 == 0;
     if (!p.qt) {
-        const int lanes = (p.K + 31) / 32 * 4;
-        const int64_t total = (int64_t)p.M * lanes;
-        const int64_t blocks = (total + 255) / 256;
-        const dim3 grid((unsigned)(blocks < 16384 ? blocks : 16384));
-        if (vec)
-            hipLaunchKernelGGL((mx_quantize_rows_kernel<T, true>), grid, dim3(256), 0, stream, p, lanes, total);
+        const int pieces = (p.K + 31) / 32 * 4;
+        const MxSpread at(p.M, pieces);
+        if (vec && at.four)
+            hipLaunchKernelGGL((mx_quantize_rows_kernel<T, true, 4>), at.grid, dim3(256), 0, stream, p, at.tlog, pieces);
+        else if (vec)
+            hipLaunchKernelGGL((mx_quantize_rows_kernel<T, true, 1>), at.grid, dim3(256), 0, stream, p, at.tlog, pieces);
+        else if (at.four)
+            hipLaunchKernelGGL((mx_quantize_rows_kernel<T, false, 4>), at.grid, dim3(256), 0, stream, p, at.tlog, pieces);
         else
-            hipLaunchKernelGGL((mx_quantize_rows_kernel<T, false>), grid, dim3(256), 0, stream, p, lanes, total);
+            hipLaunchKernelGGL((mx_quantize_rows_kernel<T, false, 1>), at.grid, dim3(256), 0, stream, p, at.tlog, pieces);
         return hipGetLastError();
     }
     const int tiles_k = (p.K + 127) / 128;
@@ -207,14 +245,16 @@ hipError_t launch_mx_quantize(int type, const MxQuantize &p, hipStream_t stream)
 template <typename T>
 static hipError_t dequantize_type(const MxDequantize &p, hipStream_t stream) {
     const bool vec = (reinterpret_cast<uintptr_t>(p.y) & 15) == 0 && (p.ldy * sizeof(T)) % 16 == 0;
-    const int lanes = (p.K + 7) / 8;
-    const int64_t total = (int64_t)p.M * lanes;
-    const int64_t blocks = (total + 255) / 256;
-    const dim3 grid((unsigned)(blocks < 16384 ? blocks : 16384));
-    if (vec)
-        hipLaunchKernelGGL((mx_dequantize_kernel<T, true>), grid, dim3(256), 0, stream, p, lanes, total);
+    const int pieces = (p.K + 7) / 8;
+    const MxSpread at(p.M, pieces);
+    if (vec && at.four)
+        hipLaunchKernelGGL((mx_dequantize_kernel<T, true, 4>), at.grid, dim3(256), 0, stream, p, at.tlog, pieces);
+    else if (vec)
+        hipLaunchKernelGGL((mx_dequantize_kernel<T, true, 1>), at.grid, dim3(256), 0, stream, p, at.tlog, pieces);
+    else if (at.four)
+        hipLaunchKernelGGL((mx_dequantize_kernel<T, false, 4>), at.grid, dim3(256), 0, stream, p, at.tlog, pieces);
     else
-        hipLaunchKernelGGL((mx_dequantize_kernel<T, false>), grid, dim3(256), 0, stream, p, lanes, total);
+        hipLaunchKernelGGL((mx_dequantize_kernel<T, false, 1>), at.grid, dim3(256), 0, stream, p, at.tlog, pieces);
     return hipGetLastError();
 }
 
