@@ -35,7 +35,7 @@ def _torch_flags():
     inc = cpp_extension.include_paths() + ["/opt/rocm/include", sysconfig.get_path("include")]
     comp = ["-w"] + [f for i in inc for f in ("-isystem", i)] \
         + [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1"]
-    link = ["-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu",
+    link = ["-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip",
             "-ltorch_python", "-L", HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
     return comp, link
 

@@ -13,6 +13,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/hip/HIPStream.h>
 
@@ -121,8 +122,9 @@ const void *bias_of(PyObject *o, int64_t n, at::ScalarType type, const at::Devic
     return b.data_ptr();
 }
 
+// (torch.empty without its way through the dispatcher)
 at::Tensor empty(at::IntArrayRef size, at::ScalarType type, const at::Device &dev) {
-    return at::empty(size, at::TensorOptions().dtype(type).device(dev));
+    return at::Tensor(at::detail::empty_cuda(size, type, dev, std::nullopt));
 }
 
 // The result (new, or the caller's) and its row stride.
@@ -138,13 +140,15 @@ at::Tensor result(PyObject *out, int64_t rows, int64_t cols, at::ScalarType type
     return t;
 }
 
-// New codes and scales; the scale rows are padded to 16 bytes.
+// New codes and scales, in one allocation; the scale rows are padded to 16 bytes.
 struct NewHeld {
     at::Tensor q, s;
     NewHeld(int64_t rows, int64_t k, const at::Device &dev) {
         const int64_t nb = blocks_of(k), lds = (nb + 15) / 16 * 16;
-        q = empty({rows, 16 * nb}, at::kByte, dev);
-        s = empty({rows, lds}, at::kByte, dev);
+        q = empty({rows * (16 * nb + lds)}, at::kByte, dev);
+        s = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(q.storage()), q.key_set(), q.dtype());
+        q.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef{rows, 16 * nb}, at::IntArrayRef{16 * nb, 1});
+        s.unsafeGetTensorImpl()->set_storage_offset(rows * 16 * nb);
         s.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef{rows, nb}, at::IntArrayRef{lds, 1});
     }
 };
