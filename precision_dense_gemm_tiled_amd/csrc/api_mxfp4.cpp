@@ -293,20 +293,18 @@ mpgemm_status_t mpgemm_run_mxfp4_backward(mpgemm_handle_t h, int64_t M, int64_t 
         if (mpg::launch_mx_quantize(type, z, s) != hipSuccess)
             return MPGEMM_ERR_HIP;
     }
-    if (want_x) {
-        const mpg::MxPlan plan = mpg::plan_mx(M, K, blocks_of(N), h->cu_count);
-        const mpg::MxGemm p =
-            product(M, K, N, rq, r.ldq, rq + r.q_bytes, r.lds, WT, ldwt, SWT, ldswt, nullptr, dX, lddx);
-        if (mpg::launch_mx_gemm(type, p, plan, partial, s) != hipSuccess)
-            return MPGEMM_ERR_HIP;
-    }
-    if (want_w) {
-        const mpg::MxPlan plan = mpg::plan_mx(N, K, blocks_of(M), h->cu_count);
-        const mpg::MxGemm p =
-            product(N, K, M, cq, c.ldq, cq + c.q_bytes, c.lds, XT, ldxt, SXT, ldsxt, nullptr, dW, lddw);
-        if (mpg::launch_mx_gemm(MPGEMM_TYPE_F32, p, plan, partial, s) != hipSuccess)
-            return MPGEMM_ERR_HIP;
-    }
+    const mpg::MxPlan plan_x = mpg::plan_mx(M, K, blocks_of(N), h->cu_count);
+    const mpg::MxPlan plan_w = mpg::plan_mx(N, K, blocks_of(M), h->cu_count);
+    const mpg::MxGemm px =
+        product(M, K, N, rq, r.ldq, rq + r.q_bytes, r.lds, WT, ldwt, SWT, ldswt, nullptr, dX, lddx);
+    const mpg::MxGemm pw =
+        product(N, K, M, cq, c.ldq, cq + c.q_bytes, c.lds, XT, ldxt, SXT, ldsxt, nullptr, dW, lddw);
+    if (want_x && want_w && mpg::mx_pairs(plan_x, plan_w))
+        return status_of(mpg::launch_mx_pair(type, px, pw, h->cu_count, s));
+    if (want_x && mpg::launch_mx_gemm(type, px, plan_x, partial, s) != hipSuccess)
+        return MPGEMM_ERR_HIP;
+    if (want_w && mpg::launch_mx_gemm(MPGEMM_TYPE_F32, pw, plan_w, partial, s) != hipSuccess)
+        return MPGEMM_ERR_HIP;
     return MPGEMM_OK;
 }
 

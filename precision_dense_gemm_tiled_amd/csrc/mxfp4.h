@@ -60,6 +60,9 @@ MxPlan plan_mx(int64_t M, int64_t N, int64_t nb, int cu_count);
 // Whether the product quantises the activations itself.
 bool mx_fuses(const MxPlan &plan, int64_t M, int64_t nb);
 hipError_t launch_mx_gemm(int type, const MxGemm &p, const MxPlan &plan, float *partial, hipStream_t stream);
+// Two products in one launch, where mx_pairs allows it: p in `type`, q in fp32.
+bool mx_pairs(const MxPlan &p, const MxPlan &q);
+hipError_t launch_mx_pair(int type, const MxGemm &p, const MxGemm &q, int cus, hipStream_t stream);
 hipError_t launch_mx_gemm_x(int type, const MxGemm &p, const MxSkinnyX &x, const MxPlan &plan, hipStream_t stream);
 
 // Newton-Schulz orthogonalisation (see the public header).
