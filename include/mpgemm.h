@@ -358,9 +358,15 @@ int64_t mpgemm_run_mxfp4_backward_workspace(int64_t M, int64_t N, int64_t K, int
  * then `steps` times X <- a X + (b A + c A A) X with A = X X^T (X^T in the
  * place of X where M > N), written to Y (`type`, ldy, stridey; Y may be G
  * itself). coeffs: host pointer to a, b, c. Every factor of a product is held
- * as a sum of two bf16 values (16 significant bits) and products are summed in
- * fp32; the result is rounded once to `type`. A G of zeros gives zeros
- * (eps > 0). 0 <= steps <= 100; M, N <= 65536; batch <= 65535. */
+ * as a sum of two fp16 values of a scaled matrix (22 significant bits) and
+ * products are summed in fp32; the result is rounded once to `type`. Before that
+ * rounding it is within 1/8 of a half step of `type` of the exact one, relative to
+ * its norm. Where one side is at least 1.25 times the other, the steps are taken in
+ * groups as polynomials of A, and A is formed anew between groups. A G of zeros
+ * gives zeros (eps > 0), one with a NaN or an infinity NaN throughout.
+ * Coefficients have to keep singular values that start in [2^-8, 1] above 2^-14 of
+ * the bound that the polynomial gives for them (all that orthogonalise do; else
+ * MPGEMM_ERR_UNSUPPORTED). 0 <= steps <= 100; M, N <= 65536; batch <= 65535. */
 mpgemm_status_t mpgemm_run_newton_schulz(mpgemm_handle_t h, int64_t batch, int64_t M, int64_t N, int type,
                                          const void *G, int64_t ldg, int64_t strideg, int steps,
                                          const float *coeffs, float eps, void *Y, int64_t ldy,

@@ -336,14 +336,16 @@ mpgemm_status_t mpgemm_run_newton_schulz(mpgemm_handle_t h, int64_t batch, int64
         return MPGEMM_ERR_UNSUPPORTED;
     if (!h)
         return MPGEMM_ERR_INVALID_ARG;
+    const float zero[3] = {0.f, 0.f, 0.f};
+    const float *k = coeffs ? coeffs : zero;
+    if (!mpg::newton_schulz_supported(steps, k[0], k[1], k[2]))
+        return MPGEMM_ERR_UNSUPPORTED;
     st = check_workspace(workspace, workspace_bytes, mpgemm_run_newton_schulz_workspace(batch, M, N));
     if (st != MPGEMM_OK)
         return st;
     DeviceGuard dg(h->device);
     if (!dg.ok)
         return MPGEMM_ERR_HIP;
-    const float zero[3] = {0.f, 0.f, 0.f};
-    const float *k = coeffs ? coeffs : zero;
     const mpg::NewtonSchulz p{G, Y, ldg, strideg, ldy, stridey, (int)batch, (int)M, (int)N, steps, k[0], k[1], k[2], eps, h->cu_count};
     return status_of(mpg::launch_newton_schulz(type, p, workspace, static_cast<hipStream_t>(stream)));
 }

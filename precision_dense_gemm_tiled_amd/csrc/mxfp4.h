@@ -75,6 +75,8 @@ struct NewtonSchulz {
     float a, b, c, eps;
     int cus;   // CUs of the device
 };
+// Whether the kernels' number format holds the iteration with these coefficients.
+bool newton_schulz_supported(int steps, float a, float b, float c);
 int64_t newton_schulz_bytes(int64_t batch, int64_t M, int64_t N);
 hipError_t launch_newton_schulz(int type, const NewtonSchulz &p, void *workspace, hipStream_t stream);
 

@@ -18,8 +18,8 @@
 // the rounding of the sum. The exponents e put each matrix's spectral norm, which
 // bounds its entries, at about 2^13 of fp16's 2^16. They come from bounds that
 // follow from |singular values of X| <= 1 and the polynomial, and are found per
-// matrix on the GPU (ns_norm_kernel), so any coefficients and any |G| against eps
-// work. G itself (fp16 or bf16) needs one part: scaled by a power of two it is an
+// matrix on the GPU (ns_norm_kernel), so any |G| against eps works; polynomials for
+// which the bounds say nothing are refused (newton_schulz_supported). G itself (fp16 or bf16) needs one part: scaled by a power of two it is an
 // fp16 matrix exactly, but for entries below 2^-26 |G|. So the first A is one
 // product and the first W X two.
 //
@@ -28,6 +28,7 @@
 // rank 8 with noise of 1e-2 below it, in groups of three steps; 6e-5 and 1.7e-4 in one
 // group of five. Single fp16 values without the l part: 1.5e-3 and 3e-3.
 #include <cfloat>
+#include <cmath>
 
 #include "mxfp4.h"
 #include "lds_dma.h"
@@ -113,11 +114,11 @@ struct NsGroups {
     }
 };
 
-// Exponent that takes a matrix of spectral norm `bound` to about 2^13.
+// Exponent that takes a matrix of spectral norm `bound` to about 2^13. (Norms below
+// 2^-100, the squares of tiny singular values, count as that: it keeps the factors,
+// 2^(difference of exponents), in fp32's range, and nothing of such an A reaches Q.)
 __device__ __forceinline__ int ns_exponent(float bound) {
-    if (!(bound > 0.f && bound < FLT_MAX))
-        return 0;
-    return 13 - (ilogbf(bound) + 1);
+    return bound < FLT_MAX ? 13 - (ilogbf(fmaxf(bound, 0x1p-100f)) + 1) : 0;
 }
 
 __global__ __launch_bounds__(256) void ns_norm_kernel(const double *sums, int tiles, NewtonSchulz p, NsGroups gr,
@@ -137,12 +138,11 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(const double *sums, int ti
         return;
     const double norm = sqrt((red[0] + red[1]) + (red[2] + red[3]));
     const double inv = 1. / (norm + (double)p.eps);
-    const bool finite = norm < DBL_MAX;   // (false for NaN)
+    const bool finite = norm < DBL_MAX && inv < DBL_MAX;   // (false for NaN, and for 0 / 0)
     const int ex0 = finite && norm > 0. ? min(12 - ilogb(norm), 126) : 0;
     if (lane == 0) {
         head[2 * blockIdx.x] = finite ? (float)ldexp(1., ex0) : __builtin_nanf("");
-        // (finite where eps > 0, so that zeros stay zeros)
-        head[2 * blockIdx.x + 1] = (float)(p.eps > 0.f ? fmin(inv, (double)FLT_MAX) : inv);
+        head[2 * blockIdx.x + 1] = (float)fmin(inv, (double)FLT_MAX);
     }
     // The singular values x of X lie in [0, r]. Lane t looks at four x of [0, r]: the
     // largest |Q|, |T| = |x^2 Q| and next r = |x Q|. The factors are products of
@@ -178,7 +178,9 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(const double *sums, int ti
             const int e = lane == NS_Q_ACC ? eq - 2 * ea : lane == NS_Q_ADD ? eq - ea : lane == NS_Q_ONE ? eq
                           : lane == NS_T ? et - eq - ea : lane == NS_A ? ea2 - eq - et : lane == NS_W ? ew2 - eq - ew
                           : lane == NS_GRAM ? ea : ex - ew2;
-            factors[((int64_t)blockIdx.x * p.steps + k) * NS_FACTORS + lane] = (float)(base * two(e));
+            // (finite, so that zeros stay zeros)
+            factors[((int64_t)blockIdx.x * p.steps + k) * NS_FACTORS + lane] =
+                (float)fmin(fmax(base * two(e), -(double)FLT_MAX), (double)FLT_MAX);
         }
         ew = ew2;
         if (last)
@@ -436,7 +438,10 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
     // lane, stored along rows), then columns (stored into the transpose).
     constexpr int LPR = WT / 8, RPP = 64 / LPR, PASSES = WT / RPP;   // lanes per row, rows per pass
     const int rb = row0 + wm0, cb = col0 + wn0;
-    const bool inside = rb < p.M && cb < p.N;   // (whole blocks: the padding is a multiple of WT)
+    // (Whole blocks: the padding is a multiple of WT. Of a symmetric matrix only what is
+    // on or below the diagonal is used, in a block on it too: the results do not depend
+    // on the size of the tiles, and so not on the batch.)
+    const bool inside = rb < p.M && cb < p.N && !(SYM && rb < cb), diagonal = SYM && rb == cb;
     const int lr = lane / LPR, lc = lane % LPR;
     const float *fac = p.factors + z * p.fstride;
     const float kp = fac[job.factor];
@@ -476,8 +481,10 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
         uint32_t *from = w + rl * S::PITCH + lc * 8;
         float v[8];
 #pragma unroll
-        for (int d = 0; d < 8; ++d)
-            v[d] = __uint_as_float(from[d]) * kp;
+        for (int d = 0; d < 8; ++d) {
+            const int c = lc * 8 + d;
+            v[d] = __uint_as_float(diagonal && c > rl ? w[c * S::PITCH + rl] : from[d]) * kp;
+        }
         const int row = rb + rl, col = cb + lc * 8;
         if constexpr (MODE == NS_POLY) {
 #pragma unroll
@@ -509,12 +516,17 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
             uint32_t u[8];
 #pragma unroll
             for (int d = 0; d < 8; ++d)
-                from[d] = u[d] = ns_split(v[d]);
+                u[d] = ns_split(v[d]);
+            if (!diagonal) {
+#pragma unroll
+                for (int d = 0; d < 8; ++d)
+                    from[d] = u[d];
+            }
             ns_store8(job.out.p + z * job.out.stride + (int64_t)row * job.out.ld, col, u);
         }
     }
-    if (MODE == NS_OUT || (SYM && tm == tn))
-        return;   // (the wavefronts of a diagonal tile store all of it along rows)
+    if (MODE == NS_OUT || diagonal)
+        return;
     wave_lds_fence();
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
@@ -577,6 +589,32 @@ int group_length(int type, float a) {
 }
 
 }  // namespace
+
+// The exponents follow a bound r of X's largest singular value, r <- max |x Q(x)| over
+// [0, r] from 1 on, while the value itself may start as small as 1 / sqrt(m) >= 2^-8.
+// fp16's h + l have 2^-37 of r; the polynomial must keep whatever starts in [2^-8, 1]
+// above 2^-14 r, which leaves them 22 bits. (a, b, c) that orthogonalise do. Powers
+// (a = 0) and polynomials that grow with every step do not: r and the matrix part by
+// the third or fifth power of what they were apart, at every step.
+bool newton_schulz_supported(int steps, float a, float b, float c) {
+    constexpr int POINTS = 33, GRID = 64;
+    float x[POINTS], r = 1.f;
+    for (int i = 0; i < POINTS; ++i)
+        x[i] = exp2f(-8.f + 0.25f * (float)i);
+    auto next = [&](float v) { return v * (a + v * v * (b + v * v * c)); };
+    for (int k = 0; k < steps; ++k) {
+        float top = 0.f;
+        for (int i = 1; i <= GRID; ++i)
+            top = fmaxf(top, fabsf(next(r * (float)i / GRID)));
+        for (int i = 0; i < POINTS; ++i) {
+            x[i] = next(x[i]);
+            if (!(fabsf(x[i]) >= 0x1p-14f * top) || !(top < FLT_MAX))
+                return false;
+        }
+        r = top;
+    }
+    return true;
+}
 
 int64_t newton_schulz_bytes(int64_t batch, int64_t M, int64_t N) {
     if (batch == 0 || M == 0 || N == 0)
