@@ -36,7 +36,7 @@
 namespace mpg {
 
 typedef int ns_i32x4 __attribute__((ext_vector_type(4)));
-typedef float ns_f32x16 __attribute__((ext_vector_type(16)));
+typedef float ns_f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 ns_f16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t ns_u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t ns_u32x4 __attribute__((ext_vector_type(4)));
@@ -268,28 +268,24 @@ enum { NS_SYM, NS_POLY, NS_X, NS_OUT };
 
 // PA, PB: parts of the operands. C tile of 2 WT x 2 WT per workgroup, four
 // wavefronts of WT x WT, stages of KS of K in an LDS ring of NS slots. 16-byte chunk c
-// of LDS row r sits at c ^ swz(r), which keeps the fragment reads free of bank
-// conflicts.
+// of LDS row r sits at c ^ swz(r), which keeps the fragment reads (a chunk column over
+// 16 rows) free of bank conflicts.
 template <int PA, int PB, int WT, int KS, int NS>
 struct NsTile {
-    static constexpr int BT = 2 * WT, TB = WT / 32;
+    static constexpr int BT = 2 * WT, TB = WT / 16, STEPS = KS / 32;
     static constexpr int RBA = 2 * PA * KS, RBB = 2 * PB * KS;        // bytes of a row and stage
     static constexpr int CA = RBA / 16, CB = RBB / 16;                // chunks
     static constexpr int RSA = 256 / CA, RSB = 256 / CB;              // rows of a round of loads
-    static constexpr int RA = BT / RSA, RB = BT / RSB, NL = RA + RB;  // rounds
-    static constexpr int A_BYTES = BT * RBA, STAGE = A_BYTES + BT * RBB;
+    // (a last round past the tile's rows loads rows that nobody reads)
+    static constexpr int RA = (BT + RSA - 1) / RSA, RB = (BT + RSB - 1) / RSB, NL = RA + RB;
+    static constexpr int A_BYTES = RA * RSA * RBA, STAGE = A_BYTES + RB * RSB * RBB;
     static constexpr int PITCH = WT + 1, EPI = 4 * WT * PITCH * 4;
     static constexpr int LDS = NS * STAGE > EPI ? NS * STAGE : EPI;
-    static_assert(LDS <= 160 * 1024 && NS >= 2 && (NS - 2) * NL < 64, "ring");
+    static_assert(LDS <= 160 * 1024 && NS >= 2 && (NS - 1) * NL < 64, "ring");
 
     template <int CHUNKS>
     static __device__ __forceinline__ int swz(int row) {
         return CHUNKS == 4 ? ((row >> 1) & 3) ^ ((row >> 3) & 1) : (row & 7) ^ ((row >> 3) & 1);
-    }
-    // chunk of step s (16 of K), half q of the lanes, part l
-    template <int PARTS>
-    static __device__ __forceinline__ int chunk(int s, int q, int l) {
-        return PARTS == 1 ? 2 * s + q : 8 * (s / 2) + 4 * l + 2 * (s % 2) + q;
     }
 };
 
@@ -368,96 +364,115 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
     };
 
     const int wm0 = (wave >> 1) * WT, wn0 = (wave & 1) * WT;
-    ns_f32x16 acc[S::TB][S::TB];
+    constexpr int TB = S::TB;
+    ns_f32x4 acc[TB][TB];
 #pragma unroll
-    for (int i = 0; i < S::TB; ++i)
+    for (int i = 0; i < TB; ++i)
 #pragma unroll
-        for (int j = 0; j < S::TB; ++j)
-            acc[i][j] = ns_f32x16{};
-    typedef ns_i32x4 Frags[PA + PB][S::TB];   // h and l of A, of B
-    auto read = [&](int e, int s, Frags &f) {
+        for (int j = 0; j < TB; ++j)
+            acc[i][j] = ns_f32x4{};
+    // A stage's fragments: lane l has row l % 16 of a block and the 8 of K of quarter
+    // l / 16 of a step.
+    struct Frags {
+        ns_i32x4 a[S::STEPS][PA][TB], b[S::STEPS][PB][TB];
+    };
+    auto read = [&](int e, Frags &f) {
         const uint8_t *st = smem + (e % NS) * S::STAGE;
+        const int q = lane >> 4, r = lane & 15;
 #pragma unroll
-        for (int k = 0; k < S::TB; ++k) {
-            const int ra = wm0 + k * 32 + (lane & 31), rb = wn0 + k * 32 + (lane & 31);
+        for (int s = 0; s < S::STEPS; ++s) {
 #pragma unroll
-            for (int l = 0; l < PA; ++l)
-                f[l][k] = *reinterpret_cast<const ns_i32x4 *>(
-                    st + ra * S::RBA + ((S::template chunk<PA>(s, lane >> 5, l) ^ S::template swz<S::CA>(ra)) * 16));
+            for (int k = 0; k < TB; ++k) {
+                const int ra = wm0 + k * 16 + r;
 #pragma unroll
-            for (int l = 0; l < PB; ++l)
-                f[PA + l][k] = *reinterpret_cast<const ns_i32x4 *>(
-                    st + S::A_BYTES + rb * S::RBB + ((S::template chunk<PB>(s, lane >> 5, l) ^ S::template swz<S::CB>(rb)) * 16));
+                for (int l = 0; l < PA; ++l)
+                    f.a[s][l][k] = *reinterpret_cast<const ns_i32x4 *>(
+                        st + ra * S::RBA + ((((s * PA + l) * 4 + q) ^ S::template swz<S::CA>(ra)) * 16));
+            }
+#pragma unroll
+            for (int k = 0; k < TB; ++k) {
+                const int rb = wn0 + k * 16 + r;
+#pragma unroll
+                for (int l = 0; l < PB; ++l)
+                    f.b[s][l][k] = *reinterpret_cast<const ns_i32x4 *>(
+                        st + S::A_BYTES + rb * S::RBB + ((((s * PB + l) * 4 + q) ^ S::template swz<S::CB>(rb)) * 16));
+            }
         }
     };
-    // products lo ... hi - 1 of a step: l h, h l, h h of each block
-    constexpr int BLOCKS = S::TB * S::TB, TERMS = PA + PB - 1, NMF = BLOCKS * TERMS;
+    // products lo ... hi - 1 of a stage: in each step l h, h l, h h of each block
+    constexpr int BLOCKS = TB * TB, TERMS = PA + PB - 1, NMF = S::STEPS * BLOCKS * TERMS;
     auto mfmas = [&](const Frags &f, int lo, int hi) {
 #pragma unroll
         for (int n = lo; n < hi; ++n) {
-            const int term = n / BLOCKS, i = n % BLOCKS / S::TB, j = n % S::TB;
+            const int s = n / (BLOCKS * TERMS), term = n / BLOCKS % TERMS, i = n % BLOCKS / TB, j = n % TB;
             const bool last = term == TERMS - 1;
-            const int x = !last && PA == 2 && term == 0 ? 1 : 0, y = !last && x == 0 ? PA + 1 : PA;
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(ns_f16x8, f[x][i]),
-                                                               __builtin_bit_cast(ns_f16x8, f[y][j]), acc[i][j], 0, 0, 0);
+            const int x = !last && PA == 2 && term == 0 ? 1 : 0, y = !last && x == 0 ? 1 : 0;
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(ns_f16x8, f.a[s][x][i]),
+                                                               __builtin_bit_cast(ns_f16x8, f.b[s][y][j]), acc[i][j], 0, 0, 0);
         }
     };
 
-    Frags f[2];
+    Frags f0, f1;
 #pragma unroll
-    for (int e = 0; e < NS - 1; ++e)
+    for (int e = 0; e < NS; ++e)
         dma(e);
-    wait_vm_lds<(NS - 2) * S::NL>();
+    wait_vm_lds<(NS - 1) * S::NL>();
     lds_barrier();
-    read(0, 0, f[0]);
-    // Stage e: the loads of stage e + NS - 1 go into the slot that stage e - 1 has
-    // left; each step's fragments are read during the step before; after the first
-    // products of the last step the barrier publishes stage e + 1, whose first
-    // fragments are read under the rest.
-    constexpr int SUB = KS / 16, KA = NMF >= 4 ? NMF / 4 : 1;
-    for (int e = 0; e < KT; ++e) {
+    read(0, f0);
+    // Stage e has its fragments in registers. After the first half of its products the
+    // barrier says that stage e + 1 has landed and that everybody has read stage e: under
+    // the other half the fragments of e + 1 are read, and the loads of stage e + NS go
+    // into e's slot. (No branch in it: the compiler moves products past one.)
+    auto stage = [&](int e, const Frags &f, Frags &next) {
         __builtin_amdgcn_sched_barrier(0);
-        dma(e + NS - 1);
-#pragma unroll
-        for (int s = 0; s < SUB - 1; ++s) {
-            read(e, s + 1, f[(s + 1) & 1]);
-            mfmas(f[s & 1], 0, NMF);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        mfmas(f[(SUB - 1) & 1], 0, KA);
+        mfmas(f, 0, NMF / 2);
         __builtin_amdgcn_sched_barrier(0);
         wait_vm_lds<(NS - 2) * S::NL>();
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        read(e + 1, 0, f[0]);
-        mfmas(f[(SUB - 1) & 1], KA, NMF);
+        read(e + 1, next);
+        dma(e + NS);
+        mfmas(f, NMF / 2, NMF);
         __builtin_amdgcn_sched_barrier(0);
+    };
+    int e = 0;
+    for (; e + 1 < KT; e += 2) {
+        stage(e, f0, f1);
+        stage(e + 1, f1, f0);
     }
+    if (e < KT)
+        stage(e, f0, f1);
 
     // Epilogue through LDS, a WT x WT block per wavefront: rows first (8 columns per
-    // lane, stored along rows), then columns (stored into the transpose).
-    constexpr int LPR = WT / 8, RPP = 64 / LPR, PASSES = WT / RPP;   // lanes per row, rows per pass
+    // lane, stored along rows), then columns (stored into the transpose). Of a symmetric
+    // matrix only what is on or below the diagonal is used, and the rest is its mirror
+    // image: the results do not depend on the size of the tiles, and so not on the
+    // batch. 16 x 16 blocks are below the diagonal (stored both ways), above it (not
+    // stored) or on it (the elements above taken from below, stored along rows).
+    constexpr int LPR = WT / 8, ITEMS = WT * LPR, PASSES = (ITEMS + 63) / 64;
     const int rb = row0 + wm0, cb = col0 + wn0;
-    // (Whole blocks: the padding is a multiple of WT. Of a symmetric matrix only what is
-    // on or below the diagonal is used, in a block on it too: the results do not depend
-    // on the size of the tiles, and so not on the batch.)
-    const bool inside = rb < p.M && cb < p.N && !(SYM && rb < cb), diagonal = SYM && rb == cb;
-    const int lr = lane / LPR, lc = lane % LPR;
+    const bool inside = rb < p.M && cb < p.N && !(SYM && cb >= rb + WT);
     const float *fac = p.factors + z * p.fstride;
     const float kp = fac[job.factor];
     const float kadd = MODE == NS_POLY ? fac[NS_Q_ADD] : 0.f, kone = MODE == NS_POLY ? fac[NS_Q_ONE] : 0.f;
+    auto item = [&](int i, int &r, int &c) {   // row and first column (or the other way round) of a lane's 8 elements
+        const int g = i * 64 + lane;
+        r = g / LPR;
+        c = g % LPR * 8;
+        return ITEMS % 64 == 0 || g < ITEMS;
+    };
     // (all of `add` on its way before the accumulators go through LDS)
     constexpr int ADDS = MODE == NS_POLY ? PASSES : 1;
     ns_u32x4 ah[ADDS], al[ADDS];
     if constexpr (MODE == NS_POLY) {
-        if (inside) {
 #pragma unroll
-            for (int i = 0; i < PASSES; ++i) {
-                const ns_u32x4 *from = reinterpret_cast<const ns_u32x4 *>(
-                    job.add.p + z * job.add.stride + (int64_t)(rb + i * RPP + lr) * job.add.ld + ns_column(cb + lc * 8));
-                ah[i] = from[0];
-                al[i] = from[4];
-            }
+        for (int i = 0; i < PASSES; ++i) {
+            int r, c;
+            item(i, r, c);
+            const ns_u32x4 *from = reinterpret_cast<const ns_u32x4 *>(
+                job.add.p + z * job.add.stride + (int64_t)min(rb + r, p.M - 1) * job.add.ld + ns_column(min(cb + c, p.N - 8)));
+            ah[i] = from[0];
+            al[i] = from[4];
         }
     }
     // (the ring's last loads have landed and every wavefront is past its last read)
@@ -467,25 +482,29 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
         return;
     uint32_t *w = reinterpret_cast<uint32_t *>(smem) + wave * WT * S::PITCH;
 #pragma unroll
-    for (int i = 0; i < S::TB; ++i)
+    for (int i = 0; i < TB; ++i)
 #pragma unroll
-        for (int j = 0; j < S::TB; ++j)
+        for (int j = 0; j < TB; ++j)
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                w[(i * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4) * S::PITCH + j * 32 + (lane & 31)] =
-                    __float_as_uint(acc[i][j][r]);
+            for (int r = 0; r < 4; ++r)
+                w[(i * 16 + 4 * (lane >> 4) + r) * S::PITCH + j * 16 + (lane & 15)] = __float_as_uint(acc[i][j][r]);
     wave_lds_fence();
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-        const int rl = i * RPP + lr;
-        uint32_t *from = w + rl * S::PITCH + lc * 8;
+        int rl, c;
+        if (!item(i, rl, c))
+            continue;
+        uint32_t *from = w + rl * S::PITCH + c;
+        const int row = rb + rl, col = cb + c;
+        if (row >= p.M || col >= p.N)
+            continue;
+        const int over = SYM ? (col & ~15) - (row & ~15) : -1;   // > 0 above the diagonal's blocks, 0 on it
         float v[8];
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
-            const int c = lc * 8 + d;
-            v[d] = __uint_as_float(diagonal && c > rl ? w[c * S::PITCH + rl] : from[d]) * kp;
+            const bool mirror = SYM && over == 0 && col + d > row;
+            v[d] = __uint_as_float(mirror ? w[(col + d - rb) * S::PITCH + row - cb] : from[d]) * kp;
         }
-        const int row = rb + rl, col = cb + lc * 8;
         if constexpr (MODE == NS_POLY) {
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
@@ -517,25 +536,31 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
 #pragma unroll
             for (int d = 0; d < 8; ++d)
                 u[d] = ns_split(v[d]);
-            if (!diagonal) {
+            if (over < 0) {
 #pragma unroll
                 for (int d = 0; d < 8; ++d)
                     from[d] = u[d];
             }
-            ns_store8(job.out.p + z * job.out.stride + (int64_t)row * job.out.ld, col, u);
+            if (over <= 0)
+                ns_store8(job.out.p + z * job.out.stride + (int64_t)row * job.out.ld, col, u);
         }
     }
-    if (MODE == NS_OUT || diagonal)
+    if (MODE == NS_OUT || (SYM && cb >= rb + WT - 16))   // (nothing of the block is below the diagonal)
         return;
     wave_lds_fence();
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-        const int cl = i * RPP + lr;
+        int cl, r;
+        if (!item(i, cl, r))
+            continue;
+        const int row = cb + cl, col = rb + r;   // of the transpose
+        if (row >= p.N || col >= p.M || (SYM && (row & ~15) >= (col & ~15)))
+            continue;
         uint32_t u[8];
 #pragma unroll
         for (int d = 0; d < 8; ++d)
-            u[d] = w[(lc * 8 + d) * S::PITCH + cl];
-        ns_store8(job.outt.p + z * job.outt.stride + (int64_t)(cb + cl) * job.outt.ld, rb + lc * 8, u);
+            u[d] = w[(r + d) * S::PITCH + cl];
+        ns_store8(job.outt.p + z * job.outt.stride + (int64_t)row * job.outt.ld, col, u);
     }
 }
 
@@ -623,29 +648,50 @@ int64_t newton_schulz_bytes(int64_t batch, int64_t M, int64_t N) {
     return (pl.chunk * pl.per + 255) / 256 * 256;
 }
 
+// Tile sizes: us for a stage and for the ends of a workgroup that has a CU for itself
+// (symmetric 2048 x 2048 on 528, 253 and 136 workgroups: 39.4, 34.5 and 48.3 us; 12 of 512 x 512 on
+// 432, 252 and 120: 12.0, 15.5 and 20.5; 2048 x 8192 on 4096, 1892 and 1024: 227, 195 and 167). 32 has the
+// most workgroups, 64 the fewest loads per flop.
+struct NsSize {
+    int wt;
+    double stage, ends;
+};
+static const NsSize kNsSizes[] = {{32, 0.21, 0.3}, {48, 0.40, 3.0}, {64, 0.63, 4.4}};
+
 template <typename T, int MODE, int PA, int PB>
 static void ns_product(NsGemm g, const NewtonSchulz &p, int z0, int cus, hipStream_t stream) {
     constexpr bool sym = MODE == NS_SYM || MODE == NS_POLY;
+    constexpr int KS = PA + PB == 2 ? 64 : 32;
     auto count = [&](int bt) {
         const int64_t tm = (g.M + bt - 1) / bt, tn = (g.N + bt - 1) / bt;
         return sym ? tm * (tm + 1) / 2 : tm * tn;
     };
-    // 128 x 128 tiles load half the bytes per flop of 64 x 64 ones, which finish
-    // sooner where there are few: on 136 CUs (2048 x 2048, symmetric) 39 us against 38
-    // at K = 2048, 128 against 141 at K = 8192; on 192 CUs (12 x 512 x 512) 19 against 16.
-    const int64_t want = sym ? cus / 2 : cus;
-    const bool big = count(128) * g.jobs * g.nz >= want;
-    const int bt = big ? 128 : 64;
-    g.tiles_m = (g.M + bt - 1) / bt;
-    g.tiles = (int)count(bt);
+    int wt = 32;
+    double best = 0;
+    for (const NsSize &z : kNsSizes) {
+        // workgroups per CU, a begun one for half (they run side by side)
+        const double r = (double)(count(2 * z.wt) * g.jobs * g.nz) / cus, rounds = r <= 1 ? 1 : (r + ceil(r)) / 2;
+        const double cost = rounds * (g.K / KS * z.stage + z.ends);
+        if (z.wt == 32 || cost < best) {
+            best = cost;
+            wt = z.wt;
+        }
+    }
+    g.tiles_m = (g.M + 2 * wt - 1) / (2 * wt);
+    g.tiles = (int)count(2 * wt);
     const dim3 grid((unsigned)((int64_t)g.tiles * g.jobs * g.nz));
-    constexpr int KS = PA + PB == 2 ? 64 : 32;
-    if (big && grid.x <= (unsigned)cus)
+    // a deeper ring for workgroups that have their CU for themselves
+    const bool alone = grid.x <= (unsigned)cus;
+    if (wt == 32)
+        hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 32, KS, 2>), grid, dim3(256), 0, stream, g, p, z0);
+    else if (wt == 48 && alone)
+        hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 48, KS, 3>), grid, dim3(256), 0, stream, g, p, z0);
+    else if (wt == 48)
+        hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 48, KS, 2>), grid, dim3(256), 0, stream, g, p, z0);
+    else if (alone)
         hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 64, KS, 4>), grid, dim3(256), 0, stream, g, p, z0);
-    else if (big)
-        hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 64, KS, 2>), grid, dim3(256), 0, stream, g, p, z0);
     else
-        hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 32, KS, 3>), grid, dim3(256), 0, stream, g, p, z0);
+        hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 64, KS, 2>), grid, dim3(256), 0, stream, g, p, z0);
 }
 
 template <typename T, bool VEC>
