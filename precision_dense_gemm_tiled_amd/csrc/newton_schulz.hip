@@ -18,7 +18,7 @@
 // the rounding of the sum. The exponents e put each matrix's spectral norm, which
 // bounds its entries, at about 2^13 of fp16's 2^16. They come from bounds that
 // follow from |singular values of X| <= 1 and the polynomial, and are found per
-// matrix on the GPU (ns_norm_kernel), so any |G| against eps works; polynomials for
+// matrix on the GPU (ns_factors), so any |G| against eps works; polynomials for
 // which the bounds say nothing are refused (newton_schulz_supported). G itself (fp16 or bf16) needs one part: scaled by a power of two it is an
 // fp16 matrix exactly, but for entries below 2^-26 |G|. So the first A is one
 // product and the first W X two.
@@ -73,37 +73,46 @@ __device__ __forceinline__ void ns_load8(const T *row, int c0, int cols, T (&v)[
     }
 }
 
-// Sum of squares of each 64 x 64 tile of G. In 64 bits: bf16 squares leave the
-// range of fp32 at both ends, and the pass is bound by memory.
-template <typename T, bool VEC>
-__global__ __launch_bounds__(256) void ns_square_kernel(NewtonSchulz p, int batch0, double *sums) {
-    __shared__ double red[4];
-    const int tid = threadIdx.x;
-    const T *G = (const T *)p.g + (int64_t)(batch0 + blockIdx.z) * p.strideg;
-    const int r0 = blockIdx.y * 64 + tid / 8, c0 = blockIdx.x * 64 + (tid & 7) * 8;
-    double s = 0.;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (r0 + 32 * i < p.M) {
-            T v[8];
-            ns_load8<T, VEC>(G + (int64_t)(r0 + 32 * i) * p.ldg, c0, p.N, v);
-#pragma unroll
-            for (int d = 0; d < 8; ++d)
-                s += (double)(float)v[d] * (double)(float)v[d];
-        }
+// Sums of squares of G: workgroup b of the gridDim.x of a matrix takes the 64 x 64 tiles
+// b, b + gridDim.x, ... In 64 bits: bf16 squares leave the range of fp32 at both ends,
+// and the pass is bound by memory.
+constexpr int NS_SUMS = 1024;
+
+// Sum over the workgroup's 256 threads, in every thread, in a fixed order.
+__device__ __forceinline__ double ns_block_sum(double s, double *red) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1)
         s += __shfl_xor(s, o);
-    if ((tid & 63) == 0)
-        red[tid >> 6] = s;
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = s;
     __syncthreads();
-    if (tid == 0)
-        sums[((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
+    return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// Per matrix: head[0] = the power of two that G is scaled by (NaN when |G| is not
-// finite, which makes the whole result NaN), head[1] = 1 / (|G| + eps); then for
-// each step the factors of the products' epilogues.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(256) void ns_square_kernel(NewtonSchulz p, int batch0, int across, int tiles, double *sums) {
+    __shared__ double red[4];
+    const int tid = threadIdx.x;
+    const T *G = (const T *)p.g + (int64_t)(batch0 + blockIdx.y) * p.strideg;
+    double s = 0.;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int r0 = t / across * 64 + tid / 8, c0 = t % across * 64 + (tid & 7) * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (r0 + 32 * i < p.M) {
+                T v[8];
+                ns_load8<T, VEC>(G + (int64_t)(r0 + 32 * i) * p.ldg, c0, p.N, v);
+#pragma unroll
+                for (int d = 0; d < 8; ++d)
+                    s += (double)(float)v[d] * (double)(float)v[d];
+            }
+    }
+    s = ns_block_sum(s, red);
+    if (tid == 0)
+        sums[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
+}
+
+// Factors of the products' epilogues, for each step.
 enum { NS_Q_ACC, NS_Q_ADD, NS_Q_ONE, NS_T, NS_A, NS_W, NS_GRAM, NS_APPLY, NS_FACTORS };
 
 struct NsGroups {
@@ -121,35 +130,30 @@ __device__ __forceinline__ int ns_exponent(float bound) {
     return bound < FLT_MAX ? 13 - (ilogbf(fmaxf(bound, 0x1p-100f)) + 1) : 0;
 }
 
-__global__ __launch_bounds__(256) void ns_norm_kernel(const double *sums, int tiles, NewtonSchulz p, NsGroups gr,
-                                                      float *head, float *factors) {
-    __shared__ double red[4];
-    const int tid = threadIdx.x, lane = tid & 63;
-    double s = 0.;
-    for (int i = tid; i < tiles; i += 256)
-        s += sums[(int64_t)blockIdx.x * tiles + i];
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        s += __shfl_xor(s, o);
-    if (lane == 0)
-        red[tid >> 6] = s;
-    __syncthreads();
-    if (tid >= 64)
-        return;
-    const double norm = sqrt((red[0] + red[1]) + (red[2] + red[3]));
-    const double inv = 1. / (norm + (double)p.eps);
-    const bool finite = norm < DBL_MAX && inv < DBL_MAX;   // (false for NaN, and for 0 / 0)
-    const int ex0 = finite && norm > 0. ? min(12 - ilogb(norm), 126) : 0;
-    if (lane == 0) {
-        head[2 * blockIdx.x] = finite ? (float)ldexp(1., ex0) : __builtin_nanf("");
-        head[2 * blockIdx.x + 1] = (float)fmin(inv, (double)FLT_MAX);
+// |G| of a matrix and what follows from it, in every thread.
+struct NsNorm {
+    double norm, inv;   // inv: 1 / (|G| + eps)
+    bool finite;        // false for NaN, and for 0 / 0
+    int ex;             // G is scaled by 2^ex
+    __device__ __forceinline__ NsNorm(const double *sums, int count, float eps, double *red) {
+        double s = 0.;
+        for (int i = threadIdx.x; i < count; i += 256)
+            s += sums[i];
+        norm = sqrt(ns_block_sum(s, red));
+        inv = 1. / (norm + (double)eps);
+        finite = norm < DBL_MAX && inv < DBL_MAX;
+        ex = finite && norm > 0. ? min(12 - ilogb(norm), 126) : 0;
     }
+};
+
+// The factors of every step's products of a matrix, by one wavefront.
+__device__ __forceinline__ void ns_factors(const NewtonSchulz &p, NsGroups gr, const NsNorm &g, int lane, float *factors) {
     // The singular values x of X lie in [0, r]. Lane t looks at four x of [0, r]: the
     // largest |Q|, |T| = |x^2 Q| and next r = |x Q|. The factors are products of
     // powers of two with exponents in the range of a double.
     auto two = [](int e) { return ldexp(1., e); };
-    float r = finite ? (float)fmin(norm * inv, 1.) : 1.f, wb = 1.f;
-    double to_x = inv * two(-ex0);   // stored X -> X
+    float r = g.finite ? (float)fmin(g.norm * g.inv, 1.) : 1.f, wb = 1.f;
+    double to_x = g.inv * two(-g.ex);   // stored X -> X
     int ew = 0;
     for (int k = 0; k < p.steps; ++k) {
         float v[3] = {0.f, 0.f, 0.f};
@@ -179,7 +183,7 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(const double *sums, int ti
                           : lane == NS_T ? et - eq - ea : lane == NS_A ? ea2 - eq - et : lane == NS_W ? ew2 - eq - ew
                           : lane == NS_GRAM ? ea : ex - ew2;
             // (finite, so that zeros stay zeros)
-            factors[((int64_t)blockIdx.x * p.steps + k) * NS_FACTORS + lane] =
+            factors[k * NS_FACTORS + lane] =
                 (float)fmin(fmax(base * two(e), -(double)FLT_MAX), (double)FLT_MAX);
         }
         ew = ew2;
@@ -189,14 +193,22 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(const double *sums, int ti
     }
 }
 
-// G (M x N), scaled, as X (m x n, padded) and X^T. FLIP: G is taller than wide, X = G^T.
+// G (M x N), scaled by a power of two, as X (m x n, padded) and X^T, and the factors (one
+// workgroup per matrix). FLIP: G is taller than wide, X = G^T. Every workgroup sums the
+// sums of squares: a launch less. A |G| that is not finite makes X, and with it the whole
+// result, NaN.
 template <typename T, bool FLIP, bool VEC>
-__global__ __launch_bounds__(256) void ns_load_kernel(NewtonSchulz p, int batch0, const float *head, NsMat X, NsMat XT) {
+__global__ __launch_bounds__(256) void ns_load_kernel(NewtonSchulz p, NsGroups gr, int batch0, const double *sums, int count,
+                                                      float *factors, NsMat X, NsMat XT) {
     __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];
+    __shared__ double red[4];
     const int tid = threadIdx.x;
     const T *G = (const T *)p.g + (int64_t)(batch0 + blockIdx.z) * p.strideg;
     const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-    const float up = head[2 * blockIdx.z];
+    const NsNorm norm(sums + (int64_t)blockIdx.z * count, count, p.eps, red);
+    const float up = norm.finite ? (float)ldexp(1., norm.ex) : __builtin_nanf("");
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid < 64)
+        ns_factors(p, gr, norm, tid, factors + (int64_t)blockIdx.z * p.steps * NS_FACTORS);
     const NsMat own = FLIP ? XT : X, other = FLIP ? X : XT;   // own: rows as G's
     const int g = tid & 7;
 #pragma unroll
@@ -231,15 +243,17 @@ __global__ __launch_bounds__(256) void ns_load_kernel(NewtonSchulz p, int batch0
 
 // Y = G / (|G| + eps) (no steps)
 template <typename T>
-__global__ __launch_bounds__(256) void ns_scale_kernel(NewtonSchulz p, int batch0, const float *head) {
+__global__ __launch_bounds__(256) void ns_scale_kernel(NewtonSchulz p, int batch0, const double *sums, int count) {
+    __shared__ double red[4];
     const int z = batch0 + blockIdx.z;
     const T *G = (const T *)p.g + (int64_t)z * p.strideg;
     T *Y = (T *)p.y + (int64_t)z * p.stridey;
     const int64_t total = (int64_t)p.M * p.N;
-    const float s = head[2 * blockIdx.z] != head[2 * blockIdx.z] ? head[2 * blockIdx.z] : head[2 * blockIdx.z + 1];
+    const NsNorm norm(sums + (int64_t)blockIdx.z * count, count, p.eps, red);
+    const double s = norm.finite ? norm.inv : (double)__builtin_nanf("");
     for (int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x; f < total; f += (int64_t)gridDim.x * 256) {
         const int64_t r = f / p.N, c = f - r * p.N;
-        Y[r * p.ldy + c] = (T)((float)G[r * p.ldg + c] * s);
+        Y[r * p.ldy + c] = (T)(float)((double)(float)G[r * p.ldg + c] * s);
     }
 }
 
@@ -572,7 +586,7 @@ struct NsPlan {
     int64_t mp, np;          // padded sizes
     int64_t per;             // bytes per matrix
     int64_t chunk;           // matrices in one go
-    int64_t tiles;
+    int64_t sums;            // partial sums of squares
 };
 
 constexpr int kMaxSteps = 100;
@@ -584,8 +598,10 @@ NsPlan ns_plan(int64_t batch, int64_t M, int64_t N) {
     const int64_t m = M < N ? M : N, n = M < N ? N : M;
     pl.mp = (m + 63) / 64 * 64;
     pl.np = (n + 63) / 64 * 64;
-    pl.tiles = (pl.mp / 64) * (pl.np / 64);
-    pl.per = 3 * pl.mp * pl.np * 4 + 5 * pl.mp * pl.mp * 4 + pl.tiles * 8 + 8 + kMaxSteps * NS_FACTORS * 4;
+    pl.sums = (pl.mp / 64) * (pl.np / 64);
+    if (pl.sums > NS_SUMS)
+        pl.sums = NS_SUMS;
+    pl.per = 3 * pl.mp * pl.np * 4 + 5 * pl.mp * pl.mp * 4 + pl.sums * 8 + kMaxSteps * NS_FACTORS * 4;
     const int64_t most = (int64_t)4 << 30;
     pl.chunk = most / pl.per;
     if (pl.chunk < 1)
@@ -716,7 +732,8 @@ static hipError_t ns_type(int type, const NewtonSchulz &p, void *workspace, hipS
     const NsMat A = mat(mp, as), Tm = mat(mp, as);
     NsMat Q = mat(mp, as), W = mat(mp, as), W2 = mat(mp, as);
     double *sums = (double *)w;
-    float *head = (float *)(sums + pl.chunk * pl.tiles), *factors = head + 2 * pl.chunk;
+    float *factors = (float *)(sums + pl.chunk * pl.sums);
+    const int across = (p.N + 63) / 64, tiles = across * ((p.M + 63) / 64), count = (int)pl.sums;
 
     // Per step and m^3 flop: L steps in a group cost (3 n / m + 4 L - 3) / L products. For a
     // square matrix that is 4 whatever L is, and single steps need fewer launches
@@ -731,15 +748,14 @@ static hipError_t ns_type(int type, const NewtonSchulz &p, void *workspace, hipS
     for (int64_t b0 = 0; b0 < p.batch; b0 += pl.chunk) {
         const int nz = (int)(p.batch - b0 < pl.chunk ? p.batch - b0 : pl.chunk);
         const int z0 = (int)b0;
-        hipLaunchKernelGGL((ns_square_kernel<T, VEC>), dim3((p.N + 63) / 64, (p.M + 63) / 64, nz), dim3(256), 0, stream, p, z0, sums);
-        hipLaunchKernelGGL(ns_norm_kernel, dim3(nz), dim3(256), 0, stream, sums, (int)pl.tiles, p, gr, head, factors);
+        hipLaunchKernelGGL((ns_square_kernel<T, VEC>), dim3(count, nz), dim3(256), 0, stream, p, z0, across, tiles, sums);
         if (p.steps == 0) {
             const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
-            hipLaunchKernelGGL((ns_scale_kernel<T>), dim3((unsigned)(blocks < 4096 ? blocks : 4096), 1, nz), dim3(256), 0, stream, p, z0, head);
+            hipLaunchKernelGGL((ns_scale_kernel<T>), dim3((unsigned)(blocks < 4096 ? blocks : 4096), 1, nz), dim3(256), 0, stream, p, z0, sums, count);
         } else if (flip) {
-            hipLaunchKernelGGL((ns_load_kernel<T, true, VEC>), dim3(mp / 64, np / 64, nz), dim3(256), 0, stream, p, z0, head, one(X), one(XT));
+            hipLaunchKernelGGL((ns_load_kernel<T, true, VEC>), dim3(mp / 64, np / 64, nz), dim3(256), 0, stream, p, gr, z0, sums, count, factors, one(X), one(XT));
         } else {
-            hipLaunchKernelGGL((ns_load_kernel<T, false, VEC>), dim3(np / 64, mp / 64, nz), dim3(256), 0, stream, p, z0, head, one(X), one(XT));
+            hipLaunchKernelGGL((ns_load_kernel<T, false, VEC>), dim3(np / 64, mp / 64, nz), dim3(256), 0, stream, p, gr, z0, sums, count, factors, one(X), one(XT));
         }
         for (int s = 0; s < p.steps; ++s) {
             const bool first = gr.starts(s), last = s + 1 == p.steps, ends = last || gr.starts(s + 1);
