@@ -1,20 +1,19 @@
 // MXFP4 product C = A B^T + bias on gfx950's scaled matrix instructions.
 //
 // C[m][n] = sum over blocks of 2^(sa - 127 + sb - 127) * (sum of 32 products
-// of e2m1 values). v_mfma_scale_f32_32x32x64_f8f6f4 (and 16x16x128) take one
-// block of 32 codes (16 bytes) and its scale byte per lane for each operand,
-// so the 16-byte chunks of the stored rows are the fragments and the stored
-// e8m0 bytes the scales: nothing is unpacked. Lane l supplies row l % 32 (16)
-// and block l / 32 (16) of a step; which blocks of K make up a step is free,
-// as long as both operands agree. A lane therefore takes four consecutive
-// blocks over four steps, whose scale bytes are one word, the step selecting
-// the byte.
+// of e2m1 values). v_mfma_scale_f32_16x16x128_f8f6f4 takes one block of 32 codes
+// (16 bytes) and its scale byte per lane for each operand, so the 16-byte
+// chunks of the stored rows are the fragments and the stored e8m0 bytes the
+// scales: nothing is unpacked. Lane l supplies row l % 16 and block l / 16 of a
+// step; which blocks of K make up a step is free, as long as both operands
+// agree. The scale bytes of the blocks that a lane takes over several steps are
+// one word, and the step selects the byte.
 //
 // Two kernels:
 //   tile    operands through LDS (compute and L2 bandwidth bound)
 //   skinny  M <= 64: operands straight from memory into the matrix unit's
 //           registers, K over the wavefronts of a workgroup (bound by reading
-//           B once); with M <= 16 the activations may be quantised in it
+//           B once); few activations are quantised in it
 #include "mxfp4.h"
 #include "mxfp4_device.h"
 #include "lds_dma.h"

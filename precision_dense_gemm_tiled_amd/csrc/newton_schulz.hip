@@ -19,16 +19,22 @@
 // bounds its entries, at about 2^13 of fp16's 2^16. They come from bounds that
 // follow from |singular values of X| <= 1 and the polynomial, and are found per
 // matrix on the GPU (ns_factors), so any |G| against eps works; polynomials for
-// which the bounds say nothing are refused (newton_schulz_supported). G itself (fp16 or bf16) needs one part: scaled by a power of two it is an
-// fp16 matrix exactly, but for entries below 2^-26 |G|. So the first A is one
-// product and the first W X two.
+// which the bounds say nothing are refused (newton_schulz_supported). G itself (fp16
+// or bf16) needs one part: scaled by a power of two it is an fp16 matrix exactly, but
+// for entries below 2^-26 |G|. So the first A is one product and the first W X two.
+// Single fp16 values without the l part are not enough: off by 1.5e-3 of the norm on
+// gradients of rank 64 plus noise, 3e-3 on rank 8 with noise of 1e-2 below it (bf16's
+// own rounding: 1.7e-3, fp16's: 2.1e-4; with the l part: nothing next to either).
 //
-// Measured against 64 bits before the output's rounding (rms 1.7e-3 of the norm for
-// bf16, 2.1e-4 for fp16), five steps: 4e-6 on gradients of rank 64 plus noise, 3e-5 on
-// rank 8 with noise of 1e-2 below it, in groups of three steps; 6e-5 and 1.7e-4 in one
-// group of five. Single fp16 values without the l part: 1.5e-3 and 3e-3.
+// Bound by the matrix units' power for large matrices (2048 x 8192, W X: 1.2 to 1.4
+// PFLOP/s of fp16 products; the library's bf16 product reaches 1.4), by the number of
+// tiles for the symmetric products (253 of 96 x 96 at 2048: 0.75), by launches and the
+// way to L2 for small ones (12 x 512 x 512: 12 us a product, 6 of them with no K loop).
+// Therefore a matrix with a side up to 128 takes all steps of a group in one launch
+// (ns_small_kernel), and A = X X^T of a long and narrow X is split along n.
 #include <cfloat>
 #include <cmath>
+#include <initializer_list>
 
 #include "mxfp4.h"
 #include "lds_dma.h"
@@ -273,12 +279,18 @@ struct NsGemm {
     int tiles_m, tiles;
     const float *factors;   // of this step, NS_FACTORS each, `fstride` floats between matrices
     int64_t fstride;
+    // NS_PART: `jobs` slices of K, of `slice` each but the last; slice i of a matrix goes to
+    // part + i M M, `pstride` floats between matrices
+    float *part;
+    int64_t pstride;
+    int slice;
 };
 
 // Results: NS_SYM a symmetric matrix (tiles on and below the diagonal, mirrored),
 // NS_POLY the same with the multiples of `add` and of the identity, NS_X a matrix
-// and its transpose, NS_OUT the caller's Y.
-enum { NS_SYM, NS_POLY, NS_X, NS_OUT };
+// and its transpose, NS_OUT the caller's Y, NS_PART the plain fp32 sums of a slice of K of
+// a symmetric matrix, on and below the diagonal.
+enum { NS_SYM, NS_POLY, NS_X, NS_OUT, NS_PART };
 
 // PA, PB: parts of the operands. C tile of 2 WT x 2 WT per workgroup, four
 // wavefronts of WT x WT, stages of KS of K in an LDS ring of NS slots. 16-byte chunk c
@@ -322,7 +334,7 @@ __device__ __forceinline__ void ns_store8(uint16_t *row, int c0, const uint32_t 
 template <typename T, int MODE, int PA, int PB, int WT, int KS, int NS>
 __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz q, int batch0) {
     typedef NsTile<PA, PB, WT, KS, NS> S;
-    constexpr bool SYM = MODE == NS_SYM || MODE == NS_POLY;
+    constexpr bool SYM = MODE == NS_SYM || MODE == NS_POLY || MODE == NS_PART;
     __shared__ __attribute__((aligned(16))) uint8_t smem[S::LDS];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -336,7 +348,8 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
     const int t = bid % p.tiles, jz = bid / p.tiles;
     const int jn = jz % p.jobs;
     const int64_t z = jz / p.jobs;
-    const NsJob &job = p.job[jn];
+    const NsJob &job = p.job[MODE == NS_PART ? 0 : jn];
+    const int k0 = MODE == NS_PART ? jn * p.slice : 0;
     int tm, tn;
     if (SYM) {   // lower triangle: tile t is (tm, tn), tn <= tm
         tm = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
@@ -359,12 +372,12 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
         const uint16_t *pa = job.a.p + z * job.a.stride, *pb = job.b.p + z * job.b.stride;
 #pragma unroll
         for (int i = 0; i < S::RA; ++i)
-            srca[i] = reinterpret_cast<const uint8_t *>(pa + (int64_t)min(row0 + ra + i * S::RSA, p.M - 1) * job.a.ld) + ca * 16;
+            srca[i] = reinterpret_cast<const uint8_t *>(pa + (int64_t)min(row0 + ra + i * S::RSA, p.M - 1) * job.a.ld + k0 * PA) + ca * 16;
 #pragma unroll
         for (int i = 0; i < S::RB; ++i)
-            srcb[i] = reinterpret_cast<const uint8_t *>(pb + (int64_t)min(col0 + rb + i * S::RSB, p.N - 1) * job.b.ld) + cb * 16;
+            srcb[i] = reinterpret_cast<const uint8_t *>(pb + (int64_t)min(col0 + rb + i * S::RSB, p.N - 1) * job.b.ld + k0 * PB) + cb * 16;
     }
-    const int KT = p.K / KS;
+    const int KT = (MODE == NS_PART ? min(p.K - k0, p.slice) : p.K) / KS;
     // (every call issues NL loads: stages past the last re-read it)
     auto dma = [&](int e) {
         const int kt = min(e, KT - 1);
@@ -467,7 +480,7 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
     const int rb = row0 + wm0, cb = col0 + wn0;
     const bool inside = rb < p.M && cb < p.N && !(SYM && cb >= rb + WT);
     const float *fac = p.factors + z * p.fstride;
-    const float kp = fac[job.factor];
+    const float kp = MODE == NS_PART ? 1.f : fac[job.factor];
     const float kadd = MODE == NS_POLY ? fac[NS_Q_ADD] : 0.f, kone = MODE == NS_POLY ? fac[NS_Q_ONE] : 0.f;
     auto item = [&](int i, int &r, int &c) {   // row and first column (or the other way round) of a lane's 8 elements
         const int g = i * 64 + lane;
@@ -545,6 +558,12 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
                             Y[d] = o[d];
                 }
             }
+        } else if constexpr (MODE == NS_PART) {
+            if (over <= 0) {
+                ns_f32x4 *to = reinterpret_cast<ns_f32x4 *>(p.part + z * p.pstride + ((int64_t)jn * p.M + row) * p.M + col);
+                to[0] = ns_f32x4{v[0], v[1], v[2], v[3]};
+                to[1] = ns_f32x4{v[4], v[5], v[6], v[7]};
+            }
         } else {
             uint32_t u[8];
 #pragma unroll
@@ -559,7 +578,7 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
                 ns_store8(job.out.p + z * job.out.stride + (int64_t)row * job.out.ld, col, u);
         }
     }
-    if (MODE == NS_OUT || (SYM && cb >= rb + WT - 16))   // (nothing of the block is below the diagonal)
+    if (MODE == NS_OUT || MODE == NS_PART || (SYM && cb >= rb + WT - 16))   // (nothing of the block is below the diagonal)
         return;
     wave_lds_fence();
 #pragma unroll
@@ -575,6 +594,220 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
         for (int d = 0; d < 8; ++d)
             u[d] = w[(r + d) * S::PITCH + cl];
         ns_store8(job.outt.p + z * job.outt.stride + (int64_t)row * job.outt.ld, col, u);
+    }
+}
+
+// A = the sum of the slices, in their order, of one 64 x 64 tile on or below the
+// diagonal.
+__global__ __launch_bounds__(256) void ns_join_kernel(NsGemm p) {
+    __shared__ float tile[64][65];
+    const int tid = threadIdx.x, t = blockIdx.x;
+    const int64_t z = blockIdx.y;
+    int tm = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
+    while ((tm + 1) * (tm + 2) / 2 <= t)
+        ++tm;
+    while (tm * (tm + 1) / 2 > t)
+        --tm;
+    const int row0 = tm * 64, col0 = (t - tm * (tm + 1) / 2) * 64;
+    const float k = p.factors[z * p.fstride + NS_GRAM];
+    const float *part = p.part + z * p.pstride;
+    const int64_t size = (int64_t)p.M * p.M;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 16 + tid / 16, c = tid % 16 * 4;
+        ns_f32x4 v = {};
+        if ((col0 + c & ~15) <= (row0 + r & ~15))   // (the others are not there)
+            for (int s = 0; s < p.jobs; ++s)
+                v += *reinterpret_cast<const ns_f32x4 *>(part + s * size + (int64_t)(row0 + r) * p.M + col0 + c);
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            tile[r][c + d] = v[d] * k;
+    }
+    __syncthreads();
+    const NsMat &out = p.job[0].out;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = i * 32 + tid / 8, c = tid % 8 * 8;
+        uint32_t u[8], w[8];
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+            u[d] = ns_split(row0 == col0 && c + d > r ? tile[c + d][r] : tile[r][c + d]);
+            w[d] = ns_split(tile[c + d][r]);
+        }
+        ns_store8(out.p + z * out.stride + (int64_t)(row0 + r) * out.ld, col0 + c, u);
+        if (row0 != col0)
+            ns_store8(out.p + z * out.stride + (int64_t)(col0 + r) * out.ld, row0 + c, w);
+    }
+}
+
+// ------------------------------------------------------------ small matrices
+
+// All steps of a group for matrices of MP x MP, one per workgroup: A comes from the slices
+// of X X^T, A (in turn T) and Q stay in LDS, W in memory, where the apply takes it from.
+// One 64 x 64: 74 -> 45 us, 64 x 4096: 166 -> 65 us, 16 of them 187 -> 83.
+//
+// In LDS a row is 4 MP bytes, 32 h and their 32 l in turn, its 16-byte chunks permuted
+// within 256 bytes by the row (chunk c at c ^ (row % 16)): a chunk column over 16 rows is
+// free of bank conflicts. A lane's four sums are consecutive down a column; all matrices
+// are symmetric, so they are stored along the row of that number.
+struct NsSmall {
+    const float *part;
+    int64_t pstride;
+    int slices, steps;
+    NsMat w[2];             // the result in w[(steps - 1) % 2]
+    const float *factors;   // of the group's first step
+    int64_t fstride;
+};
+
+template <int MP>
+__global__ __launch_bounds__(512) void ns_small_kernel(NsSmall p) {
+    constexpr int ROW = MP * 4, SIZE = MP * ROW, WM = MP / 4, WN = MP / 2, TM = WM / 16, TN = WN / 16;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * SIZE];
+    constexpr int A = 0, Q = SIZE;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t z = blockIdx.x;
+    const float *fac = p.factors + z * p.fstride;
+    // byte of element k (of part l) of a row
+    auto at = [](int row, int k, int l) {
+        return row * ROW + (k / 64) * 256 + ((((k / 32 & 1) * 8 + l * 4 + k % 32 / 8) ^ (row & 15)) * 16) + k % 8 * 2;
+    };
+    {
+        const float *part = p.part + z * p.pstride, k = fac[NS_GRAM];
+        for (int f = tid; f < MP * MP / 4; f += 512) {
+            const int r = f / (MP / 4), c = f % (MP / 4) * 4;
+            if ((c & ~15) > (r & ~15))   // (not there)
+                continue;
+            ns_f32x4 v = {};
+            for (int s = 0; s < p.slices; ++s)
+                v += *reinterpret_cast<const ns_f32x4 *>(part + ((int64_t)s * MP + r) * MP + c);
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                if (c + d <= r) {
+                    const uint32_t u = ns_split(v[d] * k);
+                    *reinterpret_cast<uint16_t *>(smem + A + at(r, c + d, 0)) = (uint16_t)u;
+                    *reinterpret_cast<uint16_t *>(smem + A + at(r, c + d, 1)) = (uint16_t)(u >> 16);
+                    *reinterpret_cast<uint16_t *>(smem + A + at(c + d, r, 0)) = (uint16_t)u;
+                    *reinterpret_cast<uint16_t *>(smem + A + at(c + d, r, 1)) = (uint16_t)(u >> 16);
+                }
+        }
+    }
+    __syncthreads();
+
+    const int m0 = (wave >> 1) * WM, n0 = (wave & 1) * WN, q = lane >> 4, r16 = lane & 15;
+    typedef ns_f32x4 Acc[TM][TN];
+    auto in_lds = [&](int x) {
+        return [=](int row, int k, int l) { return *reinterpret_cast<const ns_i32x4 *>(smem + x + at(row, 32 * k + 8 * q, l)); };
+    };
+    auto in_memory = [&](const NsMat &x) {
+        const uint16_t *from = x.p + z * x.stride;
+        const int64_t ld = x.ld;
+        return [=](int row, int k, int l) { return *reinterpret_cast<const ns_i32x4 *>(from + row * ld + 64 * k + 32 * l + 8 * q); };
+    };
+    // acc = x y^T
+    auto product = [&](auto x, auto y, Acc &acc) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = ns_f32x4{};
+#pragma unroll
+        for (int k = 0; k < MP / 32; ++k) {
+            ns_i32x4 a[2][TM], b[2][TN];
+#pragma unroll
+            for (int l = 0; l < 2; ++l) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    a[l][i] = x(m0 + 16 * i + r16, k, l);
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    b[l][j] = y(n0 + 16 * j + r16, k, l);
+            }
+#pragma unroll
+            for (int term = 0; term < 3; ++term)   // l h, h l, h h
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(ns_f16x8, a[term == 0][i]),
+                                                                           __builtin_bit_cast(ns_f16x8, b[term == 1][j]),
+                                                                           acc[i][j], 0, 0, 0);
+        }
+    };
+    // four split values into row `row` from column c0 (a multiple of 4) on
+    auto pack = [](const float (&v)[4], ns_u32x2 &h, ns_u32x2 &l) {
+        uint32_t u[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            u[d] = ns_split(v[d]);
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+            h[d] = __builtin_amdgcn_perm(u[2 * d + 1], u[2 * d], 0x05040100u);
+            l[d] = __builtin_amdgcn_perm(u[2 * d + 1], u[2 * d], 0x07060302u);
+        }
+    };
+    auto to_lds = [&](int x) {
+        return [=](int row, int c0, ns_u32x2 h, ns_u32x2 l) {
+            *reinterpret_cast<ns_u32x2 *>(smem + x + at(row, c0, 0)) = h;
+            *reinterpret_cast<ns_u32x2 *>(smem + x + at(row, c0, 1)) = l;
+        };
+    };
+    auto to_memory = [&](const NsMat &x) {
+        uint16_t *to = x.p + z * x.stride;
+        const int64_t ld = x.ld;
+        return [=](int row, int c0, ns_u32x2 h, ns_u32x2 l) {
+            *reinterpret_cast<ns_u32x2 *>(to + row * ld + ns_column(c0)) = h;
+            *reinterpret_cast<ns_u32x2 *>(to + row * ld + ns_column(c0) + 32) = l;
+        };
+    };
+    auto store = [&](const Acc &acc, float k, auto to) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int row = n0 + 16 * j + r16, c0 = m0 + 16 * i + 4 * q;
+                const float v[4] = {acc[i][j][0] * k, acc[i][j][1] * k, acc[i][j][2] * k, acc[i][j][3] * k};
+                ns_u32x2 h, l;
+                pack(v, h, l);
+                to(row, c0, h, l);
+            }
+    };
+
+    Acc acc;
+    for (int s = 0; s < p.steps; ++s, fac += NS_FACTORS) {
+        // Q = a I + b A + c A A; the first is W too
+        product(in_lds(A), in_lds(A), acc);
+        const float kadd = fac[NS_Q_ADD], kone = fac[NS_Q_ONE], kacc = fac[NS_Q_ACC];
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int row = n0 + 16 * j + r16, c0 = m0 + 16 * i + 4 * q;
+                const ns_u32x2 h = *reinterpret_cast<const ns_u32x2 *>(smem + A + at(row, c0, 0));
+                const ns_u32x2 l = *reinterpret_cast<const ns_u32x2 *>(smem + A + at(row, c0, 1));
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const float x = ns_f32(h[d / 2] >> (16 * (d & 1)) & 0xFFFF) + ns_f32(l[d / 2] >> (16 * (d & 1)) & 0xFFFF);
+                    acc[i][j][d] = __builtin_fmaf(kadd, x, acc[i][j][d] * kacc) + (row == c0 + d ? kone : 0.f);
+                }
+            }
+        store(acc, 1.f, to_lds(Q));
+        if (s == 0)
+            store(acc, 1.f, to_memory(p.w[0]));
+        __syncthreads();
+        if (s > 0) {   // W <- Q W
+            product(in_lds(Q), in_memory(p.w[(s - 1) & 1]), acc);
+            store(acc, fac[NS_W], to_memory(p.w[s & 1]));
+        }
+        if (s + 1 < p.steps) {
+            product(in_lds(Q), in_lds(A), acc);   // T = Q A in A's place
+            __syncthreads();
+            store(acc, fac[NS_T], to_lds(A));
+            __syncthreads();
+            product(in_lds(Q), in_lds(A), acc);   // A <- Q T
+            __syncthreads();
+            store(acc, fac[NS_A], to_lds(A));
+        }
+        __syncthreads();
     }
 }
 
@@ -738,12 +971,27 @@ static hipError_t ns_type(int type, const NewtonSchulz &p, void *workspace, hipS
     // Per step and m^3 flop: L steps in a group cost (3 n / m + 4 L - 3) / L products. For a
     // square matrix that is 4 whatever L is, and single steps need fewer launches
     // (12 x 512 x 512: 199 against 248 us).
-    const int most = pl.np * 4 >= pl.mp * 5 ? group_length(type, p.a) : 1, groups = (p.steps + most - 1) / most;
+    const bool small = mp <= 128;
+    const int most = small || pl.np * 4 >= pl.mp * 5 ? group_length(type, p.a) : 1, groups = (p.steps + most - 1) / most;
     NsGroups gr = {1, 0};
     if (groups > 0) {
         gr.len = p.steps / groups;
         gr.longer = p.steps % groups;
     }
+
+    // A of few tiles and a long n: slices of n, of 256 at least, as many as give the tiles
+    // of one matrix a workgroup per CU. 256 x 4096 227 -> 182 us, 700 x 3000 315 -> 271, four of
+    // 500 x 4000 327 -> 292; with n = 2 m the join costs more than it gives (16 of 512 x 1024:
+    // 342 -> 361). ns_small_kernel adds them up in one workgroup, so few of 128 x 128. Not a
+    // matter of the batch: the sums are the same in any.
+    const int t64 = mp / 64, tiles64 = t64 * (t64 + 1) / 2;
+    int split = np / (mp == 128 ? 512 : 256);
+    for (const int most_slices : {mp == 128 ? 8 : 16, np / mp, 256 / tiles64})
+        split = split < most_slices ? split : most_slices;
+    if (split < 1 || (!small && np / mp < 4))
+        split = 1;
+    const int slice = (np / 64 + split - 1) / split * 64;
+    split = (np + slice - 1) / slice;
 
     for (int64_t b0 = 0; b0 < p.batch; b0 += pl.chunk) {
         const int nz = (int)(p.batch - b0 < pl.chunk ? p.batch - b0 : pl.chunk);
@@ -768,42 +1016,75 @@ static hipError_t ns_type(int type, const NewtonSchulz &p, void *workspace, hipS
             if (first) {   // A = X X^T
                 g.K = np;
                 g.job[0] = {X, X, A, A, A, NS_GRAM};
-                if (s == 0) {
+                if (s == 0)
                     g.job[0].a = g.job[0].b = one(X);
+                if (split > 1 || small) {
+                    g.part = reinterpret_cast<float *>(XT2.p);   // (free between two applies)
+                    g.pstride = xs;
+                    g.slice = slice;
+                    g.jobs = split;
+                    g.tiles = tiles64;
+                    const dim3 grid((unsigned)((int64_t)tiles64 * split * nz));
+                    if (s == 0)
+                        hipLaunchKernelGGL((ns_gemm_kernel<T, NS_PART, 1, 1, 32, 64, 4>), grid, dim3(256), 0, stream, g, p, z0);
+                    else
+                        hipLaunchKernelGGL((ns_gemm_kernel<T, NS_PART, 2, 2, 32, 32, 4>), grid, dim3(256), 0, stream, g, p, z0);
+                    if (!small)
+                        hipLaunchKernelGGL(ns_join_kernel, dim3(tiles64, nz), dim3(256), 0, stream, g);
+                } else if (s == 0) {
                     ns_product<T, NS_SYM, 1, 1>(g, p, z0, p.cus, stream);
                 } else {
                     ns_product<T, NS_SYM, 2, 2>(g, p, z0, p.cus, stream);
                 }
-            }
-            g.K = mp;
-            g.job[0] = {A, A, A, Q, Q, NS_Q_ACC};
-            ns_product<T, NS_POLY, 2, 2>(g, p, z0, p.cus, stream);
-            // T = Q A and W <- Q W, side by side (the first W is Q itself, the last T is not needed)
-            g.jobs = 0;
-            if (!ends)
-                g.job[g.jobs++] = {Q, A, A, Tm, Tm, NS_T};
-            if (!first)
-                g.job[g.jobs++] = {Q, W, W, W2, W2, NS_W};
-            if (g.jobs)
-                ns_product<T, NS_SYM, 2, 2>(g, p, z0, p.cus, stream);
-            if (!ends) {   // A <- Q T
+                if (small) {   // the whole group
+                    int len = 1;
+                    while (s + len < p.steps && !gr.starts(s + len))
+                        ++len;
+                    const NsSmall q = {g.part, g.pstride, split, len, {W, W2}, g.factors, g.fstride};
+                    if (mp == 64)
+                        hipLaunchKernelGGL((ns_small_kernel<64>), dim3(nz), dim3(512), 0, stream, q);
+                    else
+                        hipLaunchKernelGGL((ns_small_kernel<128>), dim3(nz), dim3(512), 0, stream, q);
+                    if (len % 2 == 0) {
+                        const NsMat t = W;
+                        W = W2;
+                        W2 = t;
+                    }
+                }
                 g.jobs = 1;
-                g.job[0] = {Q, Tm, A, A, A, NS_A};
-                ns_product<T, NS_SYM, 2, 2>(g, p, z0, p.cus, stream);
             }
-            if (first) {
-                const NsMat t = Q;
-                Q = W;
-                W = t;
-            } else {
-                const NsMat t = W;
-                W = W2;
-                W2 = t;
+            if (!small) {
+                g.K = mp;
+                g.job[0] = {A, A, A, Q, Q, NS_Q_ACC};
+                ns_product<T, NS_POLY, 2, 2>(g, p, z0, p.cus, stream);
+                // T = Q A and W <- Q W, side by side (the first W is Q itself, the last T is not needed)
+                g.jobs = 0;
+                if (!ends)
+                    g.job[g.jobs++] = {Q, A, A, Tm, Tm, NS_T};
+                if (!first)
+                    g.job[g.jobs++] = {Q, W, W, W2, W2, NS_W};
+                if (g.jobs)
+                    ns_product<T, NS_SYM, 2, 2>(g, p, z0, p.cus, stream);
+                if (!ends) {   // A <- Q T
+                    g.jobs = 1;
+                    g.job[0] = {Q, Tm, A, A, A, NS_A};
+                    ns_product<T, NS_SYM, 2, 2>(g, p, z0, p.cus, stream);
+                }
+                if (first) {
+                    const NsMat t = Q;
+                    Q = W;
+                    W = t;
+                } else {
+                    const NsMat t = W;
+                    W = W2;
+                    W2 = t;
+                }
             }
             if (!ends)
                 continue;
             // X <- W X; X^T is the operand whose rows run along the contracted axis
             g.jobs = 1;
+            g.K = mp;
             const bool exact = s + 1 <= gr.len + (gr.longer > 0);   // G's own X: one part
             const NsMat xt = exact ? one(XT) : XT;
             if (last && !flip) {
