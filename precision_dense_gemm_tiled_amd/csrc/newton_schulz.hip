@@ -311,7 +311,7 @@ struct NsTile {
 
     template <int CHUNKS>
     static __device__ __forceinline__ int swz(int row) {
-        return CHUNKS == 4 ? ((row >> 1) & 3) ^ ((row >> 3) & 1) : (row & 7) ^ ((row >> 3) & 1);
+        return CHUNKS == 16 ? row & 15 : CHUNKS == 4 ? ((row >> 1) & 3) ^ ((row >> 3) & 1) : (row & 7) ^ ((row >> 3) & 1);
     }
 };
 
@@ -401,19 +401,18 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
     // A stage's fragments: lane l has row l % 16 of a block and the 8 of K of quarter
     // l / 16 of a step.
     struct Frags {
-        ns_i32x4 a[S::STEPS][PA][TB], b[S::STEPS][PB][TB];
+        ns_i32x4 a[PA][TB], b[PB][TB];
     };
-    auto read = [&](int e, Frags &f) {
+    auto read = [&](int e, int s, Frags &f) {
         const uint8_t *st = smem + (e % NS) * S::STAGE;
         const int q = lane >> 4, r = lane & 15;
-#pragma unroll
-        for (int s = 0; s < S::STEPS; ++s) {
+        {
 #pragma unroll
             for (int k = 0; k < TB; ++k) {
                 const int ra = wm0 + k * 16 + r;
 #pragma unroll
                 for (int l = 0; l < PA; ++l)
-                    f.a[s][l][k] = *reinterpret_cast<const ns_i32x4 *>(
+                    f.a[l][k] = *reinterpret_cast<const ns_i32x4 *>(
                         st + ra * S::RBA + ((((s * PA + l) * 4 + q) ^ S::template swz<S::CA>(ra)) * 16));
             }
 #pragma unroll
@@ -421,21 +420,21 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
                 const int rb = wn0 + k * 16 + r;
 #pragma unroll
                 for (int l = 0; l < PB; ++l)
-                    f.b[s][l][k] = *reinterpret_cast<const ns_i32x4 *>(
+                    f.b[l][k] = *reinterpret_cast<const ns_i32x4 *>(
                         st + S::A_BYTES + rb * S::RBB + ((((s * PB + l) * 4 + q) ^ S::template swz<S::CB>(rb)) * 16));
             }
         }
     };
     // products lo ... hi - 1 of a stage: in each step l h, h l, h h of each block
-    constexpr int BLOCKS = TB * TB, TERMS = PA + PB - 1, NMF = S::STEPS * BLOCKS * TERMS;
+    constexpr int BLOCKS = TB * TB, TERMS = PA + PB - 1, NMF = BLOCKS * TERMS;
     auto mfmas = [&](const Frags &f, int lo, int hi) {
 #pragma unroll
         for (int n = lo; n < hi; ++n) {
-            const int s = n / (BLOCKS * TERMS), term = n / BLOCKS % TERMS, i = n % BLOCKS / TB, j = n % TB;
+            const int term = n / BLOCKS, i = n % BLOCKS / TB, j = n % TB;
             const bool last = term == TERMS - 1;
             const int x = !last && PA == 2 && term == 0 ? 1 : 0, y = !last && x == 0 ? 1 : 0;
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(ns_f16x8, f.a[s][x][i]),
-                                                               __builtin_bit_cast(ns_f16x8, f.b[s][y][j]), acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(ns_f16x8, f.a[x][i]),
+                                                               __builtin_bit_cast(ns_f16x8, f.b[y][j]), acc[i][j], 0, 0, 0);
         }
     };
 
@@ -445,30 +444,45 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
         dma(e);
     wait_vm_lds<(NS - 1) * S::NL>();
     lds_barrier();
-    read(0, f0);
-    // Stage e has its fragments in registers. After the first half of its products the
-    // barrier says that stage e + 1 has landed and that everybody has read stage e: under
-    // the other half the fragments of e + 1 are read, and the loads of stage e + NS go
-    // into e's slot. (No branch in it: the compiler moves products past one.)
-    auto stage = [&](int e, const Frags &f, Frags &next) {
+    read(0, 0, f0);
+    // Under the products of a step the next step's fragments are read. The barrier says
+    // that stage e + 1 has landed and that everybody has read stage e: the loads of stage
+    // e + NS go into e's slot. (No branch in it: the compiler moves products past one.)
+    auto step1 = [&](int e, const Frags &f, Frags &next) {   // stages of one step
         __builtin_amdgcn_sched_barrier(0);
         mfmas(f, 0, NMF / 2);
         __builtin_amdgcn_sched_barrier(0);
         wait_vm_lds<(NS - 2) * S::NL>();
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        read(e + 1, next);
+        read(e + 1, 0, next);
         dma(e + NS);
         mfmas(f, NMF / 2, NMF);
         __builtin_amdgcn_sched_barrier(0);
     };
     int e = 0;
-    for (; e + 1 < KT; e += 2) {
-        stage(e, f0, f1);
-        stage(e + 1, f1, f0);
+    if constexpr (S::STEPS == 1) {
+        for (; e + 1 < KT; e += 2) {
+            step1(e, f0, f1);
+            step1(e + 1, f1, f0);
+        }
+        if (e < KT)
+            step1(e, f0, f1);
+    } else {
+        for (; e < KT; ++e) {
+            __builtin_amdgcn_sched_barrier(0);
+            read(e, 1, f1);
+            mfmas(f0, 0, NMF);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vm_lds<(NS - 2) * S::NL>();
+            lds_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            read(e + 1, 0, f0);
+            dma(e + NS);
+            mfmas(f1, 0, NMF);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
-    if (e < KT)
-        stage(e, f0, f1);
 
     // Epilogue through LDS, a WT x WT block per wavefront: rows first (8 columns per
     // lane, stored along rows), then columns (stored into the transpose). Of a symmetric
@@ -929,9 +943,18 @@ static void ns_product(NsGemm g, const NewtonSchulz &p, int z0, int cus, hipStre
     g.tiles_m = (g.M + 2 * wt - 1) / (2 * wt);
     g.tiles = (int)count(2 * wt);
     const dim3 grid((unsigned)((int64_t)g.tiles * g.jobs * g.nz));
-    // a deeper ring for workgroups that have their CU for themselves
+    // Workgroups that have a CU for themselves wait at their barriers for nobody's benefit
+    // and for loads from beyond L2: deeper rings, and for tiles of 64 stages of two steps, half
+    // the barriers (1024 x 1024: 300 -> 212 us). Where several share a CU small rings let more of
+    // them in (symmetric 2048 on 528 tiles of 64: 38.8 -> 50.6; 2048 x 8192 on 1024 of 128: 145 ->
+    // 168). In between, tiles of 64 in stages of two steps, without the depth: on 300
+    // 29.2 -> 22.3, on 432 11.2 -> 11.9.
     const bool alone = grid.x <= (unsigned)cus;
-    if (wt == 32)
+    if (wt == 32 && alone)
+        hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 32, 64, 4>), grid, dim3(256), 0, stream, g, p, z0);
+    else if (wt == 32 && 2 * (int64_t)grid.x <= 3 * (int64_t)cus)
+        hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 32, 64, 2>), grid, dim3(256), 0, stream, g, p, z0);
+    else if (wt == 32)
         hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 32, KS, 2>), grid, dim3(256), 0, stream, g, p, z0);
     else if (wt == 48 && alone)
         hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 48, KS, 3>), grid, dim3(256), 0, stream, g, p, z0);
@@ -1028,7 +1051,7 @@ static hipError_t ns_type(int type, const NewtonSchulz &p, void *workspace, hipS
                     if (s == 0)
                         hipLaunchKernelGGL((ns_gemm_kernel<T, NS_PART, 1, 1, 32, 64, 4>), grid, dim3(256), 0, stream, g, p, z0);
                     else
-                        hipLaunchKernelGGL((ns_gemm_kernel<T, NS_PART, 2, 2, 32, 32, 4>), grid, dim3(256), 0, stream, g, p, z0);
+                        hipLaunchKernelGGL((ns_gemm_kernel<T, NS_PART, 2, 2, 32, 64, 4>), grid, dim3(256), 0, stream, g, p, z0);
                     if (!small)
                         hipLaunchKernelGGL(ns_join_kernel, dim3(tiles64, nz), dim3(256), 0, stream, g);
                 } else if (s == 0) {
