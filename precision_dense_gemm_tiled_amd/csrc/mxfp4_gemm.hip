@@ -352,15 +352,21 @@ template <typename OUT, int BM, int BN, int WGM, int WGN, int NS>
 __global__ __launch_bounds__(64 * WGM * WGN) void mx_pair_kernel(MxGemm p, MxGemm q, int ptiles) {
     typedef MxTile<BM, BN, WGM, WGN, NS> MT;
     __shared__ __attribute__((aligned(16))) uint8_t smem[MT::LDS_BYTES];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // one main loop for both, none of which has a bias
     const bool second = (int)blockIdx.x >= ptiles;
-    const int M = second ? q.M : p.M, N = second ? q.N : p.N;
+    MxGemm g = second ? q : p;
+    g.bias = nullptr;
     int tm, tn;
-    mx_tile_of(second ? blockIdx.x - ptiles : blockIdx.x, second ? gridDim.x - ptiles : ptiles, (M + BM - 1) / BM,
-               (N + BN - 1) / BN, tm, tn);
+    mx_tile_of(second ? blockIdx.x - ptiles : blockIdx.x, second ? gridDim.x - ptiles : ptiles, (g.M + BM - 1) / BM,
+               (g.N + BN - 1) / BN, tm, tn);
+    mx_f32x4 acc[MT::TM][MT::TN];
+    MT::template mainloop<float>(g, smem, tm * BM, tn * BN, 0, (g.nb + 7) / 8, tid, lane, wave, acc);
     if (second)
-        mx_tile<float, MT>(q, smem, tm * BM, tn * BN, 0, (q.nb + 7) / 8);
+        MT::template epilogue<float>(g, smem, tm * BM, tn * BN, lane, wave, acc);
     else
-        mx_tile<OUT, MT>(p, smem, tm * BM, tn * BN, 0, (p.nb + 7) / 8);
+        MT::template epilogue<OUT>(g, smem, tm * BM, tn * BN, lane, wave, acc);
 }
 
 // C = sum of ks slices of M x N fp32 partial results (row stride ldp) + bias,
