@@ -294,8 +294,11 @@ enum { NS_SYM, NS_POLY, NS_X, NS_OUT, NS_PART };
 
 // PA, PB: parts of the operands. C tile of 2 WT x 2 WT per workgroup, four
 // wavefronts of WT x WT, stages of KS of K in an LDS ring of NS slots. 16-byte chunk c
-// of LDS row r sits at c ^ swz(r), which keeps the fragment reads (a chunk column over
-// 16 rows) free of bank conflicts.
+// of LDS row r sits at c ^ swz(r). A 16-byte read is served in four groups of 16 lanes,
+// 0-3, 12-15 and 20-27 the first, 4-11, 16-19 and 28-31 the second: half of the rows with
+// one chunk and the other half with its neighbour. swz(r) is even and takes every even
+// value once in each half, so a group has all banks once. (With r % 8 ^ r / 8 % 2 half of the
+// LDS cycles were conflicts; 2048 x 8192: XX.)
 template <int PA, int PB, int WT, int KS, int NS>
 struct NsTile {
     static constexpr int BT = 2 * WT, TB = WT / 16, STEPS = KS / 32;
@@ -311,7 +314,7 @@ struct NsTile {
 
     template <int CHUNKS>
     static __device__ __forceinline__ int swz(int row) {
-        return CHUNKS == 16 ? row & 15 : CHUNKS == 4 ? ((row >> 1) & 3) ^ ((row >> 3) & 1) : (row & 7) ^ ((row >> 3) & 1);
+        return CHUNKS == 16 ? (row & 7) * 2 : CHUNKS == 8 ? row & 6 : (row >> 2) & 2;
     }
 };
 
@@ -661,8 +664,7 @@ __global__ __launch_bounds__(256) void ns_join_kernel(NsGemm p) {
 // One 64 x 64: 74 -> 45 us, 64 x 4096: 166 -> 65 us, 16 of them 187 -> 83.
 //
 // In LDS a row is 4 MP bytes, 32 h and their 32 l in turn, its 16-byte chunks permuted
-// within 256 bytes by the row (chunk c at c ^ (row % 16)): a chunk column over 16 rows is
-// free of bank conflicts. A lane's four sums are consecutive down a column; all matrices
+// within 256 bytes by the row as in NsTile. A lane's four sums are consecutive down a column; all matrices
 // are symmetric, so they are stored along the row of that number.
 struct NsSmall {
     const float *part;
@@ -683,7 +685,7 @@ __global__ __launch_bounds__(512) void ns_small_kernel(NsSmall p) {
     const float *fac = p.factors + z * p.fstride;
     // byte of element k (of part l) of a row
     auto at = [](int row, int k, int l) {
-        return row * ROW + (k / 64) * 256 + ((((k / 32 & 1) * 8 + l * 4 + k % 32 / 8) ^ (row & 15)) * 16) + k % 8 * 2;
+        return row * ROW + (k / 64) * 256 + ((((k / 32 & 1) * 8 + l * 4 + k % 32 / 8) ^ (row & 7) * 2) * 16) + k % 8 * 2;
     };
     {
         const float *part = p.part + z * p.pstride, k = fac[NS_GRAM];
