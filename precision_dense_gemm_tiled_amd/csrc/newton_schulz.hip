@@ -292,13 +292,45 @@ struct NsGemm {
 // a symmetric matrix, on and below the diagonal.
 enum { NS_SYM, NS_POLY, NS_X, NS_OUT, NS_PART };
 
+// Tile t of rows x cols: bands of NS_BAND rows, column by column, so that the tiles that
+// an XCD works on at a time share few rows and columns of the operands (32 of them: 8 + 4).
+constexpr int NS_BAND = 8;
+
+__device__ __forceinline__ void ns_tile(int t, int rows, int cols, int &tm, int &tn) {
+    const int r0 = t / (NS_BAND * cols) * NS_BAND, u = t - r0 * cols, h = min(NS_BAND, rows - r0);
+    tn = u / h;
+    tm = r0 + u - tn * h;
+}
+
+// The same for the tiles on and below the diagonal.
+__device__ __forceinline__ void ns_lower_tile(int t, int rows, int &tm, int &tn) {
+    int r = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);   // t's row if they went row by row
+    while ((r + 1) * (r + 2) / 2 <= t)
+        ++r;
+    while (r * (r + 1) / 2 > t)
+        --r;
+    const int r0 = r / NS_BAND * NS_BAND, h = min(NS_BAND, rows - r0);
+    int u = t - r0 * (r0 + 1) / 2;
+    if (u < r0 * h) {
+        tn = u / h;
+        tm = r0 + u - tn * h;
+        return;
+    }
+    u -= r0 * h;
+    int c = 0;
+    while (u >= h - c)
+        u -= h - c++;
+    tn = r0 + c;
+    tm = tn + u;
+}
+
 // PA, PB: parts of the operands. C tile of 2 WT x 2 WT per workgroup, four
 // wavefronts of WT x WT, stages of KS of K in an LDS ring of NS slots. 16-byte chunk c
 // of LDS row r sits at c ^ swz(r). A 16-byte read is served in four groups of 16 lanes,
 // 0-3, 12-15 and 20-27 the first, 4-11, 16-19 and 28-31 the second: half of the rows with
 // one chunk and the other half with its neighbour. swz(r) is even and takes every even
 // value once in each half, so a group has all banks once. (With r % 8 ^ r / 8 % 2 half of the
-// LDS cycles were conflicts; 2048 x 8192: XX.)
+// LDS cycles were conflicts; 2048 x 8192: 1072 -> 1030 us.)
 template <int PA, int PB, int WT, int KS, int NS>
 struct NsTile {
     static constexpr int BT = 2 * WT, TB = WT / 16, STEPS = KS / 32;
@@ -354,17 +386,10 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p, NewtonSchulz 
     const NsJob &job = p.job[MODE == NS_PART ? 0 : jn];
     const int k0 = MODE == NS_PART ? jn * p.slice : 0;
     int tm, tn;
-    if (SYM) {   // lower triangle: tile t is (tm, tn), tn <= tm
-        tm = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
-        while ((tm + 1) * (tm + 2) / 2 <= t)
-            ++tm;
-        while (tm * (tm + 1) / 2 > t)
-            --tm;
-        tn = t - tm * (tm + 1) / 2;
-    } else {
-        tm = t % p.tiles_m;
-        tn = t / p.tiles_m;
-    }
+    if (SYM)
+        ns_lower_tile(t, p.tiles_m, tm, tn);
+    else
+        ns_tile(t, p.tiles_m, p.tiles / p.tiles_m, tm, tn);
     const int row0 = tm * S::BT, col0 = tn * S::BT;
 
     // (rows past the padding repeat the last: not stored)
@@ -620,12 +645,9 @@ __global__ __launch_bounds__(256) void ns_join_kernel(NsGemm p) {
     __shared__ float tile[64][65];
     const int tid = threadIdx.x, t = blockIdx.x;
     const int64_t z = blockIdx.y;
-    int tm = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
-    while ((tm + 1) * (tm + 2) / 2 <= t)
-        ++tm;
-    while (tm * (tm + 1) / 2 > t)
-        --tm;
-    const int row0 = tm * 64, col0 = (t - tm * (tm + 1) / 2) * 64;
+    int tm, tn;
+    ns_lower_tile(t, p.tiles_m, tm, tn);
+    const int row0 = tm * 64, col0 = tn * 64;
     const float k = p.factors[z * p.fstride + NS_GRAM];
     const float *part = p.part + z * p.pstride;
     const int64_t size = (int64_t)p.M * p.M;
@@ -664,8 +686,8 @@ __global__ __launch_bounds__(256) void ns_join_kernel(NsGemm p) {
 // One 64 x 64: 74 -> 45 us, 64 x 4096: 166 -> 65 us, 16 of them 187 -> 83.
 //
 // In LDS a row is 4 MP bytes, 32 h and their 32 l in turn, its 16-byte chunks permuted
-// within 256 bytes by the row as in NsTile. A lane's four sums are consecutive down a column; all matrices
-// are symmetric, so they are stored along the row of that number.
+// within 256 bytes by the row as in NsTile. A lane's four sums are consecutive down a
+// column; all matrices are symmetric, so they are stored along the row of that number.
 struct NsSmall {
     const float *part;
     int64_t pstride;
@@ -1049,6 +1071,7 @@ static hipError_t ns_type(int type, const NewtonSchulz &p, void *workspace, hipS
                     g.slice = slice;
                     g.jobs = split;
                     g.tiles = tiles64;
+                    g.tiles_m = t64;
                     const dim3 grid((unsigned)((int64_t)tiles64 * split * nz));
                     if (s == 0)
                         hipLaunchKernelGGL((ns_gemm_kernel<T, NS_PART, 1, 1, 32, 64, 4>), grid, dim3(256), 0, stream, g, p, z0);
