@@ -87,6 +87,26 @@ def test_backward_pairs(M, N, K):
     assert torch.equal(dw, mp.gemm_mxfp4(qt, st, *xt, M))
 
 
+# tiles of 128 and 256 on one and on several workgroups per CU, ragged, in products and pairs
+@pytest.mark.parametrize("M,N,K", [(2000, 4000, 1000), (2048, 4097, 296), (4090, 2000, 72), (1900, 1100, 2600)])
+@pytest.mark.parametrize("name", ["bf16", "f32"])
+def test_large_tiles(M, N, K, name):
+    g = gen(M + N + K)
+    A, B = mx.random_held(g, M, K, spread=1), mx.random_held(g, N, K, spread=1)
+    dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[name]
+    out = mp.gemm_mxfp4(*mx.on_gpu(A), *mx.on_gpu(B), K, dtype=dtype)
+    rows = torch.cat([torch.arange(0, M, max(1, M // 100)), torch.arange(M - 3, M)])
+    y, t = product((A[0][rows], A[1][rows]), B, K)
+    mx.check(out[rows.cuda()], y, mx.gemm_tol(y, t, (K + 31) // 32, dtype))
+    whole = mp.gemm_mxfp4(*mx.on_gpu((A[0][:65], A[1][:65])), *mx.on_gpu(B), K, dtype=dtype)   # smaller tiles
+    assert torch.equal(out[:65], whole) or K > 2048   # (few rows and a long K: the sum is split)
+
+
+@pytest.mark.parametrize("M,N,K", [(1500, 1000, 1000), (1000, 1000, 4000), (2000, 2100, 1900)])
+def test_backward_pairs_of_large_tiles(M, N, K):
+    test_backward_pairs(M, N, K)
+
+
 def test_a_held_pair_shares_its_allocation():
     q, s, qt, st = mp.quantize_mxfp4_both(torch.ones(40, 70, device="cuda"))
     assert q.untyped_storage().data_ptr() == s.untyped_storage().data_ptr()
