@@ -26,10 +26,11 @@
 // gradients of rank 64 plus noise, 3e-3 on rank 8 with noise of 1e-2 below it (bf16's
 // own rounding: 1.7e-3, fp16's: 2.1e-4; with the l part: nothing next to either).
 //
-// Bound by the matrix units' power for large matrices (2048 x 8192, W X: 1.2 to 1.4
-// PFLOP/s of fp16 products; the library's bf16 product reaches 1.4), by the number of
-// tiles for the symmetric products (253 of 96 x 96 at 2048: 0.75), by launches and the
-// way to L2 for small ones (12 x 512 x 512: 12 us a product, 6 of them with no K loop).
+// Bound by the matrix units' power for large matrices (2048 x 8192, W X: 1.2 PFLOP/s of
+// fp16 products between the others at 1.9 GHz, 1.6 alone; the library's bf16 product reaches
+// 1.47), by waits for symmetric products on a workgroup per CU (253 tiles of 96 x 96 at 2048:
+// 36 us, 24.5 without loads and LDS reads), by launches and the way to L2 for small ones
+// (12 x 512 x 512: 11 to 15 us a product, about 6 of them with no K loop).
 // Therefore a matrix with a side up to 128 takes all steps of a group in one launch
 // (ns_small_kernel), and A = X X^T of a long and narrow X is split along n.
 #include <cfloat>
@@ -936,8 +937,8 @@ int64_t newton_schulz_bytes(int64_t batch, int64_t M, int64_t N) {
 }
 
 // Tile sizes: us for a stage and for the ends of a workgroup that has a CU for itself
-// (symmetric 2048 x 2048 on 528, 253 and 136 workgroups: 39.4, 34.5 and 48.3 us; 12 of 512 x 512 on
-// 432, 252 and 120: 12.0, 15.5 and 20.5; 2048 x 8192 on 4096, 1892 and 1024: 227, 195 and 167). 32 has the
+// (symmetric 2048 x 2048 on 528, 253 and 136 workgroups: 36.8, 31.0 and 47.1 us; 12 of 512 x 512 on
+// 432, 252 and 120: 11.2, 14.6 and 20.5; 2048 x 8192 on 4096, 1892 and 1024: 181, 149 and 130). 32 has the
 // most workgroups, 64 the fewest loads per flop.
 struct NsSize {
     int wt;
@@ -970,9 +971,9 @@ static void ns_product(NsGemm g, const NewtonSchulz &p, int z0, int cus, hipStre
     // Workgroups that have a CU for themselves wait at their barriers for nobody's benefit
     // and for loads from beyond L2: deeper rings, and for tiles of 64 stages of two steps, half
     // the barriers (1024 x 1024: 300 -> 212 us). Where several share a CU small rings let more of
-    // them in (symmetric 2048 on 528 tiles of 64: 38.8 -> 50.6; 2048 x 8192 on 1024 of 128: 145 ->
-    // 168). In between, tiles of 64 in stages of two steps, without the depth: on 300
-    // 29.2 -> 22.3, on 432 11.2 -> 11.9.
+    // them in (symmetric 2048 on 528 tiles of 64: 36.8 -> 49.4; 2048 x 8192 on 1024 of 128: 130 ->
+    // 167). In between, tiles of 64 in stages of two steps, without the depth: on 300
+    // 28.0 -> 22.6, on 432 11.2 -> 11.9.
     const bool alone = grid.x <= (unsigned)cus;
     if (wt == 32 && alone)
         hipLaunchKernelGGL((ns_gemm_kernel<T, MODE, PA, PB, 32, 64, 4>), grid, dim3(256), 0, stream, g, p, z0);
@@ -1017,7 +1018,7 @@ static hipError_t ns_type(int type, const NewtonSchulz &p, void *workspace, hipS
 
     // Per step and m^3 flop: L steps in a group cost (3 n / m + 4 L - 3) / L products. For a
     // square matrix that is 4 whatever L is, and single steps need fewer launches
-    // (12 x 512 x 512: 199 against 248 us).
+    // (12 x 512 x 512: a fifth less time).
     const bool small = mp <= 128;
     const int most = small || pl.np * 4 >= pl.mp * 5 ? group_length(type, p.a) : 1, groups = (p.steps + most - 1) / most;
     NsGroups gr = {1, 0};
