@@ -135,6 +135,34 @@ def test_newton_schulz_large_tiles(B, M, N):
         assert torch.equal(mp.newton_schulz(x[b].cuda()), got[b])
 
 
+# sides up to 128, where one workgroup takes all steps of a group, and beyond; the long side short, one slice of it,
+# several with a ragged last one, and as many as there are
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("B,M,N", [(2, 64, 512), (1, 64, 4096), (5, 50, 2900), (2, 100, 1024), (1, 128, 5000), (4, 3000, 127),
+                                   (1, 20, 20000), (1, 129, 1100), (3, 192, 768), (1, 192, 2500), (2, 256, 4096), (1, 700, 2900)])
+def test_newton_schulz_long_and_narrow(B, M, N, name):
+    dtype = {"f16": torch.float16, "bf16": torch.bfloat16}[name]
+    g = gen(B + M + N)
+    x = grads(g, B, M, N, dtype)
+    got = mp.newton_schulz(x.cuda())
+    for b in range(B):
+        want = mx.newton_schulz(x[b])
+        off, norm = torch.linalg.vector_norm(got[b].double().cpu() - want), torch.linalg.vector_norm(want)
+        assert off <= mx.half_step(dtype) * 1.125 * norm
+        assert torch.equal(mp.newton_schulz(x[b].cuda()), got[b])
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 7])
+@pytest.mark.parametrize("M,N", [(60, 1100), (128, 128), (900, 128), (190, 1300)])
+def test_newton_schulz_long_and_narrow_steps(steps, M, N):
+    x = grads(gen(steps + M + N), 2, M, N, torch.bfloat16)
+    got = mp.newton_schulz(x.cuda(), steps=steps)
+    for b in range(2):
+        want = mx.newton_schulz(x[b], steps=steps)
+        off, norm = torch.linalg.vector_norm(got[b].double().cpu() - want), torch.linalg.vector_norm(want)
+        assert off <= mx.half_step(torch.bfloat16) * 1.125 * norm
+
+
 @pytest.mark.parametrize("name", ["f16", "bf16"])
 @pytest.mark.parametrize("M,N", [(256, 256), (200, 1000), (900, 130), (300, 333)])
 @pytest.mark.parametrize("noise", [1e-2, 1e-4])
