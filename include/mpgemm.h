@@ -361,8 +361,8 @@ int64_t mpgemm_run_mxfp4_backward_workspace(int64_t M, int64_t N, int64_t K, int
  * as a sum of two fp16 values of a scaled matrix (22 significant bits) and
  * products are summed in fp32; the result is rounded once to `type`. Before that
  * rounding it is within 1/8 of a half step of `type` of the exact one, relative to
- * its norm. Where one side is at least 1.25 times the other, the steps are taken in
- * groups as polynomials of A, and A is formed anew between groups. A G of zeros
+ * its norm. Where one side is at least 1.25 times the other, or is 128 at most, the
+ * steps are taken in groups as polynomials of A, and A is formed anew between groups. A G of zeros
  * gives zeros (eps > 0), one with a NaN or an infinity NaN throughout.
  * Coefficients have to keep singular values that start in [2^-8, 1] above 2^-14 of
  * the bound that the polynomial gives for them (all that orthogonalise do; else
