@@ -152,6 +152,29 @@ def test_newton_schulz_long_and_narrow(B, M, N, name):
         assert torch.equal(mp.newton_schulz(x[b].cuda()), got[b])
 
 
+@pytest.mark.parametrize("B,M,N", [(2, 64, 2048), (1, 256, 2048), (3, 120, 130)])
+def test_newton_schulz_long_and_narrow_graph(B, M, N):
+    """A captured call gives the eager results at every replay, with other work and other inputs in between."""
+    g = gen(B + M + N)
+    inputs = [grads(g, B, M, N, torch.bfloat16).cuda() for _ in range(3)]
+    want = [mp.newton_schulz(x) for x in inputs]
+    x = inputs[0].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        mp.newton_schulz(x)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = mp.newton_schulz(x)
+    for i in (1, 0, 2, 2, 1):
+        x.copy_(inputs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i])
+        assert torch.equal(mp.newton_schulz(inputs[i]), want[i])
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 7])
 @pytest.mark.parametrize("M,N", [(60, 1100), (128, 128), (900, 128), (190, 1300)])
 def test_newton_schulz_long_and_narrow_steps(steps, M, N):
