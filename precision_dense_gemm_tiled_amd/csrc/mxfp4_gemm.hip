@@ -11,7 +11,7 @@
 //
 // Two kernels:
 //   tile    operands through LDS (compute and L2 bandwidth bound)
-//   skinny  M <= 64: operands straight from memory into the matrix unit's
+//   skinny  up to 64 rows (mx_is_skinny): operands straight from memory into the matrix unit's
 //           registers, K over the wavefronts of a workgroup (bound by reading
 //           B once); few activations are quantised in it
 #include "mxfp4.h"
@@ -597,13 +597,22 @@ static int mx_cheapest(int cu_count, F tiles) {
     return cfg;
 }
 
+// Few rows: the skinny kernel, whose workgroups each read all the activations, while their
+// 32 columns go round the CUs once (M of 17 to 64) or a few times; then tiles of 64. Skinny and
+// tile, us, weights cold, at K = 4096: 64 x 8192 11.2 and 13.0, 64 x 10240 19.3 and 11.8, 32 x 8192 8.6 and 12.3,
+// 32 x 10240 14.1 and 11.4, 64 x 28672 36.8 and 20.2, 16 x 16384 12.4 and 13.0, 16 x 28672 20.9 and 16.8, 8 x 28672 18.7
+// and 16.7, 1 x 28672 17.2 and 16.5, where the tiles need a launch for the activations as well.
+static bool mx_is_skinny(int64_t M, int64_t N, int cu_count) {
+    return M <= 4 || (M <= 16 && N < 96 * cu_count) || (M <= 32 && N < 40 * cu_count) || (M <= 64 && N <= 32 * cu_count);
+}
+
 MxPlan plan_mx(int64_t M, int64_t N, int64_t nb, int cu_count) {
     MxPlan pl = {MX_TILE, 0, 1, 0, 0, cu_count};
     if (nb == 0) {
         pl.kind = MX_EMPTY;
         return pl;
     }
-    if (M <= 64) {
+    if (mx_is_skinny(M, N, cu_count)) {
         pl.kind = MX_SKINNY;
         pl.cfg = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
         return pl;

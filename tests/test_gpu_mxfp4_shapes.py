@@ -37,6 +37,25 @@ def test_wide_skinny(M, N, K):
 
 # activations quantised by the product itself: one piece of 8 per thread, four, and the most rows that still are;
 # rows that are not 16-byte aligned or whose length is not a multiple of 8
+# few rows of many columns, on both sides of the sizes from which tiles take them
+@pytest.mark.parametrize("M,N,K", [(64, 8193, 300), (33, 9000, 2100), (32, 10239, 520), (32, 10240, 520), (17, 12000, 1100),
+                                   (16, 24575, 264), (16, 24576, 264), (5, 24577, 1030), (4, 24600, 520), (1, 30000, 1000)])
+@pytest.mark.parametrize("name", ["f16", "f32"])
+def test_few_rows_of_many_columns(M, N, K, name):
+    g = gen(M + N + K)
+    dtype = {"f16": torch.float16, "f32": torch.float32}[name]
+    x = (torch.randn(M, K, generator=g) * 0.1).to(dtype)
+    W = mx.random_held(g, N, K, spread=1)
+    w = mx.on_gpu(W)
+    bias = torch.randn(N, generator=g).to(dtype)
+    out = mp.gemm_mxfp4_dyn(x.cuda(), *w, bias=bias.cuda())
+    X = mx.quantize(x)
+    y, t = product(X, W, K)
+    tol = mx.gemm_tol(y + bias.double(), t + bias.double().abs(), (K + 31) // 32 + 1, dtype)
+    mx.check(out, y + bias.double(), tol)
+    assert torch.equal(mp.gemm_mxfp4(*mx.on_gpu(X), *w, K, bias=bias.cuda(), dtype=dtype), out)
+
+
 @pytest.mark.parametrize("M,K,pad", [(1, 8, 0), (1, 4096, 0), (2, 4096, 0), (1, 16384, 0), (16, 1000, 0), (16, 1024, 8),
                                      (4, 4095, 1), (4, 4096, 3), (5, 2044, 4)])
 @pytest.mark.parametrize("name", ["f16", "f32"])
