@@ -689,6 +689,9 @@ __global__ __launch_bounds__(256) void ns_join_kernel(NsGemm p) {
 // In LDS a row is 4 MP bytes, 32 h and their 32 l in turn, its 16-byte chunks permuted
 // within 256 bytes by the row as in NsTile. A lane's four sums are consecutive down a
 // column; all matrices are symmetric, so they are stored along the row of that number.
+// The next A is Q A Q with one Q on either side: nothing here makes the matrices
+// symmetric, and Q Q A would lift A's roundings between large and small singular values by
+// a^2 a step (128 x 128 of rank 1, four steps in bf16: off by 7e-2 of the norm), this by a.
 struct NsSmall {
     const float *part;
     int64_t pstride;
@@ -838,11 +841,11 @@ __global__ __launch_bounds__(512) void ns_small_kernel(NsSmall p) {
             store(acc, fac[NS_W], to_memory(p.w[s & 1]));
         }
         if (s + 1 < p.steps) {
-            product(in_lds(Q), in_lds(A), acc);   // T = Q A in A's place
+            product(in_lds(A), in_lds(Q), acc);   // T = Q A (stored as the transpose of A Q) in A's place
             __syncthreads();
             store(acc, fac[NS_T], to_lds(A));
             __syncthreads();
-            product(in_lds(Q), in_lds(A), acc);   // A <- Q T
+            product(in_lds(Q), in_lds(A), acc);   // A <- Q T^T = Q A Q
             __syncthreads();
             store(acc, fac[NS_A], to_lds(A));
         }
