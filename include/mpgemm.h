@@ -360,9 +360,15 @@ int64_t mpgemm_run_mxfp4_backward_workspace(int64_t M, int64_t N, int64_t K, int
  * itself). coeffs: host pointer to a, b, c. Every factor of a product is held
  * as a sum of two fp16 values of a scaled matrix (22 significant bits) and
  * products are summed in fp32; the result is rounded once to `type`. Before that
- * rounding it is within 1/8 of a half step of `type` of the exact one, relative to
- * its norm. Where one side is at least 1.25 times the other, or is 128 at most, the
- * steps are taken in groups as polynomials of A, and A is formed anew between groups. A G of zeros
+ * rounding it is about as far from the exact one as the same steps in fp32 are.
+ * What the roundings leave in directions where G's singular values are zero, or
+ * small next to a^-steps, grows by a per step as a signal there does: a matrix of
+ * norm up to 2^-19 a^steps (2^-22 a^steps and less as measured, sides up to 2048),
+ * until it is as large as the rest. With a = 3.4445 that passes a half step of fp16
+ * after 4 steps (6 as measured), of bf16 after 6 (7): more steps on a G of low rank
+ * turn roundings into singular values, in any arithmetic of this precision. Where
+ * one side is at least 1.25 times the other, or is 128 at most, the steps are taken
+ * in groups as polynomials of A, and A is formed anew between groups. A G of zeros
  * gives zeros (eps > 0), one with a NaN or an infinity NaN throughout.
  * Coefficients have to keep singular values that start in [2^-8, 1] above 2^-14 of
  * the bound that the polynomial gives for them (all that orthogonalise do; else

@@ -886,12 +886,14 @@ NsPlan ns_plan(int64_t batch, int64_t M, int64_t N) {
     return pl;
 }
 
-// Steps between two A = X X^T. A's own rounding grows by a^2 a step in the
-// directions of small singular values, and reaches Q through b A. Against 64 bits
-// the result was off by up to 2^-23 a^(2 (L - 1)) of its norm after L steps (2.1e-3 for
-// L = 5, a = 3.4445 on rank 8 with noise of 1e-2 below it; 2e-4 on noise of the
-// signal's size). Kept below 1/8 of a half step of the output type: four steps for
-// bf16, three for fp16 with these coefficients, and five steps are three and two.
+// Steps between two A = X X^T. A's own rounding grows within a group, in the directions
+// of small singular values, and reaches Q through b A. Taken to be off by 2^-23 a^(2 (L - 1)) of
+// the norm after L steps (a Q Q A that nothing makes symmetric: 2.1e-3 for L = 5, a = 3.4445),
+// below 1/8 of a half step of the output type: four steps for bf16, three for fp16 with
+// these coefficients, and five steps are three and two. It is less where A stays
+// symmetric: 3e-5 for L = 4 on rank 4, next to 1e-5 of the iteration in fp32. That is the group's
+// share; what the rounding of X itself leaves grows by a per step however the steps are
+// grouped (see the public header).
 int group_length(int type, float a) {
     const double limit = type == MPGEMM_TYPE_F16 ? 0x1p-14 : 0x1p-11;
     const double grow = (double)a * a > 1. ? (double)a * a : 1.;
