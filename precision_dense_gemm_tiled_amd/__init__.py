@@ -517,7 +517,9 @@ def gemm_w4a4_lowrank(A, B, K, sx, sw, X, LD, LU, bias=None, out=None, handle=No
 # A matrix in MXFP4 is a pair of uint8 tensors (see include/mpgemm.h): codes
 # (R x 16 nb, nb = ceil(K / 32) blocks) and scales (R x nb), both with row
 # strides that are multiples of 16 bytes. The scales that these calls return
-# are views of rows padded to 16 bytes.
+# are views of rows padded to 16 bytes. Copies of them lose the padding (clone,
+# contiguous, to the host and back): a call that is given such scales pads them
+# again, a launch more each time, so a program that loads them keeps padded rows.
 #
 # The calls are short enough for the host's share to count, so their checks,
 # allocations and the C-ABI call are compiled (csrc/torch_calls.cpp); a call on

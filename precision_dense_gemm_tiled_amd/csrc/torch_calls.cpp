@@ -86,10 +86,16 @@ int64_t rows_of(const at::Tensor &t, at::ScalarType type, const char *name) {
 
 int64_t blocks_of(int64_t k) { return (k + 31) / 32; }
 
+// (torch.empty without its way through the dispatcher)
+at::Tensor empty(at::IntArrayRef size, at::ScalarType type, const at::Device &dev) {
+    return at::Tensor(at::detail::empty_cuda(size, type, dev, std::nullopt));
+}
+
 // Codes and scales of rows of k elements, and their row strides in bytes.
 struct Held {
     uint8_t *q = nullptr, *s = nullptr;
     int64_t ldq = 0, lds = 0, rows = 0;
+    at::Tensor padded;   // the scales' copy, where there is one
 };
 
 Held held(PyObject *oq, PyObject *os, int64_t k, const char *name, const at::Device &dev) {
@@ -109,6 +115,14 @@ Held held(PyObject *oq, PyObject *os, int64_t k, const char *name, const at::Dev
         h.lds = (h.lds + 15) / 16 * 16;
     h.q = static_cast<uint8_t *>(q.data_ptr());
     h.s = static_cast<uint8_t *>(s.data_ptr());
+    // Copies of the scales that a call returned (clone, contiguous, to the host and back) have
+    // lost the padding of their rows: they get it again here, in a launch of its own.
+    if (h.rows > 0 && nb > 0 && (h.lds % 16 != 0 || (reinterpret_cast<uintptr_t>(h.s) & 15) != 0)) {
+        h.lds = (nb + 15) / 16 * 16;
+        h.padded = empty({h.rows, h.lds}, at::kByte, dev);
+        h.padded.narrow(1, 0, nb).copy_(s);
+        h.s = static_cast<uint8_t *>(h.padded.data_ptr());
+    }
     return h;
 }
 
@@ -120,11 +134,6 @@ const void *bias_of(PyObject *o, int64_t n, at::ScalarType type, const at::Devic
         fail(PyExc_ValueError, "bias: expected " + std::to_string(n) + " contiguous " + c10::toString(type) +
                                    " values on " + dev.str());
     return b.data_ptr();
-}
-
-// (torch.empty without its way through the dispatcher)
-at::Tensor empty(at::IntArrayRef size, at::ScalarType type, const at::Device &dev) {
-    return at::Tensor(at::detail::empty_cuda(size, type, dev, std::nullopt));
 }
 
 // The result (new, or the caller's) and its row stride.
