@@ -521,6 +521,10 @@ def gemm_w4a4_lowrank(A, B, K, sx, sw, X, LD, LU, bias=None, out=None, handle=No
 # contiguous, to the host and back): a call that is given such scales pads them
 # again, a launch more each time, so a program that loads them keeps padded rows.
 #
+# None of the calls takes part in autograd. Those with floating-point results
+# raise where grad mode is on and an argument requires grad; quantisation, whose
+# results are codes, does not.
+#
 # The calls are short enough for the host's share to count, so their checks,
 # allocations and the C-ABI call are compiled (csrc/torch_calls.cpp); a call on
 # another stream is the same call with that stream made current, so that the

@@ -14,6 +14,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/hip/HIPStream.h>
 
@@ -57,6 +58,14 @@ const at::Tensor &tensor(PyObject *o, const char *name) {
     if (!THPVariable_Check(o))
         fail(PyExc_TypeError, std::string(name) + ": expected a tensor");
     return THPVariable_Unpack(o);
+}
+
+// The calls that return floating-point results take no part in autograd: a gradient that
+// the caller would miss is an error, as it is for torch's own out= forms.
+void no_gradient(const at::Tensor &t, const char *name) {
+    if (c10::GradMode::is_enabled() && t.requires_grad())
+        fail(PyExc_RuntimeError, std::string(name) + " requires grad, but this call takes no part in autograd: "
+                                                     "detach it, call under torch.no_grad() or from an autograd.Function");
 }
 
 int type_of(at::ScalarType t, const char *name, bool f32 = true) {
@@ -130,6 +139,7 @@ const void *bias_of(PyObject *o, int64_t n, at::ScalarType type, const at::Devic
     if (o == Py_None)
         return nullptr;
     const at::Tensor &b = tensor(o, "bias");
+    no_gradient(b, "bias");
     if (b.scalar_type() != type || b.dim() != 1 || b.size(0) != n || !b.is_contiguous() || b.device() != dev)
         fail(PyExc_ValueError, "bias: expected " + std::to_string(n) + " contiguous " + c10::toString(type) +
                                    " values on " + dev.str());
@@ -143,6 +153,7 @@ at::Tensor result(PyObject *out, int64_t rows, int64_t cols, at::ScalarType type
         return empty({rows, cols}, type, dev);
     }
     const at::Tensor &t = tensor(out, "out");
+    no_gradient(t, "out");
     if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols || t.device() != dev)
         fail(PyExc_ValueError, "out: expected " + std::to_string(rows) + " x " + std::to_string(cols) + " on " + dev.str());
     ld = rows_of(t, type, "out");
@@ -309,6 +320,7 @@ PyObject *gemm(PyObject *const *a) {
 // (X, Wq, Ws, bias, out, handle) -> Y
 PyObject *dyn(PyObject *const *a) {
     const at::Tensor &X = tensor(a[0], "X");
+    no_gradient(X, "X");
     const at::ScalarType dt = X.scalar_type();
     const int type = type_of(dt, "X");
     const int64_t ldx = rows_of(X, dt, "X");
@@ -328,6 +340,7 @@ PyObject *dyn(PyObject *const *a) {
 // (dY, WTq, WTs, XTq, XTs, need_dx, need_dw, handle) -> (dX, dW)
 PyObject *backward(PyObject *const *a) {
     const at::Tensor &dY = tensor(a[0], "dY");
+    no_gradient(dY, "dY");
     const at::ScalarType dt = dY.scalar_type();
     const int type = type_of(dt, "dY");
     const int64_t lddy = rows_of(dY, dt, "dY");
@@ -371,6 +384,9 @@ void strides_of(const at::Tensor &t, at::ScalarType type, const char *name, int6
 // (G, steps, coeffs, eps, out, handle) -> Y
 PyObject *newton_schulz(PyObject *const *a) {
     const at::Tensor &G = tensor(a[0], "G");
+    no_gradient(G, "G");
+    if (a[4] != Py_None)
+        no_gradient(tensor(a[4], "out"), "out");
     const at::ScalarType dt = G.scalar_type();
     const int type = type_of(dt, "G", false);
     if (G.dim() != 2 && G.dim() != 3)
