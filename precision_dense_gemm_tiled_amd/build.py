@@ -3,7 +3,8 @@
 Every source is compiled for gfx950 only, with packed-fp32 instruction
 selection disabled (-packed-fp32-ops), then linked into one shared library in
 this package directory, next to the Python binding that loads it. The compiled
-torch-facing calls (host code only) become a second one beside it.
+torch-facing calls (host code only) become a second one beside it, where torch is
+there to compile them against; the library needs neither it nor them.
 """
 import concurrent.futures as cf
 import os
@@ -43,7 +44,16 @@ def _torch_flags():
 def build(verbose: bool = False, jobs: int = 6) -> str:
     objdir = os.path.join(ROOT, "_build", "mpgemm")
     os.makedirs(objdir, exist_ok=True)
-    torch_comp, torch_link = _torch_flags()
+    try:
+        torch_comp, torch_link = _torch_flags()
+    except ImportError as e:   # (the C library needs no torch)
+        print(f"{os.path.basename(CALLS)} is not built, torch is not there: {e}", file=sys.stderr)
+        torch_comp = None
+
+    def shown(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        return cmd
 
     def compile_one(src):
         obj = os.path.join(objdir, src + ".o")
@@ -51,28 +61,21 @@ def build(verbose: bool = False, jobs: int = 6) -> str:
             cmd = [CXX, "-O2", "-std=c++17", "-fPIC"] + torch_comp + ["-I", os.path.join(ROOT, "include")]
         else:
             cmd = [HIPCC] + FLAGS
-        cmd = cmd + ["-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
+        r = subprocess.run(shown(cmd + ["-c", os.path.join(CSRC, src), "-o", obj]), capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"compiling {src} failed:\n{r.stdout}\n{r.stderr}")
         return obj
 
+    def link(cmd, to):
+        subprocess.run(shown(cmd), check=True)
+        os.replace(to + ".tmp", to)
+
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        *objs, torch_obj = ex.map(compile_one, SOURCES + [TORCH_SOURCE])
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
-    tmp = CALLS + ".tmp"
-    cmd = [CXX, "-shared", "-o", tmp, torch_obj] + torch_link
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, CALLS)
+        torch_obj = ex.submit(compile_one, TORCH_SOURCE) if torch_comp is not None else None
+        objs = list(ex.map(compile_one, SOURCES))
+    link([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", LIB + ".tmp"] + objs, LIB)
+    if torch_obj is not None:   # (an error in these is raised once the library is there)
+        link([CXX, "-shared", "-o", CALLS + ".tmp", torch_obj.result()] + torch_link, CALLS)
     return LIB
 
 
