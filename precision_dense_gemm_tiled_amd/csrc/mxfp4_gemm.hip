@@ -673,12 +673,15 @@ static void join(const float *part, int64_t ldp, int ks, const MxGemm &p, hipStr
                        part, ldp, ks, p);
 }
 
-// 32 columns per workgroup once that still gives every CU one: the activations are
-// then read, and in the fused form quantised, half as often.
+// 32 columns per workgroup once 16 would go round the CUs more than once: the activations are
+// then read, and in the fused form quantised, half as often. 16 and 32 columns, us, weights cold, at K =
+// 4096: 64 rows x 4096 9.2 and 10.4, x 4160 15.6 and 10.4, x 8191 17.0 and 11.3; 32 x 4160 9.8 and 7.8; 16 x 4160 7.4
+// and 6.5, at K = 1024 3.7 and 3.8. Up to four rows there is little to read, and in the fused form
+// the other way round (4 x 4160 x 1024 3.6 and 3.9): from the width on that gives every CU 32.
 template <typename T, int MF, int PIECES, bool VEC>
 static void skinny_one(const MxGemm &p, const MxSkinnyX &px, int cus, hipStream_t stream) {
     const unsigned fused = PIECES > 0 ? mx_fused_bytes(p.nb, px.rlog) : 0;
-    if (p.N >= 32 * cus)
+    if (p.M <= 4 ? p.N >= 32 * cus : p.N > 16 * cus)
         hipLaunchKernelGGL((mx_skinny_kernel<T, MF, 2, PIECES, VEC>), dim3((p.N + 31) / 32), dim3(512), MF * 16384 + fused, stream, p, px);
     else
         hipLaunchKernelGGL((mx_skinny_kernel<T, MF, 1, PIECES, VEC>), dim3((p.N + 15) / 16), dim3(512), MF * 8192 + fused, stream, p, px);
