@@ -599,10 +599,18 @@ static int mx_cheapest(int cu_count, F tiles) {
 
 // Few rows: the skinny kernel, whose workgroups each read all the activations, while their
 // 32 columns go round the CUs once (M of 17 to 64) or a few times; then tiles of 64. Skinny and
-// tile, us, weights cold, at K = 4096: 64 x 8192 11.2 and 13.0, 64 x 10240 19.3 and 11.8, 32 x 8192 8.6 and 12.3,
-// 32 x 10240 14.1 and 11.4, 64 x 28672 36.8 and 20.2, 16 x 16384 12.4 and 13.0, 16 x 28672 20.9 and 16.8, 8 x 28672 18.7
+// tile, us, weights cold, at K = 4096: 64 x 8192 11.2 and 12.9, 64 x 10240 19.3 and 11.7, 32 x 8192 8.5 and 11.9,
+// 32 x 10240 14.0 and 11.4, 64 x 28672 36.9 and 19.4, 16 x 16384 12.5 and 12.0, 16 x 28672 20.9 and 15.9, 8 x 28672 18.7
 // and 16.7, 1 x 28672 17.2 and 16.5, where the tiles need a launch for the activations as well.
-static bool mx_is_skinny(int64_t M, int64_t N, int cu_count) {
+// The same ends at K = 1024: 64 x 8192 5.4 and 5.6, 64 x 10240 8.7 and 5.6, 32 x 10240 6.7 and 5.6; at 16384: 32 x 8192
+// 24.3 and 24.5, 32 x 10240 42.6 and 35.1, 16 x 28672 65.6 and 56.0.
+// A long K splits over workgroups in tiles, over the eight wavefronts of one here, and more
+// rows make its steps longer: tiles where M K passes 400000. 64 x 4096: K = 6144 1.11 times
+// the skinny kernel's time in tiles, 8192 0.89, 16384 0.65; 48 x 1024: 6144 1.15, 8192 0.93, 16384 0.72; 32 x 4096: 12288 1.10,
+// 16384 0.97; 32 x 2048: 8192 0.92, 16384 0.68; 24 x 1024 and 17 x 4096 at 16384 1.06 and 1.19.
+static bool mx_is_skinny(int64_t M, int64_t N, int64_t nb, int cu_count) {
+    if (M > 16 && M * nb > 400000 / 32)
+        return false;
     return M <= 4 || (M <= 16 && N < 96 * cu_count) || (M <= 32 && N < 40 * cu_count) || (M <= 64 && N <= 32 * cu_count);
 }
 
@@ -612,7 +620,7 @@ MxPlan plan_mx(int64_t M, int64_t N, int64_t nb, int cu_count) {
         pl.kind = MX_EMPTY;
         return pl;
     }
-    if (mx_is_skinny(M, N, cu_count)) {
+    if (mx_is_skinny(M, N, nb, cu_count)) {
         pl.kind = MX_SKINNY;
         pl.cfg = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
         return pl;
