@@ -30,8 +30,9 @@ class Layer:
         self.wq, self.ws, self.wtq, self.wts = mp.quantize_mxfp4_both(self.weight.bfloat16())
 
     def forward(self, x):
-        self.xt = mp.quantize_mxfp4_both(x)[2:]   # X^T for the weight's gradient
-        return mp.gemm_mxfp4_dyn(x, self.wq, self.ws, bias=self.bias)
+        # X^T is for the weight's gradient; without a backward pass gemm_mxfp4_dyn(x, ...) quantises X in the product
+        xq, xs, *self.xt = mp.quantize_mxfp4_both(x)
+        return mp.gemm_mxfp4(xq, xs, self.wq, self.ws, x.shape[1], bias=self.bias, dtype=x.dtype)
 
     def backward(self, dy):
         return mp.gemm_mxfp4_backward(dy, self.wtq, self.wts, *self.xt)
