@@ -6,8 +6,8 @@
 // short: quantising one token's activations takes the GPU about 2 us, and the
 // same checks and allocations made from Python take the host 14 us a call
 // (ctypes with 20 arguments, five tensor attributes per operand), from here
-// 5 us, launch included (gemm_mxfp4_dyn, one token, 4096 x 4096: 13.4 -> 9.7 us
-// a call in a row of them).
+// 4 to 5 us, launch included (gemm_mxfp4_dyn, one token, 4096 x 4096: 3.9 to 4.5 us a
+// call in a row of them, about what its kernel takes).
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>

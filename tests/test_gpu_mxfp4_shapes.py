@@ -20,8 +20,8 @@ def product(A, B, K):
     return a @ b.t(), a.abs() @ b.abs().t()
 
 
-# from 8192 columns on a skinny product takes 32 per workgroup; K in one group of 16 blocks, several, and a last
-# group of one block; rows of each block of 16
+# few rows of 8192 columns and more, 32 per workgroup (33 and 64 rows: at 8192, beyond it tiles); K in one group of 16
+# blocks, several, and a last group of one block; rows of each block of 16
 @pytest.mark.parametrize("M", [1, 3, 16, 17, 33, 64])
 @pytest.mark.parametrize("N,K", [(8192, 512), (8200, 1056), (8209, 5000)])
 def test_wide_skinny(M, N, K):
@@ -35,8 +35,6 @@ def test_wide_skinny(M, N, K):
     mx.check(got, y, mx.gemm_tol(y, t, (K + 31) // 32, torch.bfloat16))
 
 
-# activations quantised by the product itself: one piece of 8 per thread, four, and the most rows that still are;
-# rows that are not 16-byte aligned or whose length is not a multiple of 8
 # few rows of many columns, on both sides of the sizes from which tiles take them
 @pytest.mark.parametrize("M,N,K", [(64, 8193, 300), (33, 9000, 2100), (32, 10239, 520), (32, 10240, 520), (17, 12000, 1100),
                                    (16, 24575, 264), (16, 24576, 264), (5, 24577, 1030), (4, 24600, 520), (1, 30000, 1000)])
@@ -56,6 +54,8 @@ def test_few_rows_of_many_columns(M, N, K, name):
     assert torch.equal(mp.gemm_mxfp4(*mx.on_gpu(X), *w, K, bias=bias.cuda(), dtype=dtype), out)
 
 
+# activations quantised by the product itself: one piece of 8 per thread, four, and the most rows that still are;
+# rows that are not 16-byte aligned or whose length is not a multiple of 8
 @pytest.mark.parametrize("M,K,pad", [(1, 8, 0), (1, 4096, 0), (2, 4096, 0), (1, 16384, 0), (16, 1000, 0), (16, 1024, 8),
                                      (4, 4095, 1), (4, 4096, 3), (5, 2044, 4)])
 @pytest.mark.parametrize("name", ["f16", "f32"])
