@@ -380,6 +380,103 @@ mpgemm_status_t mpgemm_run_newton_schulz(mpgemm_handle_t h, int64_t batch, int64
                                          void *stream);
 int64_t mpgemm_run_newton_schulz_workspace(int64_t batch, int64_t M, int64_t N);
 
+/* ------------------------------------------------- 8-bit integer linear layer
+ *
+ * A matrix of R rows and K columns is held as int8 codes (row stride ld
+ * bytes >= K) and R fp32 scales, one per row (a token's activations, or the
+ * weights of one output channel): the value of an element is code * scale.
+ *
+ * Quantisation of a row with largest magnitude amax: scale = fp32(amax / 127),
+ * code = the nearest integer to x / scale, ties to even (the exact quotient),
+ * in [-127, 127]; zeros where the scale is zero (rows of zeros, or amax below
+ * 2^-143). A row that holds NaN or an infinity gets the scale NaN and codes of
+ * zero: its products are NaN throughout.
+ *
+ * Like the MXFP4 calls, these and the calls of the gated block take their scratch
+ * memory from the caller: 16-byte aligned, at least the bytes that the matching
+ * _workspace call returns (-1 for sizes that the call refuses; NULL when that is
+ * 0), so calls that share a handle may run on several streams at once.
+ * Operands may have any (element) alignment and row stride. Above 64 rows, operands
+ * whose rows do not start at multiples of 16 bytes (or lie 2^23 bytes apart, or
+ * more) are copied into the workspace first, one launch more: a program that keeps
+ * its weights in padded rows saves that. `aligned` of a _workspace call: nonzero where
+ * no operand needs that copy (of mpgemm_run_gated_backward: and Wg and Wu have
+ * the same row stride). Sizes: K of integer products <= MPGEMM_MAX_K_INT, of 16-bit ones
+ * (and 2 N of the backward pass) <= MPGEMM_MAX_ALONG_LINEAR, all others <=
+ * MPGEMM_MAX_DIM_LINEAR, else MPGEMM_ERR_UNSUPPORTED. Results are bit-identical
+ * from call to call. Everything else is the common contract above. */
+#define MPGEMM_MAX_DIM_LINEAR (1 << 24)
+#define MPGEMM_MAX_ALONG_LINEAR ((1 << 22) - 128)
+
+/* X (M x K, `type`, row stride ldx elements) into codes Q and scales S. */
+mpgemm_status_t mpgemm_quantize_i8(mpgemm_handle_t h, int64_t M, int64_t K, int type, const void *X, int64_t ldx,
+                                   int8_t *Q, int64_t ldq, float *S, void *stream);
+
+/* Y (M x K, `type`, row stride ldy) = codes * scales in fp32, rounded once to the type. */
+mpgemm_status_t mpgemm_dequantize_i8(mpgemm_handle_t h, int64_t M, int64_t K, const int8_t *Q, int64_t ldq,
+                                     const float *S, int type, void *Y, int64_t ldy, void *stream);
+
+/* C = (A B^T) * SA[m] * SB[n] + bias for held A (M x K) and B (N x K): exact
+ * integer sums, rounded to fp32, times SA, times SB, plus the bias (N values of `type`, or
+ * NULL) in fp32, one rounding to `type`. C: M x N, row stride ldc elements. */
+mpgemm_status_t mpgemm_run_w8a8(mpgemm_handle_t h, int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda,
+                                const float *SA, const int8_t *B, int64_t ldb, const float *SB, const void *bias,
+                                int type, void *C, int64_t ldc, void *workspace, int64_t workspace_bytes, void *stream);
+int64_t mpgemm_run_w8a8_workspace(int64_t M, int64_t N, int64_t K, int aligned, int cu_count);
+
+/* The same with the activations X (M x K, `type`, row stride ldx elements) quantised
+ * in the call. Bit-identical to quantising X first. */
+mpgemm_status_t mpgemm_run_w8a8_dyn(mpgemm_handle_t h, int64_t M, int64_t N, int64_t K, int type, const void *X,
+                                    int64_t ldx, const int8_t *W, int64_t ldw, const float *SW, const void *bias,
+                                    void *Y, int64_t ldy, void *workspace, int64_t workspace_bytes, void *stream);
+int64_t mpgemm_run_w8a8_dyn_workspace(int64_t M, int64_t N, int64_t K, int aligned, int cu_count);
+
+/* --------------------------------------------- gated feed-forward block
+ *
+ * H = act(G) * U with G = X Wg^T and U = X Wu^T: X M x K, Wg and Wu N x K, H M x N.
+ * The sums, the activation and the product are fp32, H is rounded once to `type`. */
+enum {
+    MPGEMM_ACT_SILU = 0,       /* v / (1 + exp(-v)) */
+    MPGEMM_ACT_GELU = 1,       /* v (1 + erf(v / sqrt 2)) / 2 */
+    MPGEMM_ACT_GELU_TANH = 2   /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+};
+
+/* In 16 bits (`type` MPGEMM_TYPE_F16 or _BF16 of all matrices). G and U, for the
+ * backward pass: where they are not NULL (both or neither) the two products are
+ * written there, each rounded once; H is computed from the unrounded ones. */
+mpgemm_status_t mpgemm_run_gated(mpgemm_handle_t h, int64_t M, int64_t N, int64_t K, int type, int act, const void *X,
+                                 int64_t ldx, const void *Wg, int64_t ldwg, const void *Wu, int64_t ldwu, void *H,
+                                 int64_t ldh, void *G, int64_t ldg, void *U, int64_t ldu, void *workspace,
+                                 int64_t workspace_bytes, void *stream);
+int64_t mpgemm_run_gated_workspace(int64_t M, int64_t N, int64_t K, int aligned, int cu_count);
+
+/* Gradients of the above from dH (M x N) and the G and U that it wrote:
+ *   dG = dH U act'(G), dU = dH act(G)   in fp32, rounded once to `type`
+ *   dX = dG Wg + dU Wu                  M x K
+ *   dWg = dG^T X, dWu = dU^T X          N x K
+ * with fp32 sums, each result rounded once to `type`. dX may be NULL (then Wg and Wu may
+ * be), and so may dWg and dWu (X, where both are): those gradients are not computed. */
+mpgemm_status_t mpgemm_run_gated_backward(mpgemm_handle_t h, int64_t M, int64_t N, int64_t K, int type, int act,
+                                          const void *dH, int64_t lddh, const void *X, int64_t ldx, const void *Wg,
+                                          int64_t ldwg, const void *Wu, int64_t ldwu, const void *G, int64_t ldg,
+                                          const void *U, int64_t ldu, void *dX, int64_t lddx, void *dWg, int64_t lddwg,
+                                          void *dWu, int64_t lddwu, void *workspace, int64_t workspace_bytes, void *stream);
+int64_t mpgemm_run_gated_backward_workspace(int64_t M, int64_t N, int64_t K, int aligned, int cu_count);
+
+/* On integers: X held as A, SA, the weights as codes and scales; H in `type`. */
+mpgemm_status_t mpgemm_run_gated_w8a8(mpgemm_handle_t h, int64_t M, int64_t N, int64_t K, int act, const int8_t *A,
+                                      int64_t lda, const float *SA, const int8_t *Wg, int64_t ldwg, const float *SG,
+                                      const int8_t *Wu, int64_t ldwu, const float *SU, int type, void *H, int64_t ldh,
+                                      void *workspace, int64_t workspace_bytes, void *stream);
+int64_t mpgemm_run_gated_w8a8_workspace(int64_t M, int64_t N, int64_t K, int aligned, int cu_count);
+
+/* The same with X (`type`, row stride ldx elements) quantised in the call. */
+mpgemm_status_t mpgemm_run_gated_w8a8_dyn(mpgemm_handle_t h, int64_t M, int64_t N, int64_t K, int type, int act,
+                                          const void *X, int64_t ldx, const int8_t *Wg, int64_t ldwg, const float *SG,
+                                          const int8_t *Wu, int64_t ldwu, const float *SU, void *H, int64_t ldh,
+                                          void *workspace, int64_t workspace_bytes, void *stream);
+int64_t mpgemm_run_gated_w8a8_dyn_workspace(int64_t M, int64_t N, int64_t K, int aligned, int cu_count);
+
 /* Measurement aid: a plain streaming read of `bytes` bytes at `src` (device
  * memory, 16-byte aligned, bytes a multiple of 16) with 16-byte loads,
  * loads_per_lane (1, 2, 4 or 8) per lane, all issued before any is combined.

@@ -25,6 +25,12 @@ __all__ = [
     "mpgemm_run_mxfp4_dyn_workspace", "mpgemm_run_mxfp4_backward_workspace", "mpgemm_run_newton_schulz_workspace",
     "quantize_mxfp4", "quantize_mxfp4_both", "dequantize_mxfp4", "gemm_mxfp4", "gemm_mxfp4_dyn",
     "gemm_mxfp4_backward", "newton_schulz",
+    "mpgemm_quantize_i8", "mpgemm_dequantize_i8", "mpgemm_run_w8a8", "mpgemm_run_w8a8_dyn", "mpgemm_run_gated",
+    "mpgemm_run_gated_backward", "mpgemm_run_gated_w8a8", "mpgemm_run_gated_w8a8_dyn",
+    "mpgemm_run_w8a8_workspace", "mpgemm_run_w8a8_dyn_workspace", "mpgemm_run_gated_workspace",
+    "mpgemm_run_gated_backward_workspace", "mpgemm_run_gated_w8a8_workspace", "mpgemm_run_gated_w8a8_dyn_workspace",
+    "quantize_i8", "dequantize_i8", "gemm_w8a8", "gemm_w8a8_dyn", "gemm_gated", "gemm_gated_backward",
+    "gemm_gated_w8a8", "gemm_gated_w8a8_dyn",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -40,6 +46,11 @@ MPGEMM_MAX_K_MXFP4 = (1 << 24) - 32
 MPGEMM_TYPE_F16 = 0
 MPGEMM_TYPE_BF16 = 1
 MPGEMM_TYPE_F32 = 2
+MPGEMM_MAX_DIM_LINEAR = 1 << 24
+MPGEMM_MAX_ALONG_LINEAR = (1 << 22) - 128
+MPGEMM_ACT_SILU = 0
+MPGEMM_ACT_GELU = 1
+MPGEMM_ACT_GELU_TANH = 2
 
 _lib = None
 _i64 = ctypes.c_int64
@@ -113,6 +124,21 @@ def lib() -> ctypes.CDLL:
                         ("mpgemm_run_mxfp4_backward_workspace", 3), ("mpgemm_run_newton_schulz_workspace", 3)):
             f = getattr(L, name)
             f.argtypes, f.restype = [_i64] * n + ([] if "newton" in name else [_int]), _i64
+        _mat, _i8, _ws = [_vp, _i64], [_vp, _i64, _vp], [_vp, _i64, _vp]
+        for name, args in (
+                ("mpgemm_quantize_i8", [_vp, _i64, _i64, _int] + _mat + _i8 + [_vp]),
+                ("mpgemm_dequantize_i8", [_vp, _i64, _i64] + _i8 + [_int] + _mat + [_vp]),
+                ("mpgemm_run_w8a8", [_vp, _i64, _i64, _i64] + _i8 + _i8 + [_vp, _int] + _mat + _ws),
+                ("mpgemm_run_w8a8_dyn", [_vp, _i64, _i64, _i64, _int] + _mat + _i8 + [_vp] + _mat + _ws),
+                ("mpgemm_run_gated", [_vp, _i64, _i64, _i64, _int, _int] + _mat * 6 + _ws),
+                ("mpgemm_run_gated_backward", [_vp, _i64, _i64, _i64, _int, _int] + _mat * 9 + _ws),
+                ("mpgemm_run_gated_w8a8", [_vp, _i64, _i64, _i64, _int] + _i8 * 3 + [_int] + _mat + _ws),
+                ("mpgemm_run_gated_w8a8_dyn", [_vp, _i64, _i64, _i64, _int, _int] + _mat + _i8 * 2 + _mat + _ws)):
+            f = getattr(L, name)
+            f.argtypes, f.restype = args, _int
+        for name in ("w8a8", "w8a8_dyn", "gated", "gated_backward", "gated_w8a8", "gated_w8a8_dyn"):
+            f = getattr(L, f"mpgemm_run_{name}_workspace")
+            f.argtypes, f.restype = [_i64, _i64, _i64, _int, _int], _i64
         _lib = L
     return _lib
 
@@ -251,6 +277,75 @@ def mpgemm_run_mxfp4_backward_workspace(M, N, K, cu_count=256) -> int:
 
 def mpgemm_run_newton_schulz_workspace(batch, M, N) -> int:
     return lib().mpgemm_run_newton_schulz_workspace(batch, M, N)
+
+
+def mpgemm_quantize_i8(h, M, K, type, X, ldx, Q, ldq, S, stream=None) -> int:
+    return lib().mpgemm_quantize_i8(h, M, K, type, X, ldx, Q, ldq, S, stream)
+
+
+def mpgemm_dequantize_i8(h, M, K, Q, ldq, S, type, Y, ldy, stream=None) -> int:
+    return lib().mpgemm_dequantize_i8(h, M, K, Q, ldq, S, type, Y, ldy, stream)
+
+
+def mpgemm_run_w8a8(h, M, N, K, A, lda, SA, B, ldb, SB, bias, type, C, ldc, workspace=None, workspace_bytes=0,
+                    stream=None) -> int:
+    return lib().mpgemm_run_w8a8(h, M, N, K, A, lda, SA, B, ldb, SB, bias, type, C, ldc, workspace, workspace_bytes,
+                                 stream)
+
+
+def mpgemm_run_w8a8_dyn(h, M, N, K, type, X, ldx, W, ldw, SW, bias, Y, ldy, workspace=None, workspace_bytes=0,
+                        stream=None) -> int:
+    return lib().mpgemm_run_w8a8_dyn(h, M, N, K, type, X, ldx, W, ldw, SW, bias, Y, ldy, workspace, workspace_bytes,
+                                     stream)
+
+
+def mpgemm_run_gated(h, M, N, K, type, act, X, ldx, Wg, ldwg, Wu, ldwu, H, ldh, G=None, ldg=0, U=None, ldu=0,
+                     workspace=None, workspace_bytes=0, stream=None) -> int:
+    return lib().mpgemm_run_gated(h, M, N, K, type, act, X, ldx, Wg, ldwg, Wu, ldwu, H, ldh, G, ldg, U, ldu, workspace,
+                                  workspace_bytes, stream)
+
+
+def mpgemm_run_gated_backward(h, M, N, K, type, act, dH, lddh, X, ldx, Wg, ldwg, Wu, ldwu, G, ldg, U, ldu, dX, lddx,
+                              dWg, lddwg, dWu, lddwu, workspace=None, workspace_bytes=0, stream=None) -> int:
+    return lib().mpgemm_run_gated_backward(h, M, N, K, type, act, dH, lddh, X, ldx, Wg, ldwg, Wu, ldwu, G, ldg, U, ldu,
+                                           dX, lddx, dWg, lddwg, dWu, lddwu, workspace, workspace_bytes, stream)
+
+
+def mpgemm_run_gated_w8a8(h, M, N, K, act, A, lda, SA, Wg, ldwg, SG, Wu, ldwu, SU, type, H, ldh, workspace=None,
+                          workspace_bytes=0, stream=None) -> int:
+    return lib().mpgemm_run_gated_w8a8(h, M, N, K, act, A, lda, SA, Wg, ldwg, SG, Wu, ldwu, SU, type, H, ldh, workspace,
+                                       workspace_bytes, stream)
+
+
+def mpgemm_run_gated_w8a8_dyn(h, M, N, K, type, act, X, ldx, Wg, ldwg, SG, Wu, ldwu, SU, H, ldh, workspace=None,
+                              workspace_bytes=0, stream=None) -> int:
+    return lib().mpgemm_run_gated_w8a8_dyn(h, M, N, K, type, act, X, ldx, Wg, ldwg, SG, Wu, ldwu, SU, H, ldh, workspace,
+                                           workspace_bytes, stream)
+
+
+def mpgemm_run_w8a8_workspace(M, N, K, aligned=1, cu_count=256) -> int:
+    """Bytes of scratch of mpgemm_run_w8a8 (-1: sizes it refuses); aligned: no operand has to be copied."""
+    return lib().mpgemm_run_w8a8_workspace(M, N, K, aligned, cu_count)
+
+
+def mpgemm_run_w8a8_dyn_workspace(M, N, K, aligned=1, cu_count=256) -> int:
+    return lib().mpgemm_run_w8a8_dyn_workspace(M, N, K, aligned, cu_count)
+
+
+def mpgemm_run_gated_workspace(M, N, K, aligned=1, cu_count=256) -> int:
+    return lib().mpgemm_run_gated_workspace(M, N, K, aligned, cu_count)
+
+
+def mpgemm_run_gated_backward_workspace(M, N, K, aligned=1, cu_count=256) -> int:
+    return lib().mpgemm_run_gated_backward_workspace(M, N, K, aligned, cu_count)
+
+
+def mpgemm_run_gated_w8a8_workspace(M, N, K, aligned=1, cu_count=256) -> int:
+    return lib().mpgemm_run_gated_w8a8_workspace(M, N, K, aligned, cu_count)
+
+
+def mpgemm_run_gated_w8a8_dyn_workspace(M, N, K, aligned=1, cu_count=256) -> int:
+    return lib().mpgemm_run_gated_w8a8_dyn_workspace(M, N, K, aligned, cu_count)
 
 
 # ------------------------------------------------------------------ torch helpers
@@ -630,3 +725,85 @@ def newton_schulz(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out=No
         with _on(stream, G):
             return newton_schulz(G, steps, coeffs, eps, out, handle)
     return (_calls or _load_calls()).newton_schulz(G, steps, coeffs, eps, out, handle)
+
+
+# ------------------------------------------------------------------ 8-bit integers and the gated block
+#
+# A matrix in 8-bit integers is a pair: codes (R x K int8) and R float32 scales, one
+# for each row (a token, or an output channel of a weight). quantize_i8 returns codes
+# whose rows are padded to 16 bytes; others (a copy that has lost the padding) are taken
+# too, and above 64 rows copied in the call. As the MXFP4 calls, none of these takes
+# part in autograd: they raise where a gradient would be lost.
+
+
+def quantize_i8(X, handle=None, stream=None):
+    """Codes (M x K int8) and scales (M float32) of X (M x K, fp16, bf16 or fp32):
+    scale = max |row| / 127, code = the nearest integer to x / scale."""
+    if stream is not None:
+        with _on(stream, X):
+            return quantize_i8(X, handle)
+    return (_calls or _load_calls()).quantize_i8(X, handle)
+
+
+def dequantize_i8(q, s, dtype=None, out=None, handle=None, stream=None):
+    """The values (M x K) that codes and scales stand for, in fp16, bf16 or fp32 (the default)."""
+    if stream is not None:
+        with _on(stream, q):
+            return dequantize_i8(q, s, dtype, out, handle)
+    return (_calls or _load_calls()).dequantize_i8(q, s, dtype, out, handle)
+
+
+def gemm_w8a8(Aq, As, Bq, Bs, bias=None, dtype=None, out=None, handle=None, stream=None):
+    """C = (Aq @ Bq.T) * As[:, None] * Bs[None, :] + bias for held A (M x K) and B
+    (N x K); C and bias in fp16, bf16 or fp32 (the default)."""
+    if stream is not None:
+        with _on(stream, Aq):
+            return gemm_w8a8(Aq, As, Bq, Bs, bias, dtype, out, handle)
+    return (_calls or _load_calls()).gemm_w8a8(Aq, As, Bq, Bs, bias, dtype, out, handle)
+
+
+def gemm_w8a8_dyn(X, Wq, Ws, bias=None, out=None, handle=None, stream=None):
+    """Y = I8(X) @ W.T + bias: X (M x K, fp16, bf16 or fp32) is quantised for each
+    token in the call, W (N x K) is held; Y and bias in X's type."""
+    if stream is not None:
+        with _on(stream, X):
+            return gemm_w8a8_dyn(X, Wq, Ws, bias, out, handle)
+    return (_calls or _load_calls()).w8a8_dyn(X, Wq, Ws, bias, out, handle)
+
+
+def gemm_gated(X, Wg, Wu, act="silu", keep=False, out=None, handle=None, stream=None):
+    """H = act(X @ Wg.T) * (X @ Wu.T) for X (M x K), Wg and Wu (N x K) in fp16 or bf16;
+    act: "silu", "gelu" or "gelu_tanh". keep: (H, G, U) with the two products, each
+    rounded once, for gemm_gated_backward."""
+    if stream is not None:
+        with _on(stream, X):
+            return gemm_gated(X, Wg, Wu, act, keep, out, handle)
+    return (_calls or _load_calls()).gated(X, Wg, Wu, act, keep, out, handle)
+
+
+def gemm_gated_backward(dH, X, Wg, Wu, G, U, act="silu", need_dx=True, need_dw=True, handle=None, stream=None):
+    """Gradients of gemm_gated from dH (M x N) and the G and U that it kept:
+    (dX, dWg, dWu) in dH's type. What is not needed is None (need_dx=False: Wg and Wu may
+    be None; need_dw=False: X)."""
+    if stream is not None:
+        with _on(stream, dH):
+            return gemm_gated_backward(dH, X, Wg, Wu, G, U, act, need_dx, need_dw, handle)
+    return (_calls or _load_calls()).gated_backward(dH, X, Wg, Wu, G, U, act, need_dx, need_dw, handle)
+
+
+def gemm_gated_w8a8(Aq, As, Wgq, Wgs, Wuq, Wus, act="silu", dtype=None, out=None, handle=None, stream=None):
+    """The gated block with all three operands held in 8-bit integers; H in fp16, bf16 or
+    fp32 (the default)."""
+    if stream is not None:
+        with _on(stream, Aq):
+            return gemm_gated_w8a8(Aq, As, Wgq, Wgs, Wuq, Wus, act, dtype, out, handle)
+    return (_calls or _load_calls()).gated_w8a8(Aq, As, Wgq, Wgs, Wuq, Wus, act, dtype, out, handle)
+
+
+def gemm_gated_w8a8_dyn(X, Wgq, Wgs, Wuq, Wus, act="silu", out=None, handle=None, stream=None):
+    """The gated block with X (fp16, bf16 or fp32) quantised for each token in the call and
+    both weights held; H in X's type."""
+    if stream is not None:
+        with _on(stream, X):
+            return gemm_gated_w8a8_dyn(X, Wgq, Wgs, Wuq, Wus, act, out, handle)
+    return (_calls or _load_calls()).gated_w8a8_dyn(X, Wgq, Wgs, Wuq, Wus, act, out, handle)

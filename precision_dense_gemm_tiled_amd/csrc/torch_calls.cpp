@@ -1,4 +1,4 @@
-// Torch-facing calls of the MXFP4 and Newton-Schulz entry points: argument
+// Torch-facing calls of the MXFP4, Newton-Schulz, 8-bit integer and gated entry points: argument
 // checks on tensors, outputs and scratch from torch's allocator on the current
 // stream, one call of the C-ABI each.
 //
@@ -18,6 +18,7 @@
 #include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/hip/HIPStream.h>
 
+#include <cstring>
 #include <string>
 
 #include "mpgemm.h"
@@ -425,6 +426,244 @@ PyObject *newton_schulz(PyObject *const *a) {
     return wrap(Y);
 }
 
+// ---- 8-bit integers: codes (R x K int8, any row stride) and R fp32 scales
+
+struct I8Held {
+    const int8_t *q = nullptr;
+    const float *s = nullptr;
+    int64_t ld = 0, rows = 0, k = 0;
+};
+
+I8Held i8_held(PyObject *oq, PyObject *os, const char *name, const at::Device &dev) {
+    const at::Tensor &q = tensor(oq, name), &s = tensor(os, name);
+    I8Held h;
+    h.ld = rows_of(q, at::kChar, name);
+    h.rows = q.size(0);
+    h.k = q.size(1);
+    if (s.scalar_type() != at::kFloat || s.dim() != 1 || s.size(0) != h.rows || !s.is_contiguous())
+        fail(PyExc_ValueError, std::string(name) + ": expected " + std::to_string(h.rows) + " contiguous float32 scales");
+    no_gradient(s, name);
+    if (q.device() != dev || s.device() != dev)
+        fail(PyExc_ValueError, std::string(name) + ": not on " + dev.str());
+    h.q = static_cast<const int8_t *>(q.data_ptr());
+    h.s = static_cast<const float *>(s.data_ptr());
+    return h;
+}
+
+void same_k(int64_t k, int64_t other, const char *what) {
+    if (k != other)
+        fail(PyExc_ValueError, std::string(what) + " disagree on K (" + std::to_string(k) + " and " + std::to_string(other) + ")");
+}
+
+// Whether rows start at multiples of 16 bytes, not too far apart for one offset.
+bool rows_aligned(const void *p, int64_t ld, int64_t rows, int size) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (rows <= 1 || (ld * size % 16 == 0 && ld * size < (1 << 23)));
+}
+
+int act_of(PyObject *o) {
+    const char *s = PyUnicode_Check(o) ? PyUnicode_AsUTF8(o) : nullptr;
+    if (s && !strcmp(s, "silu"))
+        return MPGEMM_ACT_SILU;
+    if (s && !strcmp(s, "gelu"))
+        return MPGEMM_ACT_GELU;
+    if (s && !strcmp(s, "gelu_tanh"))
+        return MPGEMM_ACT_GELU_TANH;
+    fail(PyExc_ValueError, "act: expected 'silu', 'gelu' or 'gelu_tanh'");
+}
+
+// A 16-bit matrix of the block's type on its device, for the product named.
+const at::Tensor &block(PyObject *o, const char *name, at::ScalarType type, const at::Device &dev, int64_t &ld) {
+    const at::Tensor &t = tensor(o, name);
+    no_gradient(t, name);
+    ld = rows_of(t, type, name);
+    if (t.device() != dev)
+        fail(PyExc_ValueError, std::string(name) + ": not on " + dev.str());
+    return t;
+}
+
+void shape_is(const at::Tensor &t, int64_t rows, int64_t cols, const char *name) {
+    if (t.size(0) != rows || t.size(1) != cols)
+        fail(PyExc_ValueError, std::string(name) + ": expected " + std::to_string(rows) + " x " + std::to_string(cols) + ", got " +
+                                   std::to_string(t.size(0)) + " x " + std::to_string(t.size(1)));
+}
+
+// (X, handle) -> codes (rows padded to 16 bytes), scales
+PyObject *quantize_i8(PyObject *const *a) {
+    const at::Tensor &X = tensor(a[0], "X");
+    const int type = type_of(X.scalar_type(), "X");
+    const int64_t ldx = rows_of(X, X.scalar_type(), "X"), M = X.size(0), K = X.size(1), ld = std::max<int64_t>((K + 15) / 16 * 16, 16);
+    const at::Device dev = X.device();
+    at::Tensor q = empty({M, ld}, at::kChar, dev), s = empty({M}, at::kFloat, dev);
+    if (K != ld)
+        q.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef{M, K}, at::IntArrayRef{ld, 1});
+    if (K == 0)
+        s.zero_();
+    check(mpgemm_quantize_i8(handle_of(a[1], dev), M, K, type, X.data_ptr(), ldx, static_cast<int8_t *>(q.data_ptr()), ld,
+                             static_cast<float *>(s.data_ptr()), stream_of(dev)), "mpgemm_quantize_i8");
+    return tuple({q, s});
+}
+
+// (q, s, dtype, out, handle) -> values
+PyObject *dequantize_i8(PyObject *const *a) {
+    const at::ScalarType dt = dtype_of(a[2], a[3]);
+    const int type = type_of(dt, "dtype");
+    const at::Device dev = tensor(a[0], "q").device();
+    const I8Held m = i8_held(a[0], a[1], "q", dev);
+    int64_t ldy;
+    at::Tensor Y = result(a[3], m.rows, m.k, dt, dev, ldy);
+    check(mpgemm_dequantize_i8(handle_of(a[4], dev), m.rows, m.k, m.q, m.ld, m.s, type, Y.data_ptr(), ldy, stream_of(dev)),
+          "mpgemm_dequantize_i8");
+    return wrap(Y);
+}
+
+// (Aq, As, Bq, Bs, bias, dtype, out, handle) -> C
+PyObject *gemm_w8a8(PyObject *const *a) {
+    const at::ScalarType dt = dtype_of(a[5], a[6]);
+    const int type = type_of(dt, "dtype");
+    const at::Device dev = tensor(a[0], "A").device();
+    const I8Held A = i8_held(a[0], a[1], "A", dev), B = i8_held(a[2], a[3], "B", dev);
+    same_k(A.k, B.k, "A and B");
+    const void *bias = bias_of(a[4], B.rows, dt, dev);
+    int64_t ldc;
+    at::Tensor C = result(a[6], A.rows, B.rows, dt, dev, ldc);
+    const bool al = rows_aligned(A.q, A.ld, A.rows, 1) && rows_aligned(B.q, B.ld, B.rows, 1);
+    const int64_t n = mpgemm_run_w8a8_workspace(A.rows, B.rows, A.k, al, cu_count(dev));
+    const at::Tensor ws = scratch(n, dev, "mpgemm_run_w8a8");
+    check(mpgemm_run_w8a8(handle_of(a[7], dev), A.rows, B.rows, A.k, A.q, A.ld, A.s, B.q, B.ld, B.s, bias, type, C.data_ptr(), ldc,
+                          pointer(ws), n, stream_of(dev)), "mpgemm_run_w8a8");
+    return wrap(C);
+}
+
+// (X, Wq, Ws, bias, out, handle) -> Y
+PyObject *w8a8_dyn(PyObject *const *a) {
+    const at::Tensor &X = tensor(a[0], "X");
+    no_gradient(X, "X");
+    const at::ScalarType dt = X.scalar_type();
+    const int type = type_of(dt, "X");
+    const int64_t ldx = rows_of(X, dt, "X"), M = X.size(0), K = X.size(1);
+    const at::Device dev = X.device();
+    const I8Held W = i8_held(a[1], a[2], "W", dev);
+    same_k(K, W.k, "X and W");
+    const void *bias = bias_of(a[3], W.rows, dt, dev);
+    int64_t ldy;
+    at::Tensor Y = result(a[4], M, W.rows, dt, dev, ldy);
+    const int64_t n = mpgemm_run_w8a8_dyn_workspace(M, W.rows, K, rows_aligned(W.q, W.ld, W.rows, 1), cu_count(dev));
+    const at::Tensor ws = scratch(n, dev, "mpgemm_run_w8a8_dyn");
+    check(mpgemm_run_w8a8_dyn(handle_of(a[5], dev), M, W.rows, K, type, X.data_ptr(), ldx, W.q, W.ld, W.s, bias, Y.data_ptr(), ldy,
+                              pointer(ws), n, stream_of(dev)), "mpgemm_run_w8a8_dyn");
+    return wrap(Y);
+}
+
+// (X, Wg, Wu, act, keep, out, handle) -> H or (H, G, U)
+PyObject *gated(PyObject *const *a) {
+    const at::Tensor &X = tensor(a[0], "X");
+    no_gradient(X, "X");
+    const at::ScalarType dt = X.scalar_type();
+    const int type = type_of(dt, "X", false), act = act_of(a[3]);
+    const int64_t ldx = rows_of(X, dt, "X"), M = X.size(0), K = X.size(1);
+    const at::Device dev = X.device();
+    int64_t ldg, ldu, ldh;
+    const at::Tensor &Wg = block(a[1], "Wg", dt, dev, ldg), &Wu = block(a[2], "Wu", dt, dev, ldu);
+    const int64_t N = Wg.size(0);
+    shape_is(Wg, N, K, "Wg");
+    shape_is(Wu, N, K, "Wu");
+    const bool keep = truth(a[4]);
+    at::Tensor H = result(a[5], M, N, dt, dev, ldh);
+    const at::Tensor G = keep ? empty({M, N}, dt, dev) : at::Tensor(), U = keep ? empty({M, N}, dt, dev) : at::Tensor();
+    const bool al = rows_aligned(X.data_ptr(), ldx, M, 2) && rows_aligned(Wg.data_ptr(), ldg, N, 2) && rows_aligned(Wu.data_ptr(), ldu, N, 2);
+    const int64_t n = mpgemm_run_gated_workspace(M, N, K, al, cu_count(dev)), ld = std::max<int64_t>(N, 1);
+    const at::Tensor ws = scratch(n, dev, "mpgemm_run_gated");
+    check(mpgemm_run_gated(handle_of(a[6], dev), M, N, K, type, act, X.data_ptr(), ldx, Wg.data_ptr(), ldg, Wu.data_ptr(), ldu,
+                           H.data_ptr(), ldh, pointer(G), ld, pointer(U), ld, pointer(ws), n, stream_of(dev)), "mpgemm_run_gated");
+    if (!keep)
+        return wrap(H);
+    return tuple({H, G, U});
+}
+
+// (dH, X, Wg, Wu, G, U, act, need_dx, need_dw, handle) -> (dX, dWg, dWu)
+PyObject *gated_backward(PyObject *const *a) {
+    const at::Tensor &dH = tensor(a[0], "dH");
+    no_gradient(dH, "dH");
+    const at::ScalarType dt = dH.scalar_type();
+    const int type = type_of(dt, "dH", false), act = act_of(a[6]);
+    const int64_t lddh = rows_of(dH, dt, "dH"), M = dH.size(0), N = dH.size(1);
+    const at::Device dev = dH.device();
+    const bool need_dx = truth(a[7]), need_dw = truth(a[8]);
+    if (!need_dx && !need_dw)
+        return tuple({at::Tensor(), at::Tensor(), at::Tensor()});
+    int64_t ldx = 0, ldwg = 0, ldwu = 0, ldg, ldu, K = 0;
+    at::Tensor X, Wg, Wu;
+    if (need_dw) {
+        X = block(a[1], "X", dt, dev, ldx);
+        K = X.size(1);
+        shape_is(X, M, K, "X");
+    }
+    if (need_dx) {
+        Wg = block(a[2], "Wg", dt, dev, ldwg);
+        Wu = block(a[3], "Wu", dt, dev, ldwu);
+        if (!need_dw)
+            K = Wg.size(1);
+        shape_is(Wg, N, K, "Wg");
+        shape_is(Wu, N, K, "Wu");
+    }
+    const at::Tensor &G = block(a[4], "G", dt, dev, ldg), &U = block(a[5], "U", dt, dev, ldu);
+    shape_is(G, M, N, "G");
+    shape_is(U, M, N, "U");
+    const at::Tensor dX = need_dx ? empty({M, K}, dt, dev) : at::Tensor();
+    const at::Tensor dWg = need_dw ? empty({N, K}, dt, dev) : at::Tensor(), dWu = need_dw ? empty({N, K}, dt, dev) : at::Tensor();
+    const bool al = (!need_dw || rows_aligned(X.data_ptr(), ldx, M, 2)) &&
+                    (!need_dx || (rows_aligned(Wg.data_ptr(), ldwg, N, 2) && rows_aligned(Wu.data_ptr(), ldwu, N, 2) && (ldwg == ldwu || N <= 1)));
+    const int64_t n = mpgemm_run_gated_backward_workspace(M, N, K, al, cu_count(dev)), ld = std::max<int64_t>(K, 1);
+    const at::Tensor ws = scratch(n, dev, "mpgemm_run_gated_backward");
+    check(mpgemm_run_gated_backward(handle_of(a[9], dev), M, N, K, type, act, dH.data_ptr(), lddh, pointer(X), ldx, pointer(Wg), ldwg,
+                                    pointer(Wu), ldwu, G.data_ptr(), ldg, U.data_ptr(), ldu, pointer(dX), ld, pointer(dWg), ld,
+                                    pointer(dWu), ld, pointer(ws), n, stream_of(dev)), "mpgemm_run_gated_backward");
+    return tuple({dX, dWg, dWu});
+}
+
+// (Aq, As, Wgq, Wgs, Wuq, Wus, act, dtype, out, handle) -> H
+PyObject *gated_w8a8(PyObject *const *a) {
+    const at::ScalarType dt = dtype_of(a[7], a[8]);
+    const int type = type_of(dt, "dtype"), act = act_of(a[6]);
+    const at::Device dev = tensor(a[0], "A").device();
+    const I8Held A = i8_held(a[0], a[1], "A", dev), G = i8_held(a[2], a[3], "Wg", dev), U = i8_held(a[4], a[5], "Wu", dev);
+    same_k(A.k, G.k, "A and Wg");
+    same_k(A.k, U.k, "A and Wu");
+    if (G.rows != U.rows)
+        fail(PyExc_ValueError, "Wg and Wu disagree on N");
+    int64_t ldh;
+    at::Tensor H = result(a[8], A.rows, G.rows, dt, dev, ldh);
+    const bool al = rows_aligned(A.q, A.ld, A.rows, 1) && rows_aligned(G.q, G.ld, G.rows, 1) && rows_aligned(U.q, U.ld, U.rows, 1);
+    const int64_t n = mpgemm_run_gated_w8a8_workspace(A.rows, G.rows, A.k, al, cu_count(dev));
+    const at::Tensor ws = scratch(n, dev, "mpgemm_run_gated_w8a8");
+    check(mpgemm_run_gated_w8a8(handle_of(a[9], dev), A.rows, G.rows, A.k, act, A.q, A.ld, A.s, G.q, G.ld, G.s, U.q, U.ld, U.s, type,
+                                H.data_ptr(), ldh, pointer(ws), n, stream_of(dev)), "mpgemm_run_gated_w8a8");
+    return wrap(H);
+}
+
+// (X, Wgq, Wgs, Wuq, Wus, act, out, handle) -> H
+PyObject *gated_w8a8_dyn(PyObject *const *a) {
+    const at::Tensor &X = tensor(a[0], "X");
+    no_gradient(X, "X");
+    const at::ScalarType dt = X.scalar_type();
+    const int type = type_of(dt, "X"), act = act_of(a[5]);
+    const int64_t ldx = rows_of(X, dt, "X"), M = X.size(0), K = X.size(1);
+    const at::Device dev = X.device();
+    const I8Held G = i8_held(a[1], a[2], "Wg", dev), U = i8_held(a[3], a[4], "Wu", dev);
+    same_k(K, G.k, "X and Wg");
+    same_k(K, U.k, "X and Wu");
+    if (G.rows != U.rows)
+        fail(PyExc_ValueError, "Wg and Wu disagree on N");
+    int64_t ldh;
+    at::Tensor H = result(a[6], M, G.rows, dt, dev, ldh);
+    const bool al = rows_aligned(G.q, G.ld, G.rows, 1) && rows_aligned(U.q, U.ld, U.rows, 1);
+    const int64_t n = mpgemm_run_gated_w8a8_dyn_workspace(M, G.rows, K, al, cu_count(dev));
+    const at::Tensor ws = scratch(n, dev, "mpgemm_run_gated_w8a8_dyn");
+    check(mpgemm_run_gated_w8a8_dyn(handle_of(a[7], dev), M, G.rows, K, type, act, X.data_ptr(), ldx, G.q, G.ld, G.s, U.q, U.ld, U.s,
+                                    H.data_ptr(), ldh, pointer(ws), n, stream_of(dev)), "mpgemm_run_gated_w8a8_dyn");
+    return wrap(H);
+}
+
 template <PyObject *(*F)(PyObject *const *), Py_ssize_t N>
 PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -446,7 +685,10 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&call<name, n>)), METH_FASTCALL, nullptr}
 
 PyMethodDef methods[] = {MPG_CALL(quantize, 3), MPG_CALL(dequantize, 6), MPG_CALL(gemm, 9),      MPG_CALL(dyn, 6),
-                         MPG_CALL(backward, 8), MPG_CALL(newton_schulz, 6), {nullptr, nullptr, 0, nullptr}};
+                         MPG_CALL(backward, 8), MPG_CALL(newton_schulz, 6),
+                         MPG_CALL(quantize_i8, 2), MPG_CALL(dequantize_i8, 5), MPG_CALL(gemm_w8a8, 8), MPG_CALL(w8a8_dyn, 6),
+                         MPG_CALL(gated, 7), MPG_CALL(gated_backward, 10), MPG_CALL(gated_w8a8, 10), MPG_CALL(gated_w8a8_dyn, 8),
+                         {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

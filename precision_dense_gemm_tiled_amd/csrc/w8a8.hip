@@ -1,0 +1,257 @@
+// The linear layer in 8-bit integers: Y = (A B^T) sa sb + bias with a scale for
+// each token and each output channel; its quantiser and planning.
+//
+// The integer sums are exact; scales and bias are applied in fp32 and the
+// result is rounded once. Tiles: 16x16x64 integer matrix instructions on the
+// main loop of phase_tile.h; few rows: one pass over the weight (linear_device.h).
+#include "linear_device.h"
+
+namespace mpg {
+
+// ------------------------------------------------------------------ quantisation
+
+// One row per workgroup of 64 W threads (W = 1: four rows of one wavefront each): every thread keeps
+// P pieces of 8 elements, 64 W P 8 in all, and the row is read once. P = 0: longer rows, read
+// twice. Bound by memory: the reads of a row are on their way together.
+template <typename T, int W, int P>
+__global__ __launch_bounds__(256) void i8_quantize_kernel(I8Quantize p) {
+    constexpr int NT = 64 * W;
+    const int t = threadIdx.x % NT, lane = threadIdx.x & 63;
+    const int row = W == 1 ? blockIdx.x * 4 + threadIdx.x / 64 : blockIdx.x;
+    if (W == 1 && row >= p.M)
+        return;
+    const T *x = static_cast<const T *>(p.x) + (int64_t)row * p.ldx;
+    int8_t *qr = p.q + (int64_t)row * p.ldq;
+    const bool vec = p.K % 8 == 0 && (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && (p.ldx * (int64_t)sizeof(T)) % 16 == 0;
+    const bool qvec = (reinterpret_cast<uintptr_t>(p.q) & 7) == 0 && p.ldq % 8 == 0;
+    const int end = p.pad ? (p.K + 15) / 16 * 16 : p.K;
+    float v[P > 0 ? P : 1][8];
+    uint32_t m = 0;
+    if constexpr (P > 0) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            i8_load8<T>(x, (i * NT + t) * 8, p.K, vec, v[i]);
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            m = max(m, i8_amax8(v[i]));
+    } else {
+        for (int k0 = t * 8; k0 < p.K; k0 += NT * 8) {
+            i8_load8<T>(x, k0, p.K, vec, v[0]);
+            m = max(m, i8_amax8(v[0]));
+        }
+    }
+    m = lin_wave_max(m);
+    if constexpr (W > 1) {
+        __shared__ uint32_t top[W];
+        if (lane == 0)
+            top[threadIdx.x / 64] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            m = max(m, top[w]);
+    }
+    const I8Row r = i8_row(m);
+    if (t == 0)
+        p.s[row] = r.scale;
+    auto put = [&](int k0, const float (&e)[8]) {
+        if (k0 >= end)
+            return;
+        const uint2 c = i8_codes8(e, r);
+        if (qvec && k0 + 8 <= end) {
+            *reinterpret_cast<uint2 *>(qr + k0) = c;
+        } else {
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+                if (k0 + d < end)
+                    qr[k0 + d] = (int8_t)((d < 4 ? c.x : c.y) >> (8 * (d % 4)));
+        }
+    };
+    if constexpr (P > 0) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            put((i * NT + t) * 8, v[i]);
+    } else {
+        for (int k0 = t * 8; k0 < end; k0 += NT * 8) {
+            i8_load8<T>(x, k0, p.K, vec, v[0]);
+            put(k0, v[0]);
+        }
+    }
+}
+
+template <typename T>
+static void quantize_type(const I8Quantize &p, hipStream_t stream) {
+    const int K = p.K;
+    const dim3 rows((unsigned)p.M), fours((unsigned)((p.M + 3) / 4)), nt(256);
+    if (K <= 512)
+        hipLaunchKernelGGL((i8_quantize_kernel<T, 1, 1>), fours, nt, 0, stream, p);
+    else if (K <= 2048)
+        hipLaunchKernelGGL((i8_quantize_kernel<T, 4, 1>), rows, nt, 0, stream, p);
+    else if (K <= 4096)
+        hipLaunchKernelGGL((i8_quantize_kernel<T, 4, 2>), rows, nt, 0, stream, p);
+    else if (K <= 8192)
+        hipLaunchKernelGGL((i8_quantize_kernel<T, 4, 4>), rows, nt, 0, stream, p);
+    else
+        hipLaunchKernelGGL((i8_quantize_kernel<T, 4, 0>), rows, nt, 0, stream, p);
+}
+
+hipError_t launch_i8_quantize(int type, const I8Quantize &p, hipStream_t stream) {
+    switch (type) {
+    case MPGEMM_TYPE_F16: quantize_type<_Float16>(p, stream); break;
+    case MPGEMM_TYPE_BF16: quantize_type<__bf16>(p, stream); break;
+    default: quantize_type<float>(p, stream); break;
+    }
+    return hipGetLastError();
+}
+
+// 8 elements per thread, 2^LX threads per row piece and the rest of the workgroup's 256 over rows.
+template <typename T, int LX>
+__global__ __launch_bounds__(256) void i8_dequantize_kernel(I8Dequantize p, int per_row) {
+    const int parts = (per_row + (1 << LX) - 1) >> LX;
+    const int rb = blockIdx.x / parts, part = blockIdx.x - rb * parts;
+    const int row = rb * (256 >> LX) + (threadIdx.x >> LX), k0 = ((part << LX) + (threadIdx.x & ((1 << LX) - 1))) * 8;
+    if (row >= p.M || k0 >= p.K)
+        return;
+    const int8_t *q = p.q + (int64_t)row * p.ldq + k0;
+    T *y = static_cast<T *>(p.y) + (int64_t)row * p.ldy + k0;
+    const float s = p.s[row];
+    const bool vec = k0 + 8 <= p.K && (reinterpret_cast<uintptr_t>(p.q) & 7) == 0 && p.ldq % 8 == 0 && lin_vec<T>(p.y, p.ldy);
+    if (vec) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(q);
+        typedef T eight __attribute__((ext_vector_type(8)));
+        eight e;
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+            e[d] = (T)((float)(int8_t)((d < 4 ? w.x : w.y) >> (8 * (d % 4))) * s);
+        *reinterpret_cast<eight *>(y) = e;
+    } else {
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+            if (k0 + d < p.K)
+                y[d] = (T)((float)q[d] * s);
+    }
+}
+
+template <typename T, int LX>
+static void dequantize_one(const I8Dequantize &p, hipStream_t stream) {
+    const int per_row = (p.K + 7) / 8, rows = 256 >> LX;
+    const int64_t blocks = (int64_t)((p.M + rows - 1) / rows) * ((per_row + (1 << LX) - 1) >> LX);
+    hipLaunchKernelGGL((i8_dequantize_kernel<T, LX>), dim3((unsigned)blocks), dim3(256), 0, stream, p, per_row);
+}
+
+template <typename T>
+static void dequantize_type(const I8Dequantize &p, hipStream_t stream) {
+    if (p.K <= 256)
+        dequantize_one<T, 5>(p, stream);
+    else
+        dequantize_one<T, 8>(p, stream);
+}
+
+hipError_t launch_i8_dequantize(int type, const I8Dequantize &p, hipStream_t stream) {
+    switch (type) {
+    case MPGEMM_TYPE_F16: dequantize_type<_Float16>(p, stream); break;
+    case MPGEMM_TYPE_BF16: dequantize_type<__bf16>(p, stream); break;
+    default: dequantize_type<float>(p, stream); break;
+    }
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ copies and fills
+
+// Matrix blockIdx.y's rows, 16 bytes per thread, into rows at multiples of 16 bytes with zeros behind.
+__global__ __launch_bounds__(256) void lin_copy_kernel(LinCopy p) {
+    const int w = blockIdx.y, bytes = p.row_bytes[w], chunks = (bytes + 15) / 16;
+    const int64_t total = (int64_t)p.rows[w] * chunks;
+    for (int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x; f < total; f += (int64_t)gridDim.x * 256) {
+        const int row = (int)(f / chunks), c = (int)(f - (int64_t)row * chunks);
+        const uint8_t *s = p.from[w] + (int64_t)row * p.ldf[w] + 16 * c;
+        *reinterpret_cast<pt_u32x4 *>(p.to[w] + (int64_t)row * p.ldt[w] + 16 * c) = lin_load16_part<uint8_t>(s, bytes - 16 * c);
+    }
+}
+
+hipError_t launch_lin_copy(const LinCopy &p, hipStream_t stream) {
+    int64_t most = 1;
+    int n = 0;
+    for (int w = 0; w < 3; ++w)
+        if (p.to[w]) {
+            const int64_t b = ((int64_t)p.rows[w] * ((p.row_bytes[w] + 15) / 16) + 255) / 256;
+            most = b > most ? b : most;
+            n = w + 1;
+        }
+    hipLaunchKernelGGL(lin_copy_kernel, dim3((unsigned)(most < 4096 ? most : 4096), n), dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
+// Rows of `row_bytes` bytes, each a copy of `row` (or zeros): results of empty sums.
+template <typename T>
+__global__ __launch_bounds__(256) void lin_fill_kernel(T *c, int64_t ldc, int M, int N, const T *row) {
+    const int64_t total = (int64_t)M * N;
+    for (int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x; f < total; f += (int64_t)gridDim.x * 256) {
+        const int m = (int)(f / N), n = (int)(f - (int64_t)m * N);
+        c[(int64_t)m * ldc + n] = row ? row[n] : T(0);
+    }
+}
+
+hipError_t launch_lin_fill(int type, void *c, int64_t ldc, int M, int N, const void *row, hipStream_t stream) {
+    const int64_t blocks = ((int64_t)M * N + 255) / 256;
+    const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));
+    if (type == MPGEMM_TYPE_F32)
+        hipLaunchKernelGGL((lin_fill_kernel<uint32_t>), grid, dim3(256), 0, stream, static_cast<uint32_t *>(c), ldc, M, N,
+                           static_cast<const uint32_t *>(row));
+    else
+        hipLaunchKernelGGL((lin_fill_kernel<uint16_t>), grid, dim3(256), 0, stream, static_cast<uint16_t *>(c), ldc, M, N,
+                           static_cast<const uint16_t *>(row));
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ plan
+
+// Up to 64 rows every workgroup of the skinny kernel reads all activations, and each weight is read once.
+LinPlan plan_lin(int mode, int64_t M, int64_t N, int64_t K, int elem, int cu_count) {
+    LinPlan pl = {LINK_TILE, 0, cu_count};
+    if (K == 0) {
+        pl.kind = LINK_EMPTY;
+        return pl;
+    }
+    if (M <= 64 && (mode == LIN_SCALED || mode == LIN_GATED)) {
+        pl.kind = LINK_SKINNY;
+        pl.cfg = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+        return pl;
+    }
+    double best = 0;
+    for (int c = 0; c < 3; ++c) {
+        const int64_t cn = mode == LIN_GATED ? kLinCfg[c].BN / 2 : kLinCfg[c].BN;
+        const int64_t tiles = ((M + kLinCfg[c].BM - 1) / kLinCfg[c].BM) * ((N + cn - 1) / cn);
+        const double cost = kLinCfg[c].cost * (double)((tiles + cu_count - 1) / cu_count);
+        if (c == 0 || cost < best) {
+            best = cost;
+            pl.cfg = c;
+        }
+    }
+    return pl;
+}
+
+// Few activations: every workgroup of the product quantises all of them.
+bool lin_fuses(const LinPlan &plan, int64_t M, int64_t K) {
+    return plan.kind == LINK_SKINNY && M <= 16 && M * ((K + 511) / 512) <= LIN_X_PIECES * 8;
+}
+
+// ------------------------------------------------------------------ product
+
+hipError_t launch_w8a8(int type, const Lin &p, const LinPlan &plan, hipStream_t stream) {
+    switch (type) {
+    case MPGEMM_TYPE_F16: return lin_run<PtI8, _Float16, LIN_SCALED>(p, plan, stream);
+    case MPGEMM_TYPE_BF16: return lin_run<PtI8, __bf16, LIN_SCALED>(p, plan, stream);
+    default: return lin_run<PtI8, float, LIN_SCALED>(p, plan, stream);
+    }
+}
+
+hipError_t launch_w8a8_x(int type, const Lin &p, const LinX &x, const LinPlan &plan, hipStream_t stream) {
+    switch (type) {
+    case MPGEMM_TYPE_F16: lin_skinny_one<PtI8, _Float16, LIN_SCALED, 1, 1, true>(p, x, stream); break;
+    case MPGEMM_TYPE_BF16: lin_skinny_one<PtI8, __bf16, LIN_SCALED, 1, 1, true>(p, x, stream); break;
+    default: lin_skinny_one<PtI8, float, LIN_SCALED, 1, 1, true>(p, x, stream); break;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace mpg
