@@ -396,12 +396,14 @@ int64_t mpgemm_run_newton_schulz_workspace(int64_t batch, int64_t M, int64_t N);
  * memory from the caller: 16-byte aligned, at least the bytes that the matching
  * _workspace call returns (-1 for sizes that the call refuses; NULL when that is
  * 0), so calls that share a handle may run on several streams at once.
- * Operands may have any (element) alignment and row stride. Above 64 rows, operands
+ * Operands may have any (element) alignment and row stride. Above 32 rows, operands
  * whose rows do not start at multiples of 16 bytes (or lie 2^23 bytes apart, or
  * more) are copied into the workspace first, one launch more: a program that keeps
- * its weights in padded rows saves that. `aligned` of a _workspace call: nonzero where
- * no operand needs that copy (of mpgemm_run_gated_backward: and Wg and Wu have
- * the same row stride). Sizes: K of integer products <= MPGEMM_MAX_K_INT, of 16-bit ones
+ * its weights in padded rows saves that. So are, of the forward products, 16-bit operands with
+ * K not a multiple of 8, and held activations with K not a multiple of 16. `aligned` of a
+ * _workspace call: nonzero where all rows start at multiples of 16 bytes less than 2^23 apart
+ * (of mpgemm_run_gated_backward: and Wg and Wu have the same row stride; of the _dyn
+ * calls X does not matter). Sizes: K of integer products <= MPGEMM_MAX_K_INT, of 16-bit ones
  * (and 2 N of the backward pass) <= MPGEMM_MAX_ALONG_LINEAR, all others <=
  * MPGEMM_MAX_DIM_LINEAR, else MPGEMM_ERR_UNSUPPORTED. Results are bit-identical
  * from call to call. Everything else is the common contract above. */

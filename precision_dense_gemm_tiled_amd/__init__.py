@@ -732,7 +732,7 @@ def newton_schulz(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out=No
 # A matrix in 8-bit integers is a pair: codes (R x K int8) and R float32 scales, one
 # for each row (a token, or an output channel of a weight). quantize_i8 returns codes
 # whose rows are padded to 16 bytes; others (a copy that has lost the padding) are taken
-# too, and above 64 rows copied in the call. As the MXFP4 calls, none of these takes
+# too, and above 32 rows copied in the call. As the MXFP4 calls, none of these takes
 # part in autograd: they raise where a gradient would be lost.
 
 

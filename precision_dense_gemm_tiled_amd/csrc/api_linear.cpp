@@ -66,14 +66,15 @@ bool sizes_ok(int64_t M, int64_t N, int64_t K, int64_t along) {
 }
 
 // An operand of a tile kernel: its rows as they are, or a copy in the workspace where they do
-// not start at multiples of 16 bytes or lie too far apart.
+// not start at multiples of 16 bytes, lie too far apart, or (padded) end inside 16 bytes that have to
+// hold zeros behind them.
 struct Operand {
     const uint8_t *p;
     int64_t ld, rows, bytes;   // ld and bytes of a row, in bytes
-    bool copied = false;
-    Operand(const void *at, int64_t stride, int64_t r, int64_t row_bytes)
-        : p(static_cast<const uint8_t *>(at)), ld(r <= 1 ? round_up(row_bytes, 16) : stride), rows(r), bytes(row_bytes) {}
-    bool needs_copy() const { return misaligned(p, 16) || ld % 16 != 0 || ld >= kMaxStride; }
+    bool padded;
+    Operand(const void *at, int64_t stride, int64_t r, int64_t row_bytes, bool pad)
+        : p(static_cast<const uint8_t *>(at)), ld(r <= 1 ? round_up(row_bytes, 16) : stride), rows(r), bytes(row_bytes), padded(pad) {}
+    bool needs_copy() const { return misaligned(p, 16) || ld % 16 != 0 || ld >= kMaxStride || (padded && bytes % 16 != 0); }
     int64_t copy_bytes() const { return round_up(rows * round_up(bytes, 16), 256); }
 };
 
@@ -97,7 +98,6 @@ struct Copies {
         ws += o.copy_bytes();
         o.p = c.to[n];
         o.ld = c.ldt[n];
-        o.copied = true;
         ++n;
     }
     hipError_t launch(hipStream_t stream) const { return n ? mpg::launch_lin_copy(c, stream) : hipSuccess; }
@@ -115,7 +115,7 @@ int64_t copy_of(int64_t rows, int64_t row_bytes) { return round_up(rows * round_
 // Scratch of activations quantised by a launch before the product: codes, then scales.
 struct Codes {
     int64_t ld, s_at, bytes;
-    Codes(int64_t M, int64_t K) : ld(round_up(K, 16)), s_at(round_up(M * ld, 256)), bytes(s_at + round_up(4 * M, 256)) {}
+    Codes(int64_t M, int64_t K) : ld(round_up(K, 128)), s_at(round_up(M * ld, 256)), bytes(s_at + round_up(4 * M, 256)) {}
 };
 
 mpg::Lin product(int64_t M, int64_t N, int64_t K, void *C, int64_t ldc) {
@@ -179,10 +179,10 @@ mpgemm_status_t run_i8(mpgemm_handle_t h, const I8Args &a, bool dyn, void *works
     if (!h)
         return MPGEMM_ERR_INVALID_ARG;
     const int mode = a.gated ? mpg::LIN_GATED : mpg::LIN_SCALED;
-    const mpg::LinPlan plan = mpg::plan_lin(mode, a.M, a.N, a.K, mpg::LIN_I8, h->cu_count);
+    const mpg::LinPlan plan = mpg::plan_lin(mode, a.M, a.N, a.K, h->cu_count);
     const bool fused = dyn && mpg::lin_fuses(plan, a.M, a.K), tile = plan.kind == mpg::LINK_TILE;
     const Codes codes(a.M, a.K);
-    Operand oa(a.A, a.lda, a.M, a.K), ob(a.B[0], a.ldb[0], a.N, a.K), oc(a.B[1], a.ldb[1], a.N, a.K);
+    Operand oa(a.A, a.lda, a.M, a.K, true), ob(a.B[0], a.ldb[0], a.N, a.K, false), oc(a.B[1], a.ldb[1], a.N, a.K, false);
     const int64_t own = dyn && !fused && plan.kind != mpg::LINK_EMPTY ? codes.bytes : 0;
     int64_t need = own;
     if (tile)
@@ -203,9 +203,8 @@ mpgemm_status_t run_i8(mpgemm_handle_t h, const I8Args &a, bool dyn, void *works
         const hipError_t e = mpg::launch_i8_quantize(a.type, q, s);
         if (e != hipSuccess)
             return MPGEMM_ERR_HIP;
-        oa = Operand(ws, codes.ld, a.M, a.K);
+        oa = Operand(ws, codes.ld, a.M, a.K, false);   // (padded as it is)
         p.sa = scales;
-        p.apad = true;
     } else if (!dyn) {
         p.sa = a.SA;
     }
@@ -218,7 +217,6 @@ mpgemm_status_t run_i8(mpgemm_handle_t h, const I8Args &a, bool dyn, void *works
         const hipError_t e = c.launch(s);
         if (e != hipSuccess)
             return MPGEMM_ERR_HIP;
-        p.apad = p.apad || oa.copied;
     }
     p.a = oa.p;
     p.lda = oa.ld;
@@ -242,10 +240,12 @@ int64_t workspace_i8(int64_t M, int64_t N, int64_t K, bool gated, bool dyn, int 
         return -1;
     if (M == 0 || N == 0 || K == 0)
         return 0;
-    const mpg::LinPlan plan = mpg::plan_lin(gated ? mpg::LIN_GATED : mpg::LIN_SCALED, M, N, K, mpg::LIN_I8, cu_count);
+    const mpg::LinPlan plan = mpg::plan_lin(gated ? mpg::LIN_GATED : mpg::LIN_SCALED, M, N, K, cu_count);
     int64_t n = dyn && !mpg::lin_fuses(plan, M, K) ? Codes(M, K).bytes : 0;
+    if (plan.kind == mpg::LINK_TILE && !dyn && (!aligned || K % 16 != 0))
+        n += copy_of(M, K);
     if (plan.kind == mpg::LINK_TILE && !aligned)
-        n += (dyn ? 0 : copy_of(M, K)) + (gated ? 2 : 1) * copy_of(N, K);
+        n += (gated ? 2 : 1) * copy_of(N, K);
     return n;
 }
 
@@ -362,8 +362,8 @@ mpgemm_status_t mpgemm_run_gated(mpgemm_handle_t h, int64_t M, int64_t N, int64_
         return st;
     if (!h)
         return MPGEMM_ERR_INVALID_ARG;
-    const mpg::LinPlan plan = mpg::plan_lin(mpg::LIN_GATED, M, N, K, mpg::LIN_BF16, h->cu_count);
-    Operand ox(X, 2 * ldx, M, 2 * K), og(Wg, 2 * ldwg, N, 2 * K), ou(Wu, 2 * ldwu, N, 2 * K);
+    const mpg::LinPlan plan = mpg::plan_lin(mpg::LIN_GATED, M, N, K, h->cu_count);
+    Operand ox(X, 2 * ldx, M, 2 * K, true), og(Wg, 2 * ldwg, N, 2 * K, true), ou(Wu, 2 * ldwu, N, 2 * K, true);
     const bool tile = plan.kind == mpg::LINK_TILE;
     if ((st = check_workspace(workspace, workspace_bytes, tile ? copies_of({&ox, &og, &ou}) : 0)) != MPGEMM_OK)
         return st;
@@ -387,8 +387,6 @@ mpgemm_status_t mpgemm_run_gated(mpgemm_handle_t h, int64_t M, int64_t N, int64_
         c.add(ou);
         if (c.launch(s) != hipSuccess)
             return MPGEMM_ERR_HIP;
-        p.apad = ox.copied;
-        p.bpad = og.copied && ou.copied;
     }
     p.a = ox.p;
     p.lda = ox.ld;
@@ -407,7 +405,7 @@ mpgemm_status_t mpgemm_run_gated(mpgemm_handle_t h, int64_t M, int64_t N, int64_
 int64_t mpgemm_run_gated_workspace(int64_t M, int64_t N, int64_t K, int aligned, int cu_count) {
     if (cu_count <= 0 || !sizes_ok(M, N, K, kMaxAlong))
         return -1;
-    if (M == 0 || N == 0 || K == 0 || aligned || mpg::plan_lin(mpg::LIN_GATED, M, N, K, mpg::LIN_BF16, cu_count).kind != mpg::LINK_TILE)
+    if (M == 0 || N == 0 || K == 0 || (aligned && K % 8 == 0) || mpg::plan_lin(mpg::LIN_GATED, M, N, K, cu_count).kind != mpg::LINK_TILE)
         return 0;
     return copy_of(M, 2 * K) + 2 * copy_of(N, 2 * K);
 }
@@ -443,7 +441,7 @@ mpgemm_status_t mpgemm_run_gated_backward(mpgemm_handle_t h, int64_t M, int64_t 
     if (!h)
         return MPGEMM_ERR_INVALID_ARG;
     const int64_t part = part_of(N), d_bytes = round_up(M * 2 * part * 2, 256);
-    Operand ox(X, 2 * ldx, M, 2 * K), og(Wg, 2 * ldwg, N, 2 * K), ou(Wu, 2 * ldwu, N, 2 * K);
+    Operand ox(X, 2 * ldx, M, 2 * K, false), og(Wg, 2 * ldwg, N, 2 * K, false), ou(Wu, 2 * ldwu, N, 2 * K, false);
     // (both weights go through the same offsets: they have to have one row stride)
     const bool strides = og.ld == ou.ld, copy_w = need_dx && (og.needs_copy() || ou.needs_copy() || !strides);
     int64_t need = sums ? d_bytes : 0;
@@ -478,29 +476,21 @@ mpgemm_status_t mpgemm_run_gated_backward(mpgemm_handle_t h, int64_t M, int64_t 
     const mpg::GatedGrads gp{dH, G, U, lddh, ldg, ldu, ws, (int)M, (int)N, (int)part, act};
     if (mpg::launch_gated_grads(type, gp, s) != hipSuccess)
         return MPGEMM_ERR_HIP;
-    hipError_t e = hipSuccess;
-    if (need_dx) {
-        mpg::Lin p = product(M, K, N, dX, lddx);
-        p.a = ws;
-        p.lda = 2 * part * 2;
-        p.b[0] = og.p;
-        p.b[1] = ou.p;
-        p.ldb[0] = p.ldb[1] = og.ld;
-        p.part = (int)part;
-        e = mpg::launch_gated_dx(type, p, mpg::plan_lin(mpg::LIN_DX, M, K, N, mpg::LIN_BF16, h->cu_count), s);
-    }
-    if (need_dw && e == hipSuccess) {
-        mpg::Lin p = product(N, K, M, dWg, lddwg);
-        p.c2 = dWu;
-        p.ldc2 = lddwu;
-        p.a = ws;
-        p.lda = 2 * part * 2;
-        p.b[0] = ox.p;
-        p.ldb[0] = ox.ld;
-        p.part = (int)part;
-        e = mpg::launch_gated_dw(type, p, mpg::plan_lin(mpg::LIN_DW, 2 * part, K, M, mpg::LIN_BF16, h->cu_count), s);
-    }
-    return status_of(e);
+    mpg::Lin x = product(M, K, N, dX, lddx), w = product(N, K, M, dWg, lddwg);
+    x.a = w.a = ws;
+    x.lda = w.lda = 2 * part * 2;
+    x.part = w.part = (int)part;
+    x.b[0] = og.p;
+    x.b[1] = ou.p;
+    x.ldb[0] = x.ldb[1] = og.ld;
+    w.c2 = dWu;
+    w.ldc2 = lddwu;
+    w.b[0] = ox.p;
+    w.ldb[0] = ox.ld;
+    if (need_dx && need_dw)
+        return status_of(mpg::launch_gated_pair(type, x, w, mpg::plan_lin_pair(M, part, K, h->cu_count), s));
+    return status_of(need_dx ? mpg::launch_gated_dx(type, x, mpg::plan_lin(mpg::LIN_DX, M, K, N, h->cu_count), s)
+                             : mpg::launch_gated_dw(type, w, mpg::plan_lin(mpg::LIN_DW, 2 * part, K, M, h->cu_count), s));
 }
 
 int64_t mpgemm_run_gated_backward_workspace(int64_t M, int64_t N, int64_t K, int aligned, int cu_count) {

@@ -10,12 +10,14 @@
 
 namespace mpg {
 
-// 8 columns of a row per thread. Bound by memory: 10 bytes per element of dH.
+// 8 columns of a row per thread, 2^lx threads side by side in a row (a power of two: no division by a
+// row's pieces), the rest of the workgroup's 256 over rows. Bound by memory: 10 bytes per element of dH.
 template <typename T, int ACT>
-__global__ __launch_bounds__(256) void gated_grads_kernel(GatedGrads p) {
-    const int per_row = p.part / 8, parts = (per_row + 255) / 256;
-    const int m = blockIdx.x / parts, n0 = ((blockIdx.x - m * parts) * 256 + (int)threadIdx.x) * 8;
-    if (n0 >= p.part)
+__global__ __launch_bounds__(256) void gated_grads_kernel(GatedGrads p, int lx) {
+    const int parts = (p.part / 8 + (1 << lx) - 1) >> lx, rb = blockIdx.x / parts;
+    const int m = rb * (256 >> lx) + (threadIdx.x >> lx);
+    const int n0 = (((blockIdx.x - rb * parts) << lx) + (threadIdx.x & ((1 << lx) - 1))) * 8;
+    if (n0 >= p.part || m >= p.M)
         return;
     typedef T eight __attribute__((ext_vector_type(8)));
     const T *dh = static_cast<const T *>(p.dh) + (int64_t)m * p.lddh, *g = static_cast<const T *>(p.g) + (int64_t)m * p.ldg,
@@ -49,13 +51,17 @@ __global__ __launch_bounds__(256) void gated_grads_kernel(GatedGrads p) {
 
 template <typename T>
 static void grads_type(const GatedGrads &p, hipStream_t stream) {
-    const dim3 grid((unsigned)p.M * (unsigned)((p.part / 8 + 255) / 256)), nt(256);
+    int lx = 3;   // (part is a multiple of 64)
+    while (lx < 8 && p.part / 8 % (2 << lx) == 0)
+        ++lx;
+    const int rows = 256 >> lx;
+    const dim3 grid((unsigned)((p.M + rows - 1) / rows) * (unsigned)((p.part / 8) >> lx)), nt(256);
     if (p.act == MPGEMM_ACT_SILU)
-        hipLaunchKernelGGL((gated_grads_kernel<T, MPGEMM_ACT_SILU>), grid, nt, 0, stream, p);
+        hipLaunchKernelGGL((gated_grads_kernel<T, MPGEMM_ACT_SILU>), grid, nt, 0, stream, p, lx);
     else if (p.act == MPGEMM_ACT_GELU)
-        hipLaunchKernelGGL((gated_grads_kernel<T, MPGEMM_ACT_GELU>), grid, nt, 0, stream, p);
+        hipLaunchKernelGGL((gated_grads_kernel<T, MPGEMM_ACT_GELU>), grid, nt, 0, stream, p, lx);
     else
-        hipLaunchKernelGGL((gated_grads_kernel<T, MPGEMM_ACT_GELU_TANH>), grid, nt, 0, stream, p);
+        hipLaunchKernelGGL((gated_grads_kernel<T, MPGEMM_ACT_GELU_TANH>), grid, nt, 0, stream, p, lx);
 }
 
 hipError_t launch_gated_grads(int type, const GatedGrads &p, hipStream_t stream) {
@@ -64,6 +70,43 @@ hipError_t launch_gated_grads(int type, const GatedGrads &p, hipStream_t stream)
     else
         grads_type<__bf16>(p, stream);
     return hipGetLastError();
+}
+
+// Both products in one grid, first the tiles of dX, whose sums are longer: dW's run beside them and
+// a launch less is waited for (777 x 1000 x 520, f16: PAIRUS).
+template <class E, typename OUT, int BM, int BN, int WGM, int WGN, int NS>
+__global__ __launch_bounds__(64 * WGM * WGN) void gated_pair_kernel(Lin dx, Lin dw, int first) {
+    typedef LinTile<E, OUT, LIN_DX, BM, BN, WGM, WGN, NS> X;
+    typedef LinTile<E, OUT, LIN_DW, BM, BN, WGM, WGN, NS> W;
+    static_assert(X::PT::LDS_BYTES == W::PT::LDS_BYTES, "one buffer");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[X::PT::LDS_BYTES];
+    if ((int)blockIdx.x < first)
+        X::run(dx, blockIdx.x, first, smem);
+    else
+        W::run(dw, blockIdx.x - first, gridDim.x - first, smem);
+}
+
+template <class E, typename OUT, int BM, int BN, int WGM, int WGN, int NS>
+static void pair_one(const Lin &dx, const Lin &dw, hipStream_t stream) {
+    typedef LinTile<E, OUT, LIN_DX, BM, BN, WGM, WGN, NS> X;
+    typedef LinTile<E, OUT, LIN_DW, BM, BN, WGM, WGN, NS> W;
+    const int first = X::tiles_m(dx) * X::tiles_n(dx);
+    hipLaunchKernelGGL((gated_pair_kernel<E, OUT, BM, BN, WGM, WGN, NS>), dim3((unsigned)first + (unsigned)W::tiles_m(dw) * (unsigned)W::tiles_n(dw)),
+                       dim3(64 * WGM * WGN), 0, stream, dx, dw, first);
+}
+
+template <class E, typename OUT>
+static hipError_t pair_type(const Lin &dx, const Lin &dw, const LinPlan &plan, hipStream_t stream) {
+    switch (plan.cfg) {
+    case 0: pair_one<E, OUT, 256, 256, 2, 4, 2>(dx, dw, stream); break;
+    case 1: pair_one<E, OUT, 128, 128, 2, 2, 2>(dx, dw, stream); break;
+    default: pair_one<E, OUT, 64, 64, 2, 2, 4>(dx, dw, stream); break;
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_gated_pair(int type, const Lin &dx, const Lin &dw, const LinPlan &plan, hipStream_t stream) {
+    return type == MPGEMM_TYPE_F16 ? pair_type<PtF16, _Float16>(dx, dw, plan, stream) : pair_type<PtBF16, __bf16>(dx, dw, plan, stream);
 }
 
 hipError_t launch_gated_dx(int type, const Lin &p, const LinPlan &plan, hipStream_t stream) {

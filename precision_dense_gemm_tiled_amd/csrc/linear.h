@@ -32,7 +32,8 @@ struct I8Dequantize {
 };
 hipError_t launch_i8_dequantize(int type, const I8Dequantize &p, hipStream_t stream);
 
-// What a product of the layers computes from A (M x K, along k) and B:
+// What a product of the layers computes from A (M x K, along k) and B. The tile kernels take rows at
+// multiples of 16 bytes, and along k zeros from K to the next multiple (of integers in A alone):
 //   SCALED  int8: C = (A B^T) sa sb + bias
 //   GATED   C = act(A B0^T) (A B1^T), of int8 operands each product scaled; G and U where wanted
 //   DX      C = A [B0; B1], A M x 2 Kp, B0 and B1 K x N (across k), K of each
@@ -50,11 +51,7 @@ struct Lin {
     int M, N, K;             // of the result; of the sum (DX: of one of its two parts)
     int part;                // (DX, DW) the columns of A that belong to the first part, padding included
     int act;
-    bool apad, bpad;         // the rows of A, of B are zeros from K to the next multiple of 16 bytes
 };
-
-// Element types of the operands.
-enum LinElem { LIN_F16 = 0, LIN_BF16 = 1, LIN_I8 = 2 };
 
 enum LinKind { LINK_EMPTY = 0, LINK_SKINNY = 1, LINK_TILE = 2 };
 struct LinPlan {
@@ -62,14 +59,15 @@ struct LinPlan {
     int cfg;    // skinny: fragments of 16 rows; tile: index of the tile table
     int cus;
 };
-LinPlan plan_lin(int mode, int64_t M, int64_t N, int64_t K, int elem, int cu_count);
-// Whether the product reads its operands with 16-byte loads from 16-byte aligned rows only.
-inline bool lin_needs_aligned(const LinPlan &p) { return p.kind == LINK_TILE; }
+LinPlan plan_lin(int mode, int64_t M, int64_t N, int64_t K, int cu_count);
+LinPlan plan_lin_pair(int64_t M, int64_t part, int64_t K, int cu_count);
 hipError_t launch_w8a8(int type, const Lin &p, const LinPlan &plan, hipStream_t stream);
 hipError_t launch_gated_w8a8(int type, const Lin &p, const LinPlan &plan, hipStream_t stream);
 hipError_t launch_gated(int type, const Lin &p, const LinPlan &plan, hipStream_t stream);
 hipError_t launch_gated_dx(int type, const Lin &p, const LinPlan &plan, hipStream_t stream);
 hipError_t launch_gated_dw(int type, const Lin &p, const LinPlan &plan, hipStream_t stream);
+// Both in one launch.
+hipError_t launch_gated_pair(int type, const Lin &dx, const Lin &dw, const LinPlan &plan, hipStream_t stream);
 
 // Few activations, quantised by every workgroup of the product itself.
 bool lin_fuses(const LinPlan &plan, int64_t M, int64_t K);

@@ -191,74 +191,80 @@ __device__ __forceinline__ void lin_epilogue(const Lin &p, int row0, int col0, i
     }
 }
 
-// One tile per workgroup. GATED: a tile's columns are BN / 2 of either weight.
-template <class E, typename OUT, int MODE, int BM, int BN, int WGM, int WGN>
-__global__ __launch_bounds__(64 * WGM * WGN) void lin_tile_kernel(Lin p, int tiles_m, int tiles_n) {
-    constexpr bool AC = MODE == LIN_DW, BC = MODE == LIN_DX || MODE == LIN_DW;
-    typedef PhaseTile<E, BM, BN, WGM, WGN, AC, BC, MODE == LIN_DX> PT;
-    constexpr int EB = sizeof(typename E::T), CN = MODE == LIN_GATED ? BN / 2 : BN;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[PT::LDS_BYTES];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int tm, tn;
-    lin_tile_of(blockIdx.x, gridDim.x, tiles_m, tiles_n, tm, tn);
-    const int row0 = tm * BM, col0 = tn * CN;
-    const int arows = MODE == LIN_DW ? 2 * p.part : p.M;
-    PtSource A, B;
+// Tile `bid` of a grid of `nblk`. GATED: a tile's columns are BN / 2 of either weight.
+template <class E, typename OUT, int MODE, int BM, int BN, int WGM, int WGN, int NS>
+struct LinTile {
+    static constexpr bool AC = MODE == LIN_DW, BC = MODE == LIN_DX || MODE == LIN_DW;
+    typedef PhaseTile<E, BM, BN, WGM, WGN, NS, AC, BC, MODE == LIN_DX> PT;
+    static constexpr int EB = sizeof(typename E::T), CN = MODE == LIN_GATED ? BN / 2 : BN;
+
+    static __host__ __device__ int rows(const Lin &p) { return MODE == LIN_DW ? 2 * p.part : p.M; }
+    static __host__ __device__ int tiles_m(const Lin &p) { return (rows(p) + BM - 1) / BM; }
+    static __host__ __device__ int tiles_n(const Lin &p) { return (p.N + CN - 1) / CN; }
+
+    static __device__ __forceinline__ void run(const Lin &p, int bid, int nblk, uint8_t *smem) {
+        const int tid = threadIdx.x, lane = tid & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        int tm, tn;
+        lin_tile_of(bid, nblk, tiles_m(p), tiles_n(p), tm, tn);
+        const int row0 = tm * BM, col0 = tn * CN;
+        PtSource A, B;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int ra = row0 + h * PT::HM, rb = MODE == LIN_GATED ? col0 : col0 + h * PT::HN;
-        A.p[h] = p.a + (AC ? (int64_t)ra * EB : (int64_t)ra * p.lda);
-        A.rows[h] = arows - ra;
-        A.ld[h] = p.lda;
-        const int w = MODE == LIN_GATED ? h : 0;
-        B.p[h] = p.b[w] + (BC ? (int64_t)rb * EB : (int64_t)rb * p.ldb[w]);
-        B.next[h] = MODE == LIN_DX ? p.b[1] + (int64_t)rb * EB : nullptr;
-        B.rows[h] = p.N - rb;
-        B.ld[h] = p.ldb[w];
+        for (int h = 0; h < 2; ++h) {
+            const int ra = row0 + h * PT::HM, rb = MODE == LIN_GATED ? col0 : col0 + h * PT::HN;
+            A.p[h] = p.a + (AC ? (int64_t)ra * EB : (int64_t)ra * p.lda);
+            A.rows[h] = rows(p) - ra;
+            A.ld[h] = p.lda;
+            const int w = MODE == LIN_GATED ? h : 0;
+            B.p[h] = p.b[w] + (BC ? (int64_t)rb * EB : (int64_t)rb * p.ldb[w]);
+            B.next[h] = MODE == LIN_DX ? p.b[1] + (int64_t)rb * EB : nullptr;
+            B.rows[h] = p.N - rb;
+            B.ld[h] = p.ldb[w];
+        }
+        const int chunks = BC ? p.K : (p.K * EB + 15) / 16;
+        A.chunks = MODE == LIN_DX ? 2 * p.part / 8 : chunks;
+        B.chunks = chunks;
+        B.split = p.part / 64;
+        const int stages = MODE == LIN_DX ? 2 * p.part / 64 : BC ? (p.K + 63) / 64 : (chunks + 7) / 8;
+        typename E::Acc acc[2][2][PT::FM][PT::FN];
+        PT::mainloop(A, B, stages, smem, tid, lane, wave, acc);
+        if constexpr (MODE == LIN_GATED) {
+            if (p.act == MPGEMM_ACT_SILU)
+                lin_epilogue<E, OUT, MODE, MPGEMM_ACT_SILU, PT>(p, row0, col0, lane, wave, acc);
+            else if (p.act == MPGEMM_ACT_GELU)
+                lin_epilogue<E, OUT, MODE, MPGEMM_ACT_GELU, PT>(p, row0, col0, lane, wave, acc);
+            else
+                lin_epilogue<E, OUT, MODE, MPGEMM_ACT_GELU_TANH, PT>(p, row0, col0, lane, wave, acc);
+        } else {
+            lin_epilogue<E, OUT, MODE, 0, PT>(p, row0, col0, lane, wave, acc);
+        }
     }
-    // Of a last chunk that K ends in, zeros in A's padding are enough for integers; in 16 bits B's
-    // padding could hold a NaN, and has to be zeros too.
-    const bool whole = p.apad && (EB == 1 || p.bpad);
-    const int chunks = BC ? p.K : whole ? (p.K * EB + 15) / 16 : p.K * EB / 16;
-    A.chunks = MODE == LIN_DX ? 2 * p.part / 8 : chunks;
-    B.chunks = chunks;
-    B.split = p.part / 64;
-    const int stages = MODE == LIN_DX ? 2 * p.part / 64 : BC ? (p.K + 63) / 64 : (chunks + 7) / 8;
-    typename E::Acc acc[2][2][PT::FM][PT::FN];
-    PT::mainloop(A, B, stages, smem, tid, lane, wave, acc);
-    if (!BC && !whole && p.K * EB % 16 != 0)
-        PT::tail(A, B, p.K * EB, lane, wave, acc);
-    if constexpr (MODE == LIN_GATED) {
-        if (p.act == MPGEMM_ACT_SILU)
-            lin_epilogue<E, OUT, MODE, MPGEMM_ACT_SILU, PT>(p, row0, col0, lane, wave, acc);
-        else if (p.act == MPGEMM_ACT_GELU)
-            lin_epilogue<E, OUT, MODE, MPGEMM_ACT_GELU, PT>(p, row0, col0, lane, wave, acc);
-        else
-            lin_epilogue<E, OUT, MODE, MPGEMM_ACT_GELU_TANH, PT>(p, row0, col0, lane, wave, acc);
-    } else {
-        lin_epilogue<E, OUT, MODE, 0, PT>(p, row0, col0, lane, wave, acc);
-    }
+};
+
+template <class E, typename OUT, int MODE, int BM, int BN, int WGM, int WGN, int NS>
+__global__ __launch_bounds__(64 * WGM * WGN) void lin_tile_kernel(Lin p) {
+    typedef LinTile<E, OUT, MODE, BM, BN, WGM, WGN, NS> LT;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[LT::PT::LDS_BYTES];
+    LT::run(p, blockIdx.x, gridDim.x, smem);
 }
 
 // The tile table, and what a round of tiles over all CUs costs against the others.
 struct LinCfg { int BM, BN; double cost; };
 static const LinCfg kLinCfg[] = {{256, 256, 4.0}, {128, 128, 1.25}, {64, 64, 0.5}};
 
-template <class E, typename OUT, int MODE, int BM, int BN, int WGM, int WGN>
+template <class E, typename OUT, int MODE, int BM, int BN, int WGM, int WGN, int NS>
 static void lin_tile_one(const Lin &p, hipStream_t stream) {
-    const int rows = MODE == LIN_DW ? 2 * p.part : p.M, cn = MODE == LIN_GATED ? BN / 2 : BN;
-    const int tm = (rows + BM - 1) / BM, tn = (p.N + cn - 1) / cn;
-    hipLaunchKernelGGL((lin_tile_kernel<E, OUT, MODE, BM, BN, WGM, WGN>), dim3((unsigned)tm * (unsigned)tn), dim3(64 * WGM * WGN),
-                       0, stream, p, tm, tn);
+    typedef LinTile<E, OUT, MODE, BM, BN, WGM, WGN, NS> LT;
+    hipLaunchKernelGGL((lin_tile_kernel<E, OUT, MODE, BM, BN, WGM, WGN, NS>), dim3((unsigned)LT::tiles_m(p) * (unsigned)LT::tiles_n(p)),
+                       dim3(64 * WGM * WGN), 0, stream, p);
 }
 
 template <class E, typename OUT, int MODE>
 static void lin_tile(const Lin &p, const LinPlan &plan, hipStream_t stream) {
     switch (plan.cfg) {
-    case 0: lin_tile_one<E, OUT, MODE, 256, 256, 2, 4>(p, stream); break;
-    case 1: lin_tile_one<E, OUT, MODE, 128, 128, 2, 2>(p, stream); break;
-    default: lin_tile_one<E, OUT, MODE, 64, 64, 2, 2>(p, stream); break;
+    case 0: lin_tile_one<E, OUT, MODE, 256, 256, 2, 4, 2>(p, stream); break;
+    case 1: lin_tile_one<E, OUT, MODE, 128, 128, 2, 2, 2>(p, stream); break;
+    default: lin_tile_one<E, OUT, MODE, 64, 64, 2, 2, 4>(p, stream); break;
     }
 }
 
@@ -291,12 +297,17 @@ __device__ __forceinline__ pt_u32x4 lin_load16_part(const uint8_t *s, int left) 
     return v;
 }
 
-// Largest magnitude as an fp32 bit pattern (NaN over infinity over finite), joined over a wavefront.
+// Largest magnitude as an fp32 bit pattern (NaN over infinity over finite), joined over a wavefront: within
+// rows of 16 lanes by DPP, then over the rows by lane swaps.
 __device__ __forceinline__ uint32_t lin_wave_max(uint32_t v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        v = max(v, (uint32_t)__shfl_xor((int)v, d));
-    return v;
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));    // lanes 1 0 3 2
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));    // lanes 2 3 0 1
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));   // half rows mirrored
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));   // rows mirrored
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return max(b[0], b[1]);
 }
 
 // Scale and how a row is divided by it: values and scale go through 2^up, exact, where the scale
@@ -372,8 +383,8 @@ constexpr int LIN_X_PIECES = 4;   // pieces of 8 activations that a thread of th
 // Up to 64 rows: 16 MF rows x 16 NF columns (of each weight) per workgroup, operands straight from memory
 // into the matrix unit's registers, which read each weight once; K in groups of 256 bytes dealt out to the
 // 8 wavefronts in turn. At step s of a group, lane quarter q takes bytes 64 s + 16 q of its row, so that a
-// load instruction reads 64 contiguous bytes of each of 16 rows. B of the next group is on its way
-// during a group. The wavefronts' sums are joined in LDS in the order of the wavefronts.
+// load instruction reads 64 contiguous bytes of each of 16 rows. The next two groups are on their way
+// from the start on. The wavefronts' sums are joined in LDS in the order of the wavefronts.
 // X: the activations are quantised by every workgroup (MF = 1, few of them).
 template <class E, typename OUT, int MODE, int MF, int NF, bool X>
 __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
@@ -411,18 +422,32 @@ __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
         }
     };
 
-    pt_u32x4 bv[NB][NF][4], bn[NB][NF][4];
-    auto load_b = [&](int g, pt_u32x4 (&v)[NB][NF][4]) {
+    // A group's operands (the activations that the kernel has quantised stay in LDS).
+    struct Group {
+        pt_u32x4 b[NB][NF][4], a[X ? 1 : MF][4];
+    } g0, g1;
+    auto load_group = [&](int g, Group &v) {
 #pragma unroll
         for (int w = 0; w < NB; ++w)
 #pragma unroll
             for (int j = 0; j < NF; ++j)
-                load(b[w][j], g, v[w][j]);
+                load(b[w][j], g, v.b[w][j]);
+        if constexpr (!X) {
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+                load(a[i], g, v.a[i]);
+        }
+    };
+    auto first_groups = [&]() {
+        if (wave < full)
+            load_group(wave, g0);
+        if (wave + NW < full)
+            load_group(wave + NW, g1);
     };
     // the activations' codes: rows of `codes_ld` bytes (a multiple of 512, and 16 so that rows start at different banks)
     uint8_t *codes = smem + sizeof(Num) * NW * MF * NB * NF * 256;
     const int per_row = (p.K + 511) / 512 * 64, codes_ld = per_row * 8 + 16;
-    float *scales = reinterpret_cast<float *>(codes + 16 * 0 + (size_t)p.M * codes_ld);
+    float *scales = reinterpret_cast<float *>(codes + (size_t)p.M * codes_ld);
     if constexpr (X) {
         typedef OUT T;
         uint32_t *top = reinterpret_cast<uint32_t *>(scales + 16);
@@ -434,8 +459,7 @@ __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
             if (row < p.M)   // (the same row for a whole wavefront)
                 i8_load8<T>(static_cast<const T *>(px.x) + (int64_t)row * px.ldx, (f - row * per_row) * 8, p.K, vec, v[i]);
         }
-        if (wave < full)
-            load_b(wave, bv);   // (behind the activations: loads return in order)
+        first_groups();   // (behind the activations: loads return in order)
         if (tid < 16)
             top[tid] = 0;
         __syncthreads();
@@ -461,8 +485,7 @@ __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
         }
         __syncthreads();
     } else {
-        if (wave < full)
-            load_b(wave, bv);
+        first_groups();
     }
 
     Acc acc[NB][MF][NF];
@@ -473,7 +496,7 @@ __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
 #pragma unroll
             for (int j = 0; j < NF; ++j)
                 acc[w][i][j] = Acc{};
-    auto products = [&](const pt_u32x4 (&av)[MF][4], const pt_u32x4 (&v)[NB][NF][4]) {
+    auto products = [&](const Group &v) {
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -482,48 +505,39 @@ __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
                 for (int i = 0; i < MF; ++i)
 #pragma unroll
                     for (int j = 0; j < NF; ++j)
-                        acc[w][i][j] = E::mfma(av[i][s], v[w][j][s], acc[w][i][j]);
+                        acc[w][i][j] = E::mfma(v.a[i][s], v.b[w][j][s], acc[w][i][j]);
     };
-    auto coded = [&](int g, pt_u32x4 (&av)[MF][4]) {
+    auto coded = [&](int g, Group &v) {
 #pragma unroll
         for (int s = 0; s < 4; ++s)
-            av[0][s] = *reinterpret_cast<const pt_u32x4 *>(codes + (size_t)min(r, p.M - 1) * codes_ld + g * 256 + 64 * s + 16 * q);
+            v.a[0][s] = *reinterpret_cast<const pt_u32x4 *>(codes + (size_t)min(r, p.M - 1) * codes_ld + g * 256 + 64 * s + 16 * q);
     };
-    for (int g = wave; g < full; g += NW) {
-        pt_u32x4 av[MF][4];
-        if constexpr (X) {
-            coded(g, av);
-        } else {
-#pragma unroll
-            for (int i = 0; i < MF; ++i)
-                load(a[i], g, av[i]);
-        }
+    auto group = [&](int g, Group &v) {
+        if constexpr (X)
+            coded(g, v);
+        products(v);
+        if (g + 2 * NW < full)
+            load_group(g + 2 * NW, v);
+    };
+    for (int g = wave; g < full; g += 2 * NW) {
+        group(g, g0);
         if (g + NW < full)
-            load_b(g + NW, bn);
-        products(av, bv);
-#pragma unroll
-        for (int w = 0; w < NB; ++w)
-#pragma unroll
-            for (int j = 0; j < NF; ++j)
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    bv[w][j][s] = bn[w][j][s];
+            group(g + NW, g1);
     }
     if (groups > full && full % NW == wave) {
-        pt_u32x4 av[MF][4];
         if constexpr (X) {
-            coded(full, av);
+            coded(full, g0);
         } else {
 #pragma unroll
             for (int i = 0; i < MF; ++i)
-                load_rest(a[i], full, av[i]);
+                load_rest(a[i], full, g0.a[i]);
         }
 #pragma unroll
         for (int w = 0; w < NB; ++w)
 #pragma unroll
             for (int j = 0; j < NF; ++j)
-                load_rest(b[w][j], full, bv[w][j]);
-        products(av, bv);
+                load_rest(b[w][j], full, g0.b[w][j]);
+        products(g0);
     }
     // register d of lane l: row 4 (l / 16) + d, column l % 16 of the block
 #pragma unroll
@@ -577,15 +591,23 @@ static void lin_skinny_one(const Lin &p, const LinX &x, hipStream_t stream) {
     hipLaunchKernelGGL((lin_skinny_kernel<E, OUT, MODE, MF, NF, X>), dim3((p.N + 16 * NF - 1) / (16 * NF)), dim3(512), lds, stream, p, x);
 }
 
+template <class E, typename OUT, int MODE, int NF>
+static void lin_skinny(const Lin &p, const LinPlan &plan, hipStream_t stream) {
+    switch (plan.cfg) {
+    case 1: lin_skinny_one<E, OUT, MODE, 1, NF, false>(p, LinX{}, stream); break;
+    default: lin_skinny_one<E, OUT, MODE, 2, NF, false>(p, LinX{}, stream); break;
+    }
+}
+
 template <class E, typename OUT, int MODE>
 static hipError_t lin_run(const Lin &p, const LinPlan &plan, hipStream_t stream) {
     if (plan.kind == LINK_SKINNY) {
-        if (plan.cfg == 1)
-            lin_skinny_one<E, OUT, MODE, 1, 1, false>(p, LinX{}, stream);
-        else if (plan.cfg == 2)
-            lin_skinny_one<E, OUT, MODE, 2, 1, false>(p, LinX{}, stream);
+        // 32 columns per workgroup, 16 of two weights or 32 of one, once 16 would go round the CUs more than
+        // once: the activations are then read half as often.
+        if (MODE == LIN_SCALED && p.N > 16 * plan.cus)
+            lin_skinny<E, OUT, MODE, MODE == LIN_SCALED ? 2 : 1>(p, plan, stream);
         else
-            lin_skinny_one<E, OUT, MODE, 4, 1, false>(p, LinX{}, stream);
+            lin_skinny<E, OUT, MODE, 1>(p, plan, stream);
     } else {
         lin_tile<E, OUT, MODE>(p, plan, stream);
     }

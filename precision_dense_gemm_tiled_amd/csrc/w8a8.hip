@@ -14,9 +14,9 @@ namespace mpg {
 // P pieces of 8 elements, 64 W P 8 in all, and the row is read once. P = 0: longer rows, read
 // twice. Bound by memory: the reads of a row are on their way together.
 template <typename T, int W, int P>
-__global__ __launch_bounds__(256) void i8_quantize_kernel(I8Quantize p) {
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void i8_quantize_kernel(I8Quantize p) {
     constexpr int NT = 64 * W;
-    const int t = threadIdx.x % NT, lane = threadIdx.x & 63;
+    const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x, lane = threadIdx.x & 63;
     const int row = W == 1 ? blockIdx.x * 4 + threadIdx.x / 64 : blockIdx.x;
     if (W == 1 && row >= p.M)
         return;
@@ -87,11 +87,11 @@ static void quantize_type(const I8Quantize &p, hipStream_t stream) {
     else if (K <= 2048)
         hipLaunchKernelGGL((i8_quantize_kernel<T, 4, 1>), rows, nt, 0, stream, p);
     else if (K <= 4096)
-        hipLaunchKernelGGL((i8_quantize_kernel<T, 4, 2>), rows, nt, 0, stream, p);
+        hipLaunchKernelGGL((i8_quantize_kernel<T, 8, 1>), rows, dim3(512), 0, stream, p);
     else if (K <= 8192)
-        hipLaunchKernelGGL((i8_quantize_kernel<T, 4, 4>), rows, nt, 0, stream, p);
+        hipLaunchKernelGGL((i8_quantize_kernel<T, 16, 1>), rows, dim3(1024), 0, stream, p);
     else
-        hipLaunchKernelGGL((i8_quantize_kernel<T, 4, 0>), rows, nt, 0, stream, p);
+        hipLaunchKernelGGL((i8_quantize_kernel<T, 16, 0>), rows, dim3(1024), 0, stream, p);
 }
 
 hipError_t launch_i8_quantize(int type, const I8Quantize &p, hipStream_t stream) {
@@ -205,29 +205,47 @@ hipError_t launch_lin_fill(int type, void *c, int64_t ldc, int M, int N, const v
 
 // ------------------------------------------------------------------ plan
 
-// Up to 64 rows every workgroup of the skinny kernel reads all activations, and each weight is read once.
-LinPlan plan_lin(int mode, int64_t M, int64_t N, int64_t K, int elem, int cu_count) {
+// The cheapest tiles for a grid of tiles(c) workgroups.
+template <typename F>
+static int lin_cheapest(int cu_count, F tiles) {
+    int cfg = 0;
+    double best = 0;
+    for (int c = 0; c < 3; ++c) {
+        const double cost = kLinCfg[c].cost * (double)((tiles(c) + cu_count - 1) / cu_count);
+        if (c == 0 || cost < best) {
+            best = cost;
+            cfg = c;
+        }
+    }
+    return cfg;
+}
+
+static int64_t lin_tiles(int mode, int c, int64_t M, int64_t N) {
+    const int64_t cn = mode == LIN_GATED ? kLinCfg[c].BN / 2 : kLinCfg[c].BN;
+    return ((M + kLinCfg[c].BM - 1) / kLinCfg[c].BM) * ((N + cn - 1) / cn);
+}
+
+// Up to 32 rows the skinny kernel, whose workgroups each read all the activations; then tiles.
+// Skinny and tiles of 64, us: integers 32 x 4096 x 4096 8.7 and 10.2, 64 x 4096 x 4096 12.2 and 10.5, 64 x 8192 x 8192 27.8
+// and 22.7, 16 x 8192 x 8192 16.8 and 19.4; gated 16 x 4096 x 4096 14.6 and 18.5, 64 x 4096 x 4096 25.9 and 21.0.
+LinPlan plan_lin(int mode, int64_t M, int64_t N, int64_t K, int cu_count) {
     LinPlan pl = {LINK_TILE, 0, cu_count};
     if (K == 0) {
         pl.kind = LINK_EMPTY;
         return pl;
     }
-    if (M <= 64 && (mode == LIN_SCALED || mode == LIN_GATED)) {
+    if (M <= 32 && (mode == LIN_SCALED || mode == LIN_GATED)) {
         pl.kind = LINK_SKINNY;
-        pl.cfg = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+        pl.cfg = M <= 16 ? 1 : 2;
         return pl;
     }
-    double best = 0;
-    for (int c = 0; c < 3; ++c) {
-        const int64_t cn = mode == LIN_GATED ? kLinCfg[c].BN / 2 : kLinCfg[c].BN;
-        const int64_t tiles = ((M + kLinCfg[c].BM - 1) / kLinCfg[c].BM) * ((N + cn - 1) / cn);
-        const double cost = kLinCfg[c].cost * (double)((tiles + cu_count - 1) / cu_count);
-        if (c == 0 || cost < best) {
-            best = cost;
-            pl.cfg = c;
-        }
-    }
+    pl.cfg = lin_cheapest(cu_count, [&](int c) { return lin_tiles(mode, c, M, N); });
     return pl;
+}
+
+// Both products of the backward pass in one grid: M x K and 2 part x K results.
+LinPlan plan_lin_pair(int64_t M, int64_t part, int64_t K, int cu_count) {
+    return {LINK_TILE, lin_cheapest(cu_count, [&](int c) { return lin_tiles(LIN_DX, c, M, K) + lin_tiles(LIN_DW, c, 2 * part, K); }), cu_count};
 }
 
 // Few activations: every workgroup of the product quantises all of them.
