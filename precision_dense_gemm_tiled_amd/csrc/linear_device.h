@@ -43,14 +43,15 @@ __device__ __forceinline__ float lin_slope(float v) {
 // ------------------------------------------------------------------ tiles
 
 // Consecutive workgroups go to the 8 XCDs in turn, each with its own L2: give
-// every XCD a contiguous range of tiles, walked in groups of 8 tile rows.
+// every XCD a contiguous range of tiles, walked in groups of 4 tile rows (4096 x 10240 x 4096 gated, bf16: 495 us,
+// in groups of 8 499, of 16 513).
 __device__ __forceinline__ void lin_tile_of(int bid, int nblk, int tiles_m, int tiles_n, int &tm, int &tn) {
     int logical = bid;
     if (nblk >= 8) {
         const int xcd = bid % 8, base = nblk / 8, rem = nblk % 8;
         logical = xcd * base + (xcd < rem ? xcd : rem) + bid / 8;
     }
-    constexpr int GROUP = 8;
+    constexpr int GROUP = 4;
     const int group = logical / (GROUP * tiles_n);
     const int first = group * GROUP;
     const int rows = tiles_m - first < GROUP ? tiles_m - first : GROUP;

@@ -134,12 +134,15 @@ struct PhaseTile {
     template <bool COL, int H, int L>
     static __device__ __forceinline__ void load(const PtSource &s, int h, int e, const uint32_t (&off)[L], uint8_t *lds,
                                                 int tid, int wave) {
-        const uint8_t *from = s.p[h];
-        if (COL && JOIN) {
-            from = e < s.split ? from : s.next[h];
-            e = e < s.split ? e : e - s.split;
+        const uint8_t *base = s.p[h];
+        if constexpr (COL) {
+            if (JOIN) {
+                base = e < s.split ? base : s.next[h];
+                e = e < s.split ? e : e - s.split;
+            }
+            base += (int64_t)e * 64 * s.ld[0];
         }
-        const uint8_t *base = from + (COL ? (int64_t)e * 64 * s.ld[0] : (int64_t)e * 128);
+        const uint32_t ahead = COL ? 0 : e * 128;
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             const int f = j * NT + tid;
@@ -150,11 +153,11 @@ struct PhaseTile {
             if constexpr (ACOL || BCOL) {
                 const uint64_t at64 = reinterpret_cast<uint64_t>(base);
                 const pt_u32x4 r = {(uint32_t)at64, (uint32_t)(at64 >> 32) & 0xFFFFu, kPtRange, 0x00020000u};
-                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                             : : "s"((uint32_t)(uintptr_t)to), "v"(o), "s"(r));
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                             : : "s"((uint32_t)(uintptr_t)to), "v"(o), "s"(r), "s"(ahead));
             } else {
                 const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, kPtRange, 0x00020000);
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, o, 0, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, o, ahead, 0, 0);
             }
         }
     }
