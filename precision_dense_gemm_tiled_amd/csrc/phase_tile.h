@@ -123,7 +123,7 @@ struct PhaseTile {
         }
     }
 
-    // Loads of half h of stage e into `lds`. Buffer loads: one 32-bit offset per load in registers
+    // Loads of half h of stage e into `lds`, stage after stage (at_k, across k: where the next stage begins). Buffer loads: one 32-bit offset per load in registers
     // (the 64-bit addresses of the global form do not fit beside the sums), and what is past the
     // operand's end gets an offset out of the buffer's range, which loads zeros. Kernels with
     // transposing reads write the load as an instruction of its own: the compiler takes those
@@ -132,15 +132,14 @@ struct PhaseTile {
     // 20480 x 4096 x 4096 with both: 548 and 495). The load has no result in registers,
     // and nothing else in these kernels uses m0.
     template <bool COL, int H, int L>
-    static __device__ __forceinline__ void load(const PtSource &s, int h, int e, const uint32_t (&off)[L], uint8_t *lds,
-                                                int tid, int wave) {
+    static __device__ __forceinline__ void load(const PtSource &s, int h, int e, const uint8_t *(&at_k)[2], const uint32_t (&off)[L],
+                                                uint8_t *lds, int tid, int wave) {
         const uint8_t *base = s.p[h];
         if constexpr (COL) {
-            if (JOIN) {
-                base = e < s.split ? base : s.next[h];
+            base = at_k[h];
+            at_k[h] = JOIN && e + 1 == s.split ? s.next[h] : base + 64 * s.ld[0];
+            if (JOIN)
                 e = e < s.split ? e : e - s.split;
-            }
-            base += (int64_t)e * 64 * s.ld[0];
         }
         const uint32_t ahead = COL ? 0 : e * 128;
 #pragma unroll
@@ -234,8 +233,9 @@ struct PhaseTile {
             offsets<BCOL, HN>(B, h, tid, ob[h]);
         }
         uint8_t *la = smem, *lb = smem + 2 * NS * SA;   // half h of stage e: [NS h + e % NS]
-        auto load_a = [&](int h, int e, int slot) { load<ACOL, HM>(A, h, e, oa[h], la + (NS * h + slot) * SA, tid, wave); };
-        auto load_b = [&](int h, int e, int slot) { load<BCOL, HN>(B, h, e, ob[h], lb + (NS * h + slot) * SB, tid, wave); };
+        const uint8_t *ka[2] = {A.p[0], A.p[1]}, *kb[2] = {B.p[0], B.p[1]};
+        auto load_a = [&](int h, int e, int slot) { load<ACOL, HM>(A, h, e, ka, oa[h], la + (NS * h + slot) * SA, tid, wave); };
+        auto load_b = [&](int h, int e, int slot) { load<BCOL, HN>(B, h, e, kb, ob[h], lb + (NS * h + slot) * SB, tid, wave); };
         auto read_a = [&](int h, int slot, pt_u32x4 (&f)[FM][2]) { read<ACOL, HM>(la + (NS * h + slot) * SA, wm, lane, f); };
         auto read_b = [&](int h, int slot, pt_u32x4 (&f)[FN][2]) { read<BCOL, HN>(lb + (NS * h + slot) * SB, wn, lane, f); };
 #pragma unroll
