@@ -379,17 +379,42 @@ __device__ __forceinline__ uint2 i8_codes8(const float (&v)[8], const I8Row &r) 
     return w;
 }
 
-constexpr int LIN_X_PIECES = 4;   // pieces of 8 activations that a thread of the fused kernel takes
+constexpr int LIN_SKINNY_WAVES = 8;
+constexpr int LIN_HALF_ROWS = 4;   // GATED: up to here 8 columns of either weight per workgroup, in one fragment
+constexpr int LIN_X_MAX = 32;   // rows of 512 activations, a wavefront's load, that the fused kernel takes
 
-// Up to 64 rows: 16 MF rows x 16 NF columns (of each weight) per workgroup, operands straight from memory
-// into the matrix unit's registers, which read each weight once; K in groups of 256 bytes dealt out to the
+// One output from its sums (of either weight).
+template <class E, typename OUT, int MODE, typename Num, int NB>
+__device__ __forceinline__ void lin_output(const Lin &p, int m, int n, float sa, const Num (&t)[NB]) {
+    constexpr bool SCALED = sizeof(typename E::T) == 1;
+    float v = (float)t[0];
+    if (SCALED)
+        v = v * sa * p.sb[0][n];
+    if constexpr (MODE == LIN_GATED) {
+        float u = (float)t[1];
+        if (SCALED)
+            u = u * sa * p.sb[1][n];
+        if (!SCALED && p.g) {
+            static_cast<OUT *>(p.g)[(int64_t)m * p.ldg + n] = (OUT)v;
+            static_cast<OUT *>(p.u)[(int64_t)m * p.ldu + n] = (OUT)u;
+        }
+        v = (p.act == MPGEMM_ACT_SILU ? lin_act<MPGEMM_ACT_SILU>(v)
+             : p.act == MPGEMM_ACT_GELU ? lin_act<MPGEMM_ACT_GELU>(v) : lin_act<MPGEMM_ACT_GELU_TANH>(v)) * u;
+    } else if (p.bias) {
+        v += (float)static_cast<const OUT *>(p.bias)[n];
+    }
+    static_cast<OUT *>(p.c)[(int64_t)m * p.ldc + n] = (OUT)v;
+}
+
+// Up to 32 rows: 16 MF rows x 16 NF columns (of each weight) per workgroup, operands straight from memory
+// into the matrix unit's registers, which read each weight once; K in groups of 128 bytes dealt out to the
 // 8 wavefronts in turn. At step s of a group, lane quarter q takes bytes 64 s + 16 q of its row, so that a
-// load instruction reads 64 contiguous bytes of each of 16 rows. The next two groups are on their way
+// load instruction reads 64 contiguous bytes of each of 16 rows. Three groups are on their way
 // from the start on. The wavefronts' sums are joined in LDS in the order of the wavefronts.
 // X: the activations are quantised by every workgroup (MF = 1, few of them).
-template <class E, typename OUT, int MODE, int MF, int NF, bool X>
-__global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
-    constexpr int NW = 8, NB = MODE == LIN_GATED ? 2 : 1, EB = sizeof(typename E::T);
+template <class E, typename OUT, int MODE, int MF, int NF, bool HALF, bool X>
+__global__ __launch_bounds__(64 * LIN_SKINNY_WAVES) void lin_skinny_kernel(Lin p, LinX px) {
+    constexpr int NW = LIN_SKINNY_WAVES, NT = 64 * NW, GB = 128, AHEAD = 3, NB = MODE == LIN_GATED && !HALF ? 2 : 1, EB = sizeof(typename E::T);
     constexpr bool SCALED = EB == 1;
     typedef typename E::Acc Acc;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -398,35 +423,37 @@ __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, r = lane & 15;
-    const int n0 = blockIdx.x * 16 * NF;
-    const int bytes = p.K * EB, full = bytes / 256, groups = (bytes + 255) / 256;
+    constexpr int COLS = HALF ? 8 : 16 * NF;
+    const int n0 = blockIdx.x * COLS;
+    const int bytes = p.K * EB, full = bytes / GB, groups = (bytes + GB - 1) / GB;
 
     const uint8_t *b[NB][NF], *a[MF];
 #pragma unroll
     for (int w = 0; w < NB; ++w)
 #pragma unroll
         for (int j = 0; j < NF; ++j)
-            b[w][j] = p.b[w] + (int64_t)min(n0 + 16 * j + r, p.N - 1) * p.ldb[w];
+            b[w][j] = HALF ? p.b[r >> 3] + (int64_t)min(n0 + (r & 7), p.N - 1) * p.ldb[r >> 3]
+                           : p.b[w] + (int64_t)min(n0 + 16 * j + r, p.N - 1) * p.ldb[w];
 #pragma unroll
     for (int i = 0; i < MF; ++i)
         a[i] = X ? nullptr : p.a + (int64_t)min(16 * i + r, p.M - 1) * p.lda;
-    auto load = [&](const uint8_t *row, int g, pt_u32x4 (&v)[4]) {
+    auto load = [&](const uint8_t *row, int g, pt_u32x4 (&v)[2]) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-            v[s] = lin_load16(row + (int64_t)g * 256 + 64 * s + 16 * q);
+        for (int s = 0; s < 2; ++s)
+            v[s] = lin_load16(row + (int64_t)g * GB + 64 * s + 16 * q);
     };
-    auto load_rest = [&](const uint8_t *row, int g, pt_u32x4 (&v)[4]) {
+    auto load_rest = [&](const uint8_t *row, int g, pt_u32x4 (&v)[2]) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int at = g * 256 + 64 * s + 16 * q;
+        for (int s = 0; s < 2; ++s) {
+            const int at = g * GB + 64 * s + 16 * q;
             v[s] = lin_load16_part<typename E::T>(row + at, bytes - at);
         }
     };
 
     // A group's operands (the activations that the kernel has quantised stay in LDS).
     struct Group {
-        pt_u32x4 b[NB][NF][4], a[X ? 1 : MF][4];
-    } g0, g1;
+        pt_u32x4 b[NB][NF][2], a[X ? 1 : MF][2];
+    } gr[AHEAD];
     auto load_group = [&](int g, Group &v) {
 #pragma unroll
         for (int w = 0; w < NB; ++w)
@@ -440,10 +467,10 @@ __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
         }
     };
     auto first_groups = [&]() {
-        if (wave < full)
-            load_group(wave, g0);
-        if (wave + NW < full)
-            load_group(wave + NW, g1);
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d)
+            if (wave + d * NW < full)
+                load_group(wave + d * NW, gr[d]);
     };
     // the activations' codes: rows of `codes_ld` bytes (a multiple of 512, and 16 so that rows start at different banks)
     uint8_t *codes = smem + sizeof(Num) * NW * MF * NB * NF * 256;
@@ -453,10 +480,10 @@ __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
         typedef OUT T;
         uint32_t *top = reinterpret_cast<uint32_t *>(scales + 16);
         const bool vec = p.K % 8 == 0 && (reinterpret_cast<uintptr_t>(px.x) & 15) == 0 && (px.ldx * (int64_t)sizeof(T)) % 16 == 0;
-        float v[LIN_X_PIECES][8];
+        float v[LIN_X_MAX / NW][8];
 #pragma unroll
-        for (int i = 0; i < LIN_X_PIECES; ++i) {
-            const int f = i * 512 + tid, row = f / per_row;
+        for (int i = 0; i < LIN_X_MAX / NW; ++i) {
+            const int f = i * NT + tid, row = f / per_row;
             if (row < p.M)   // (the same row for a whole wavefront)
                 i8_load8<T>(static_cast<const T *>(px.x) + (int64_t)row * px.ldx, (f - row * per_row) * 8, p.K, vec, v[i]);
         }
@@ -465,8 +492,8 @@ __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
             top[tid] = 0;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < LIN_X_PIECES; ++i) {
-            const int row = (i * 512 + tid) / per_row;
+        for (int i = 0; i < LIN_X_MAX / NW; ++i) {
+            const int row = (i * NT + tid) / per_row;
             if (row < p.M) {
                 const uint32_t m = lin_wave_max(i8_amax8(v[i]));
                 if (lane == 0)
@@ -475,8 +502,8 @@ __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < LIN_X_PIECES; ++i) {
-            const int f = i * 512 + tid, row = f / per_row, k0 = (f - row * per_row) * 8;
+        for (int i = 0; i < LIN_X_MAX / NW; ++i) {
+            const int f = i * NT + tid, row = f / per_row, k0 = (f - row * per_row) * 8;
             if (row < p.M) {
                 const I8Row s = i8_row(top[row]);
                 *reinterpret_cast<uint2 *>(codes + (size_t)row * codes_ld + k0) = i8_codes8(v[i], s);
@@ -499,7 +526,7 @@ __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
                 acc[w][i][j] = Acc{};
     auto products = [&](const Group &v) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int w = 0; w < NB; ++w)
 #pragma unroll
@@ -510,35 +537,35 @@ __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
     };
     auto coded = [&](int g, Group &v) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-            v.a[0][s] = *reinterpret_cast<const pt_u32x4 *>(codes + (size_t)min(r, p.M - 1) * codes_ld + g * 256 + 64 * s + 16 * q);
+        for (int s = 0; s < 2; ++s)
+            v.a[0][s] = *reinterpret_cast<const pt_u32x4 *>(codes + (size_t)min(r, p.M - 1) * codes_ld + g * GB + 64 * s + 16 * q);
     };
     auto group = [&](int g, Group &v) {
         if constexpr (X)
             coded(g, v);
         products(v);
-        if (g + 2 * NW < full)
-            load_group(g + 2 * NW, v);
+        if (g + AHEAD * NW < full)
+            load_group(g + AHEAD * NW, v);
     };
-    for (int g = wave; g < full; g += 2 * NW) {
-        group(g, g0);
-        if (g + NW < full)
-            group(g + NW, g1);
-    }
+    for (int g = wave; g < full; g += AHEAD * NW)
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d)
+            if (g + d * NW < full)
+                group(g + d * NW, gr[d]);
     if (groups > full && full % NW == wave) {
         if constexpr (X) {
-            coded(full, g0);
+            coded(full, gr[0]);
         } else {
 #pragma unroll
             for (int i = 0; i < MF; ++i)
-                load_rest(a[i], full, g0.a[i]);
+                load_rest(a[i], full, gr[0].a[i]);
         }
 #pragma unroll
         for (int w = 0; w < NB; ++w)
 #pragma unroll
             for (int j = 0; j < NF; ++j)
-                load_rest(b[w][j], full, g0.b[w][j]);
-        products(g0);
+                load_rest(b[w][j], full, gr[0].b[w][j]);
+        products(gr[0]);
     }
     // register d of lane l: row 4 (l / 16) + d, column l % 16 of the block
 #pragma unroll
@@ -551,53 +578,38 @@ __global__ __launch_bounds__(512) void lin_skinny_kernel(Lin p, LinX px) {
                 for (int d = 0; d < 4; ++d)
                     red[wave][(w * MF + i) * NF + j][d][lane] = acc[w][i][j][d];
     __syncthreads();
-    for (int f = tid; f < MF * NF * 256; f += 512) {
+    for (int f = tid; f < MF * 16 * COLS; f += NT) {
         // consecutive threads take consecutive columns
-        const int col = f % (16 * NF), row = f / (16 * NF);
-        const int i = row / 16, j = col / 16, d = row % 4, l = (row % 16) / 4 * 16 + col % 16;
-        Num t[NB] = {};
+        constexpr int PARTS = MODE == LIN_GATED ? 2 : 1;
+        const int col = f % COLS, row = f / COLS, i = row / 16, d = row % 4;
+        Num t[PARTS] = {};
 #pragma unroll
-        for (int w = 0; w < NB; ++w)
+        for (int w = 0; w < PARTS; ++w) {
+            const int c = HALF ? col + 8 * w : col, block = ((HALF ? 0 : w) * MF + i) * NF + c / 16;
 #pragma unroll
             for (int x = 0; x < NW; ++x)
-                t[w] += red[x][(w * MF + i) * NF + j][d][l];
-        const int n = n0 + col;
-        if (row < p.M && n < p.N) {
-            const float sa = !SCALED ? 1.f : X ? scales[row] : p.sa[row];
-            float v = (float)t[0];
-            if (SCALED)
-                v = v * sa * p.sb[0][n];
-            if constexpr (MODE == LIN_GATED) {
-                float u = (float)t[1];
-                if (SCALED)
-                    u = u * sa * p.sb[1][n];
-                if (!SCALED && p.g) {
-                    static_cast<OUT *>(p.g)[(int64_t)row * p.ldg + n] = (OUT)v;
-                    static_cast<OUT *>(p.u)[(int64_t)row * p.ldu + n] = (OUT)u;
-                }
-                v = (p.act == MPGEMM_ACT_SILU ? lin_act<MPGEMM_ACT_SILU>(v)
-                     : p.act == MPGEMM_ACT_GELU ? lin_act<MPGEMM_ACT_GELU>(v) : lin_act<MPGEMM_ACT_GELU_TANH>(v)) * u;
-            } else if (p.bias) {
-                v += (float)static_cast<const OUT *>(p.bias)[n];
-            }
-            static_cast<OUT *>(p.c)[(int64_t)row * p.ldc + n] = (OUT)v;
+                t[w] += red[x][block][d][(row % 16) / 4 * 16 + c % 16];
         }
+        const int n = n0 + col;
+        if (row < p.M && n < p.N)
+            lin_output<E, OUT, MODE>(p, row, n, !SCALED ? 1.f : X ? scales[row] : p.sa[row], t);
     }
 }
 
-template <class E, typename OUT, int MODE, int MF, int NF, bool X>
+template <class E, typename OUT, int MODE, int MF, int NF, bool HALF, bool X>
 static void lin_skinny_one(const Lin &p, const LinX &x, hipStream_t stream) {
-    constexpr int NB = MODE == LIN_GATED ? 2 : 1;
-    const unsigned lds = MF * NB * NF * 8192u + (X ? (unsigned)p.M * ((p.K + 511) / 512 * 512 + 16) + 128 : 0);
-    hipLaunchKernelGGL((lin_skinny_kernel<E, OUT, MODE, MF, NF, X>), dim3((p.N + 16 * NF - 1) / (16 * NF)), dim3(512), lds, stream, p, x);
+    constexpr int NB = MODE == LIN_GATED && !HALF ? 2 : 1, COLS = HALF ? 8 : 16 * NF;
+    const unsigned lds = MF * NB * NF * LIN_SKINNY_WAVES * 1024u + (X ? (unsigned)p.M * ((p.K + 511) / 512 * 512 + 16) + 128 : 0);
+    hipLaunchKernelGGL((lin_skinny_kernel<E, OUT, MODE, MF, NF, HALF, X>), dim3((p.N + COLS - 1) / COLS), dim3(64 * LIN_SKINNY_WAVES), lds, stream,
+                       p, x);
 }
 
 template <class E, typename OUT, int MODE, int NF>
 static void lin_skinny(const Lin &p, const LinPlan &plan, hipStream_t stream) {
-    switch (plan.cfg) {
-    case 1: lin_skinny_one<E, OUT, MODE, 1, NF, false>(p, LinX{}, stream); break;
-    default: lin_skinny_one<E, OUT, MODE, 2, NF, false>(p, LinX{}, stream); break;
-    }
+    if (plan.cfg == 1)
+        lin_skinny_one<E, OUT, MODE, 1, NF, false, false>(p, LinX{}, stream);
+    else
+        lin_skinny_one<E, OUT, MODE, 2, NF, false, false>(p, LinX{}, stream);
 }
 
 template <class E, typename OUT, int MODE>
@@ -607,11 +619,23 @@ static hipError_t lin_run(const Lin &p, const LinPlan &plan, hipStream_t stream)
         // once: the activations are then read half as often.
         if (MODE == LIN_SCALED && p.N > 16 * plan.cus)
             lin_skinny<E, OUT, MODE, MODE == LIN_SCALED ? 2 : 1>(p, plan, stream);
+        else if (MODE == LIN_GATED && p.M <= LIN_HALF_ROWS)
+            lin_skinny_one<E, OUT, MODE, 1, 1, MODE == LIN_GATED, false>(p, LinX{}, stream);
         else
             lin_skinny<E, OUT, MODE, 1>(p, plan, stream);
     } else {
         lin_tile<E, OUT, MODE>(p, plan, stream);
     }
+    return hipGetLastError();
+}
+
+// On integers, the activations quantised in the kernel.
+template <typename OUT, int MODE>
+static hipError_t lin_run_x(const Lin &p, const LinX &x, hipStream_t stream) {
+    if (MODE == LIN_GATED && p.M <= LIN_HALF_ROWS)
+        lin_skinny_one<PtI8, OUT, MODE, 1, 1, MODE == LIN_GATED, true>(p, x, stream);
+    else
+        lin_skinny_one<PtI8, OUT, MODE, 1, 1, false, true>(p, x, stream);
     return hipGetLastError();
 }
 

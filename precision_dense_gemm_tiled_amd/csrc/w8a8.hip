@@ -250,7 +250,7 @@ LinPlan plan_lin_pair(int64_t M, int64_t part, int64_t K, int cu_count) {
 
 // Few activations: every workgroup of the product quantises all of them.
 bool lin_fuses(const LinPlan &plan, int64_t M, int64_t K) {
-    return plan.kind == LINK_SKINNY && M <= 16 && M * ((K + 511) / 512) <= LIN_X_PIECES * 8;
+    return plan.kind == LINK_SKINNY && M <= 16 && M * ((K + 511) / 512) <= LIN_X_MAX;
 }
 
 // ------------------------------------------------------------------ product
@@ -263,13 +263,12 @@ hipError_t launch_w8a8(int type, const Lin &p, const LinPlan &plan, hipStream_t 
     }
 }
 
-hipError_t launch_w8a8_x(int type, const Lin &p, const LinX &x, const LinPlan &plan, hipStream_t stream) {
+hipError_t launch_w8a8_x(int type, const Lin &p, const LinX &x, hipStream_t stream) {
     switch (type) {
-    case MPGEMM_TYPE_F16: lin_skinny_one<PtI8, _Float16, LIN_SCALED, 1, 1, true>(p, x, stream); break;
-    case MPGEMM_TYPE_BF16: lin_skinny_one<PtI8, __bf16, LIN_SCALED, 1, 1, true>(p, x, stream); break;
-    default: lin_skinny_one<PtI8, float, LIN_SCALED, 1, 1, true>(p, x, stream); break;
+    case MPGEMM_TYPE_F16: return lin_run_x<_Float16, LIN_SCALED>(p, x, stream);
+    case MPGEMM_TYPE_BF16: return lin_run_x<__bf16, LIN_SCALED>(p, x, stream);
+    default: return lin_run_x<float, LIN_SCALED>(p, x, stream);
     }
-    return hipGetLastError();
 }
 
 }  // namespace mpg
