@@ -279,7 +279,7 @@ mpgemm_status_t mpgemm_dequantize_i8(mpgemm_handle_t h, int64_t M, int64_t K, co
         return MPGEMM_ERR_INVALID_ARG;
     if (M == 0 || K == 0)
         return MPGEMM_OK;
-    if (M > kMaxDim || K > kMaxDim || ((M + 7) / 8) * ((K + 2047) / 2048) > INT_MAX / 8)
+    if (M > kMaxDim || K > kMaxDim)
         return MPGEMM_ERR_UNSUPPORTED;
     const mpgemm_status_t st = first({check_rows(Q, ldq, K, 1), check_scales(S), check_rows(Y, ldy, K, size_of(type))});
     if (st != MPGEMM_OK)

@@ -94,13 +94,26 @@ static void quantize_type(const I8Quantize &p, hipStream_t stream) {
         hipLaunchKernelGGL((i8_quantize_kernel<T, 16, 0>), rows, dim3(1024), 0, stream, p);
 }
 
-hipError_t launch_i8_quantize(int type, const I8Quantize &p, hipStream_t stream) {
-    switch (type) {
-    case MPGEMM_TYPE_F16: quantize_type<_Float16>(p, stream); break;
-    case MPGEMM_TYPE_BF16: quantize_type<__bf16>(p, stream); break;
-    default: quantize_type<float>(p, stream); break;
+// A launch has fewer than 2^32 threads: more rows than this take several.
+constexpr int LIN_ROWS_AT_ONCE = 1 << 21;
+
+hipError_t launch_i8_quantize(int type, const I8Quantize &all, hipStream_t stream) {
+    for (int64_t row = 0; row < all.M; row += LIN_ROWS_AT_ONCE) {
+        I8Quantize p = all;
+        p.x = static_cast<const uint8_t *>(all.x) + row * all.ldx * (type == MPGEMM_TYPE_F32 ? 4 : 2);
+        p.q = all.q + row * all.ldq;
+        p.s = all.s + row;
+        p.M = (int)(all.M - row < LIN_ROWS_AT_ONCE ? all.M - row : LIN_ROWS_AT_ONCE);
+        switch (type) {
+        case MPGEMM_TYPE_F16: quantize_type<_Float16>(p, stream); break;
+        case MPGEMM_TYPE_BF16: quantize_type<__bf16>(p, stream); break;
+        default: quantize_type<float>(p, stream); break;
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 // 8 elements per thread, 2^LX threads per row piece and the rest of the workgroup's 256 over rows.
@@ -146,13 +159,24 @@ static void dequantize_type(const I8Dequantize &p, hipStream_t stream) {
         dequantize_one<T, 8>(p, stream);
 }
 
-hipError_t launch_i8_dequantize(int type, const I8Dequantize &p, hipStream_t stream) {
-    switch (type) {
-    case MPGEMM_TYPE_F16: dequantize_type<_Float16>(p, stream); break;
-    case MPGEMM_TYPE_BF16: dequantize_type<__bf16>(p, stream); break;
-    default: dequantize_type<float>(p, stream); break;
+hipError_t launch_i8_dequantize(int type, const I8Dequantize &all, hipStream_t stream) {
+    const int64_t parts = (all.K + 2047) / 2048, step = (LIN_ROWS_AT_ONCE + parts - 1) / parts;
+    for (int64_t row = 0; row < all.M; row += step) {
+        I8Dequantize p = all;
+        p.q = all.q + row * all.ldq;
+        p.s = all.s + row;
+        p.y = static_cast<uint8_t *>(all.y) + row * all.ldy * (type == MPGEMM_TYPE_F32 ? 4 : 2);
+        p.M = (int)(all.M - row < step ? all.M - row : step);
+        switch (type) {
+        case MPGEMM_TYPE_F16: dequantize_type<_Float16>(p, stream); break;
+        case MPGEMM_TYPE_BF16: dequantize_type<__bf16>(p, stream); break;
+        default: dequantize_type<float>(p, stream); break;
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 // ------------------------------------------------------------------ copies and fills

@@ -312,3 +312,41 @@ def test_captured_and_on_another_stream(mp, M):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, want[i]))
         assert all(torch.equal(a, b) for a, b in zip(step(xs[i]), want[i]))
+
+
+# Long sums into few columns, and tiles whose second half has no rows, captured where nothing is mapped behind the
+# operands: stages past the last one and halves without rows read nothing.
+@pytest.mark.parametrize("M,N,K", [(3712, 8576, 384), (1856, 832, 640), (896, 256, 1152), (65, 7680, 64), (70, 333, 129)])
+def test_backward_of_long_sums_captured(mp, M, N, K):
+    dt = torch.bfloat16
+    gg = torch.Generator(device="cuda").manual_seed(N)
+    torch.cuda.empty_cache()
+    dh, x, wg, wu, g, u = (torch.randn(*s, generator=gg, device="cuda").to(dt) for s in ((M, N), (M, K), (N, K), (N, K), (M, N), (M, N)))
+    want = mp.gemm_gated_backward(dh, x, wg, wu, g, u)
+    if M < 1000:
+        for y, (w, e) in zip(want, lu.gated_backward(*(v.cpu() for v in (dh, x, wg, wu, g, u)), "silu", dt)):
+            lu.check(y, w, e)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = mp.gemm_gated_backward(dh, x, wg, wu, g, u)
+    torch.cuda.empty_cache()
+    for _ in range(3):
+        for y in held:
+            y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want))
+        assert all(torch.equal(a, b) for a, b in zip(mp.gemm_gated_backward(dh, x, wg, wu, g, u), want))
+
+
+# Rows of more than 2^23 bytes, which the products across k take from a copy, and steps of 2^25 bytes.
+@pytest.mark.parametrize("K", [5_000_001, (1 << 24) - 3])
+def test_backward_with_very_long_rows(mp, K):
+    M, N, dt = 66, 3, torch.bfloat16
+    gg = torch.Generator(device="cuda").manual_seed(K)
+    dh, x, wg, wu, g, u = (torch.randn(*s, generator=gg, device="cuda", dtype=dt) for s in ((M, N), (M, K), (N, K), (N, K), (M, N), (M, N)))
+    got = mp.gemm_gated_backward(dh, x, wg, wu, g, u)
+    for k in (slice(0, 300), slice(K // 2, K // 2 + 200), slice(K - 300, K)):
+        want = lu.gated_backward(*(v.cpu() for v in (dh, x[:, k], wg[:, k], wu[:, k], g, u)), "silu", dt)
+        for y, (w, e) in zip(got, want):
+            lu.check(y[:, k], w, e)

@@ -220,3 +220,17 @@ def test_products_of_integers_beyond_fp32(mp):
     with pytest.raises(mp.MpgemmError):
         mp.gemm_w8a8(torch.zeros(1, K + 1, dtype=torch.int8, device="cuda"), torch.ones(1, device="cuda"),
                      torch.zeros(1, K + 1, dtype=torch.int8, device="cuda"), torch.ones(1, device="cuda"))
+
+
+# More rows than one launch has threads for, in either direction, and rows behind 2^32 elements.
+def test_quantize_of_very_many_rows(mp):
+    M, K, at = (1 << 22) + 5, 4104, [0, 1, (1 << 21) - 1, 1 << 21, (1 << 21) + 1, (1 << 22) - 1, 1 << 22, (1 << 22) + 4]
+    x = torch.zeros(M, K, dtype=torch.float16, device="cuda")
+    some = (torch.randn(len(at), K, generator=gen(K)) * 3).half()
+    x[at] = some.cuda()
+    q, s = mp.quantize_i8(x)
+    wq, ws = mp.quantize_i8(some.cuda())
+    assert torch.equal(q[at], wq) and torch.equal(s[at], ws)
+    assert int((s != 0).sum()) == len(at)
+    y = mp.dequantize_i8(q, s, dtype=torch.float16)
+    assert torch.equal(y[at], mp.dequantize_i8(wq, ws, dtype=torch.float16))

@@ -87,7 +87,8 @@ def test_backward_refusals(mp, change, expect):
 def test_workspaces(mp):
     cus = 256
     assert mp.mpgemm_run_w8a8_workspace(4, 4096, 4096, 0, cus) == 0
-    assert mp.mpgemm_run_w8a8_workspace(300, 500, 100, 1, cus) == 0
+    assert mp.mpgemm_run_w8a8_workspace(300, 500, 112, 1, cus) == 0
+    assert mp.mpgemm_run_w8a8_workspace(300, 500, 100, 1, cus) >= 300 * 112         # k ends inside 16 bytes
     assert mp.mpgemm_run_w8a8_workspace(300, 500, 100, 0, cus) >= 300 * 112 + 500 * 112
     assert mp.mpgemm_run_w8a8_dyn_workspace(1, 4096, 4096, 0, cus) == 0            # quantised by the product
     assert mp.mpgemm_run_w8a8_dyn_workspace(300, 500, 100, 1, cus) >= 300 * 112 + 1200
