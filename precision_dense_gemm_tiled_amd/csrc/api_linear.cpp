@@ -179,7 +179,7 @@ mpgemm_status_t run_i8(mpgemm_handle_t h, const I8Args &a, bool dyn, void *works
     if (!h)
         return MPGEMM_ERR_INVALID_ARG;
     const int mode = a.gated ? mpg::LIN_GATED : mpg::LIN_SCALED;
-    const mpg::LinPlan plan = mpg::plan_lin(mode, a.M, a.N, a.K, h->cu_count);
+    const mpg::LinPlan plan = mpg::plan_lin(mode, a.M, a.N, a.K, 1, h->cu_count);
     const bool fused = dyn && mpg::lin_fuses(plan, a.M, a.K), tile = plan.kind == mpg::LINK_TILE;
     const Codes codes(a.M, a.K);
     Operand oa(a.A, a.lda, a.M, a.K, true), ob(a.B[0], a.ldb[0], a.N, a.K, false), oc(a.B[1], a.ldb[1], a.N, a.K, false);
@@ -240,7 +240,7 @@ int64_t workspace_i8(int64_t M, int64_t N, int64_t K, bool gated, bool dyn, int 
         return -1;
     if (M == 0 || N == 0 || K == 0)
         return 0;
-    const mpg::LinPlan plan = mpg::plan_lin(gated ? mpg::LIN_GATED : mpg::LIN_SCALED, M, N, K, cu_count);
+    const mpg::LinPlan plan = mpg::plan_lin(gated ? mpg::LIN_GATED : mpg::LIN_SCALED, M, N, K, 1, cu_count);
     int64_t n = dyn && !mpg::lin_fuses(plan, M, K) ? Codes(M, K).bytes : 0;
     if (plan.kind == mpg::LINK_TILE && !dyn && (!aligned || K % 16 != 0))
         n += copy_of(M, K);
@@ -362,7 +362,7 @@ mpgemm_status_t mpgemm_run_gated(mpgemm_handle_t h, int64_t M, int64_t N, int64_
         return st;
     if (!h)
         return MPGEMM_ERR_INVALID_ARG;
-    const mpg::LinPlan plan = mpg::plan_lin(mpg::LIN_GATED, M, N, K, h->cu_count);
+    const mpg::LinPlan plan = mpg::plan_lin(mpg::LIN_GATED, M, N, K, 2, h->cu_count);
     Operand ox(X, 2 * ldx, M, 2 * K, true), og(Wg, 2 * ldwg, N, 2 * K, true), ou(Wu, 2 * ldwu, N, 2 * K, true);
     const bool tile = plan.kind == mpg::LINK_TILE;
     if ((st = check_workspace(workspace, workspace_bytes, tile ? copies_of({&ox, &og, &ou}) : 0)) != MPGEMM_OK)
@@ -405,7 +405,7 @@ mpgemm_status_t mpgemm_run_gated(mpgemm_handle_t h, int64_t M, int64_t N, int64_
 int64_t mpgemm_run_gated_workspace(int64_t M, int64_t N, int64_t K, int aligned, int cu_count) {
     if (cu_count <= 0 || !sizes_ok(M, N, K, kMaxAlong))
         return -1;
-    if (M == 0 || N == 0 || K == 0 || (aligned && K % 8 == 0) || mpg::plan_lin(mpg::LIN_GATED, M, N, K, cu_count).kind != mpg::LINK_TILE)
+    if (M == 0 || N == 0 || K == 0 || (aligned && K % 8 == 0) || mpg::plan_lin(mpg::LIN_GATED, M, N, K, 2, cu_count).kind != mpg::LINK_TILE)
         return 0;
     return copy_of(M, 2 * K) + 2 * copy_of(N, 2 * K);
 }
@@ -489,8 +489,8 @@ mpgemm_status_t mpgemm_run_gated_backward(mpgemm_handle_t h, int64_t M, int64_t 
     w.ldb[0] = ox.ld;
     if (need_dx && need_dw)
         return status_of(mpg::launch_gated_pair(type, x, w, mpg::plan_lin_pair(M, part, K, h->cu_count), s));
-    return status_of(need_dx ? mpg::launch_gated_dx(type, x, mpg::plan_lin(mpg::LIN_DX, M, K, N, h->cu_count), s)
-                             : mpg::launch_gated_dw(type, w, mpg::plan_lin(mpg::LIN_DW, 2 * part, K, M, h->cu_count), s));
+    return status_of(need_dx ? mpg::launch_gated_dx(type, x, mpg::plan_lin(mpg::LIN_DX, M, K, 2 * part, 2, h->cu_count), s)
+                             : mpg::launch_gated_dw(type, w, mpg::plan_lin(mpg::LIN_DW, 2 * part, K, M, 2, h->cu_count), s));
 }
 
 int64_t mpgemm_run_gated_backward_workspace(int64_t M, int64_t N, int64_t K, int aligned, int cu_count) {

@@ -59,7 +59,7 @@ struct LinPlan {
     int cfg;    // skinny: fragments of 16 rows; tile: index of the tile table
     int cus;
 };
-LinPlan plan_lin(int mode, int64_t M, int64_t N, int64_t K, int cu_count);
+LinPlan plan_lin(int mode, int64_t M, int64_t N, int64_t K, int elem_bytes, int cu_count);
 LinPlan plan_lin_pair(int64_t M, int64_t part, int64_t K, int cu_count);
 hipError_t launch_w8a8(int type, const Lin &p, const LinPlan &plan, hipStream_t stream);
 hipError_t launch_gated_w8a8(int type, const Lin &p, const LinPlan &plan, hipStream_t stream);

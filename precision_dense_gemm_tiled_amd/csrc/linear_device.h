@@ -249,10 +249,6 @@ __global__ __launch_bounds__(64 * WGM * WGN) void lin_tile_kernel(Lin p) {
     LT::run(p, blockIdx.x, gridDim.x, smem);
 }
 
-// The tile table, and what a round of tiles over all CUs costs against the others.
-struct LinCfg { int BM, BN; double cost; };
-static const LinCfg kLinCfg[] = {{256, 256, 4.0}, {128, 128, 1.25}, {64, 64, 0.5}};
-
 template <class E, typename OUT, int MODE, int BM, int BN, int WGM, int WGN, int NS>
 static void lin_tile_one(const Lin &p, hipStream_t stream) {
     typedef LinTile<E, OUT, MODE, BM, BN, WGM, WGN, NS> LT;

@@ -229,30 +229,33 @@ hipError_t launch_lin_fill(int type, void *c, int64_t ldc, int M, int N, const v
 
 // ------------------------------------------------------------------ plan
 
-// The cheapest tiles for a grid of tiles(c) workgroups.
-template <typename F>
-static int lin_cheapest(int cu_count, F tiles) {
-    int cfg = 0;
-    double best = 0;
-    for (int c = 0; c < 3; ++c) {
-        const double cost = kLinCfg[c].cost * (double)((tiles(c) + cu_count - 1) / cu_count);
-        if (c == 0 || cost < best) {
-            best = cost;
-            cfg = c;
-        }
-    }
-    return cfg;
-}
+// Tiles, and what one takes of a CU's time, in us: apart from its stages, and a stage (128 bytes of k). Tiles of
+// 128 and 64 share a CU and take that long each. Measured: 5 rounds of 64 stages in tiles of 256 491 us (gated
+// 4096 x 10240 x 4096), 2 rounds of 32 in tiles of 128 37 (integers 2048 x 4096 x 4096), 4 in tiles of 64 31.5 (1024 x
+// 4096 x 4096), a launch included.
+struct LinCfg { int BM, BN; double tile, stage; };
+static const LinCfg kLinCfg[] = {{256, 256, 6.0, 1.25}, {128, 128, 2.5, 0.55}, {64, 64, 1.0, 0.22}};
 
 static int64_t lin_tiles(int mode, int c, int64_t M, int64_t N) {
     const int64_t cn = mode == LIN_GATED ? kLinCfg[c].BN / 2 : kLinCfg[c].BN;
     return ((M + kLinCfg[c].BM - 1) / kLinCfg[c].BM) * ((N + cn - 1) / cn);
 }
 
+static double lin_tile_us(int c, int64_t stages) { return kLinCfg[c].tile + kLinCfg[c].stage * (double)stages; }
+
+template <typename F>
+static int lin_cheapest(F us) {
+    int cfg = 0;
+    for (int c = 1; c < 3; ++c)
+        if (us(c) < us(cfg))
+            cfg = c;
+    return cfg;
+}
+
 // Up to 32 rows the skinny kernel, whose workgroups each read all the activations; then tiles.
 // Skinny and tiles of 64, us: integers 32 x 4096 x 4096 8.7 and 10.2, 64 x 4096 x 4096 12.2 and 10.5, 64 x 8192 x 8192 27.8
 // and 22.7, 16 x 8192 x 8192 16.8 and 19.4; gated 16 x 4096 x 4096 14.6 and 18.5, 64 x 4096 x 4096 25.9 and 21.0.
-LinPlan plan_lin(int mode, int64_t M, int64_t N, int64_t K, int cu_count) {
+LinPlan plan_lin(int mode, int64_t M, int64_t N, int64_t K, int elem_bytes, int cu_count) {
     LinPlan pl = {LINK_TILE, 0, cu_count};
     if (K == 0) {
         pl.kind = LINK_EMPTY;
@@ -263,13 +266,19 @@ LinPlan plan_lin(int mode, int64_t M, int64_t N, int64_t K, int cu_count) {
         pl.cfg = M <= 16 ? 1 : 2;
         return pl;
     }
-    pl.cfg = lin_cheapest(cu_count, [&](int c) { return lin_tiles(mode, c, M, N); });
+    const int64_t stages = (K * elem_bytes + 127) / 128;
+    pl.cfg = lin_cheapest([&](int c) { return lin_tile_us(c, stages) * (double)((lin_tiles(mode, c, M, N) + cu_count - 1) / cu_count); });
     return pl;
 }
 
-// Both products of the backward pass in one grid: M x K and 2 part x K results.
+// Both products of the backward pass in one grid, M x K over 2 part and 2 part x K over M: the work spread over the
+// CUs, or the longest tile.
 LinPlan plan_lin_pair(int64_t M, int64_t part, int64_t K, int cu_count) {
-    return {LINK_TILE, lin_cheapest(cu_count, [&](int c) { return lin_tiles(LIN_DX, c, M, K) + lin_tiles(LIN_DW, c, 2 * part, K); }), cu_count};
+    return {LINK_TILE, lin_cheapest([&](int c) {
+                const double x = lin_tile_us(c, 2 * part / 64), w = lin_tile_us(c, (M + 63) / 64);
+                const double all = (x * (double)lin_tiles(LIN_DX, c, M, K) + w * (double)lin_tiles(LIN_DW, c, 2 * part, K)) / cu_count;
+                return all > x ? (all > w ? all : w) : (x > w ? x : w);
+            }), cu_count};
 }
 
 // Few activations: every workgroup of the product quantises all of them.
