@@ -230,7 +230,7 @@ mpgemm_status_t run_i8(mpgemm_handle_t h, const I8Args &a, bool dyn, void *works
     p.act = a.act;
     if (fused) {
         const mpg::LinX x{a.X, a.ldx};
-        return status_of(a.gated ? mpg::launch_gated_w8a8_x(a.type, p, x, s) : mpg::launch_w8a8_x(a.type, p, x, s));
+        return status_of(a.gated ? mpg::launch_gated_w8a8_x(a.type, p, x, plan, s) : mpg::launch_w8a8_x(a.type, p, x, plan, s));
     }
     return status_of(a.gated ? mpg::launch_gated_w8a8(a.type, p, plan, s) : mpg::launch_w8a8(a.type, p, plan, s));
 }

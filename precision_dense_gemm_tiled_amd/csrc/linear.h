@@ -75,8 +75,8 @@ struct LinX {
     const void *x;
     int64_t ldx;
 };
-hipError_t launch_w8a8_x(int type, const Lin &p, const LinX &x, hipStream_t stream);
-hipError_t launch_gated_w8a8_x(int type, const Lin &p, const LinX &x, hipStream_t stream);
+hipError_t launch_w8a8_x(int type, const Lin &p, const LinX &x, const LinPlan &plan, hipStream_t stream);
+hipError_t launch_gated_w8a8_x(int type, const Lin &p, const LinX &x, const LinPlan &plan, hipStream_t stream);
 
 // D = [dG, dU] (M x 2 part, 16 bits, zeros from N to part) from dH, G and U.
 struct GatedGrads {

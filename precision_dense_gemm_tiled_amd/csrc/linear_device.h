@@ -405,12 +405,15 @@ __device__ __forceinline__ void lin_output(const Lin &p, int m, int n, float sa,
 // Up to 32 rows: 16 MF rows x 16 NF columns (of each weight) per workgroup, operands straight from memory
 // into the matrix unit's registers, which read each weight once; K in groups of 128 bytes dealt out to the
 // 8 wavefronts in turn. At step s of a group, lane quarter q takes bytes 64 s + 16 q of its row, so that a
-// load instruction reads 64 contiguous bytes of each of 16 rows. Three groups are on their way
-// from the start on. The wavefronts' sums are joined in LDS in the order of the wavefronts.
-// X: the activations are quantised by every workgroup (MF = 1, few of them).
-template <class E, typename OUT, int MODE, int MF, int NF, bool HALF, bool X>
+// load instruction reads 64 contiguous bytes of each of 16 rows. AHEAD groups are on their way from the
+// start on (three; of 32 rows two: integers 32 x 20480 x 4096 26.2 us, with three 29.4, with one 30.8). The wavefronts'
+// sums are joined in LDS in the order of the wavefronts.
+// X: the activations are quantised by every workgroup (MF = 1, few of them). LOOP: two workgroups per
+// CU go on to further columns with those (gated 1 x 10240 x 4096 17.7 us, 21.7 with a workgroup for each 8
+// columns; where nothing is quantised the loop has no gain: 16 bits 31.9 and 30.8).
+template <class E, typename OUT, int MODE, int MF, int NF, bool HALF, bool X, bool LOOP>
 __global__ __launch_bounds__(64 * LIN_SKINNY_WAVES) void lin_skinny_kernel(Lin p, LinX px) {
-    constexpr int NW = LIN_SKINNY_WAVES, NT = 64 * NW, GB = 128, AHEAD = 3, NB = MODE == LIN_GATED && !HALF ? 2 : 1, EB = sizeof(typename E::T);
+    constexpr int NW = LIN_SKINNY_WAVES, NT = 64 * NW, GB = 128, AHEAD = MF == 1 ? 3 : 2, NB = MODE == LIN_GATED && !HALF ? 2 : 1, EB = sizeof(typename E::T);
     constexpr bool SCALED = EB == 1;
     typedef typename E::Acc Acc;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -420,16 +423,19 @@ __global__ __launch_bounds__(64 * LIN_SKINNY_WAVES) void lin_skinny_kernel(Lin p
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, r = lane & 15;
     constexpr int COLS = HALF ? 8 : 16 * NF;
-    const int n0 = blockIdx.x * COLS;
+    int n0 = blockIdx.x * COLS;
     const int bytes = p.K * EB, full = bytes / GB, groups = (bytes + GB - 1) / GB;
 
     const uint8_t *b[NB][NF], *a[MF];
+    auto columns = [&]() {
 #pragma unroll
-    for (int w = 0; w < NB; ++w)
+        for (int w = 0; w < NB; ++w)
 #pragma unroll
-        for (int j = 0; j < NF; ++j)
-            b[w][j] = HALF ? p.b[r >> 3] + (int64_t)min(n0 + (r & 7), p.N - 1) * p.ldb[r >> 3]
-                           : p.b[w] + (int64_t)min(n0 + 16 * j + r, p.N - 1) * p.ldb[w];
+            for (int j = 0; j < NF; ++j)
+                b[w][j] = HALF ? (r < 8 ? p.b[0] : p.b[1]) + (int64_t)min(n0 + (r & 7), p.N - 1) * (r < 8 ? p.ldb[0] : p.ldb[1])
+                               : p.b[w] + (int64_t)min(n0 + 16 * j + r, p.N - 1) * p.ldb[w];
+    };
+    columns();
 #pragma unroll
     for (int i = 0; i < MF; ++i)
         a[i] = X ? nullptr : p.a + (int64_t)min(16 * i + r, p.M - 1) * p.lda;
@@ -513,13 +519,6 @@ __global__ __launch_bounds__(64 * LIN_SKINNY_WAVES) void lin_skinny_kernel(Lin p
     }
 
     Acc acc[NB][MF][NF];
-#pragma unroll
-    for (int w = 0; w < NB; ++w)
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-            for (int j = 0; j < NF; ++j)
-                acc[w][i][j] = Acc{};
     auto products = [&](const Group &v) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -543,69 +542,90 @@ __global__ __launch_bounds__(64 * LIN_SKINNY_WAVES) void lin_skinny_kernel(Lin p
         if (g + AHEAD * NW < full)
             load_group(g + AHEAD * NW, v);
     };
-    for (int g = wave; g < full; g += AHEAD * NW)
-#pragma unroll
-        for (int d = 0; d < AHEAD; ++d)
-            if (g + d * NW < full)
-                group(g + d * NW, gr[d]);
-    if (groups > full && full % NW == wave) {
-        if constexpr (X) {
-            coded(full, gr[0]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < MF; ++i)
-                load_rest(a[i], full, gr[0].a[i]);
-        }
+    for (;;) {
 #pragma unroll
         for (int w = 0; w < NB; ++w)
 #pragma unroll
-            for (int j = 0; j < NF; ++j)
-                load_rest(b[w][j], full, gr[0].b[w][j]);
-        products(gr[0]);
-    }
-    // register d of lane l: row 4 (l / 16) + d, column l % 16 of the block
+            for (int i = 0; i < MF; ++i)
 #pragma unroll
-    for (int w = 0; w < NB; ++w)
+                for (int j = 0; j < NF; ++j)
+                    acc[w][i][j] = Acc{};
+        for (int g = wave; g < full; g += AHEAD * NW)
 #pragma unroll
-        for (int i = 0; i < MF; ++i)
+            for (int d = 0; d < AHEAD; ++d)
+                if (g + d * NW < full)
+                    group(g + d * NW, gr[d]);
+        if (groups > full && full % NW == wave) {
+            if constexpr (X) {
+                coded(full, gr[0]);
+            } else {
 #pragma unroll
-            for (int j = 0; j < NF; ++j)
+                for (int i = 0; i < MF; ++i)
+                    load_rest(a[i], full, gr[0].a[i]);
+            }
 #pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    red[wave][(w * MF + i) * NF + j][d][lane] = acc[w][i][j][d];
-    __syncthreads();
-    for (int f = tid; f < MF * 16 * COLS; f += NT) {
-        // consecutive threads take consecutive columns
-        constexpr int PARTS = MODE == LIN_GATED ? 2 : 1;
-        const int col = f % COLS, row = f / COLS, i = row / 16, d = row % 4;
-        Num t[PARTS] = {};
+            for (int w = 0; w < NB; ++w)
 #pragma unroll
-        for (int w = 0; w < PARTS; ++w) {
-            const int c = HALF ? col + 8 * w : col, block = ((HALF ? 0 : w) * MF + i) * NF + c / 16;
-#pragma unroll
-            for (int x = 0; x < NW; ++x)
-                t[w] += red[x][block][d][(row % 16) / 4 * 16 + c % 16];
+                for (int j = 0; j < NF; ++j)
+                    load_rest(b[w][j], full, gr[0].b[w][j]);
+            products(gr[0]);
         }
-        const int n = n0 + col;
-        if (row < p.M && n < p.N)
-            lin_output<E, OUT, MODE>(p, row, n, !SCALED ? 1.f : X ? scales[row] : p.sa[row], t);
+        // register d of lane l: row 4 (l / 16) + d, column l % 16 of the block
+#pragma unroll
+        for (int w = 0; w < NB; ++w)
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int j = 0; j < NF; ++j)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        red[wave][(w * MF + i) * NF + j][d][lane] = acc[w][i][j][d];
+        __syncthreads();
+        for (int f = tid; f < MF * 16 * COLS; f += NT) {
+            // consecutive threads take consecutive columns
+            constexpr int PARTS = MODE == LIN_GATED ? 2 : 1;
+            const int col = f % COLS, row = f / COLS, i = row / 16, d = row % 4;
+            Num t[PARTS] = {};
+#pragma unroll
+            for (int w = 0; w < PARTS; ++w) {
+                const int c = HALF ? col + 8 * w : col, block = ((HALF ? 0 : w) * MF + i) * NF + c / 16;
+#pragma unroll
+                for (int x = 0; x < NW; ++x)
+                    t[w] += red[x][block][d][(row % 16) / 4 * 16 + c % 16];
+            }
+            const int n = n0 + col;
+            if (row < p.M && n < p.N)
+                lin_output<E, OUT, MODE>(p, row, n, !SCALED ? 1.f : X ? scales[row] : p.sa[row], t);
+        }
+        if constexpr (!LOOP)
+            break;
+        n0 += gridDim.x * COLS;
+        if (n0 >= p.N)
+            break;
+        columns();
+        first_groups();
+        wait_lds_only();
+        lds_barrier();   // (the sums have been read)
     }
 }
 
 template <class E, typename OUT, int MODE, int MF, int NF, bool HALF, bool X>
-static void lin_skinny_one(const Lin &p, const LinX &x, hipStream_t stream) {
-    constexpr int NB = MODE == LIN_GATED && !HALF ? 2 : 1, COLS = HALF ? 8 : 16 * NF;
+static void lin_skinny_one(const Lin &p, const LinX &x, const LinPlan &plan, hipStream_t stream) {
+    constexpr int NB = MODE == LIN_GATED && !HALF ? 2 : 1, COLS = HALF ? 8 : 16 * NF, NT = 64 * LIN_SKINNY_WAVES;
     const unsigned lds = MF * NB * NF * LIN_SKINNY_WAVES * 1024u + (X ? (unsigned)p.M * ((p.K + 511) / 512 * 512 + 16) + 128 : 0);
-    hipLaunchKernelGGL((lin_skinny_kernel<E, OUT, MODE, MF, NF, HALF, X>), dim3((p.N + COLS - 1) / COLS), dim3(64 * LIN_SKINNY_WAVES), lds, stream,
-                       p, x);
+    const int blocks = (p.N + COLS - 1) / COLS, at_once = 2 * plan.cus;
+    if (X && blocks > at_once)
+        hipLaunchKernelGGL((lin_skinny_kernel<E, OUT, MODE, MF, NF, HALF, X, X>), dim3(at_once), dim3(NT), lds, stream, p, x);
+    else
+        hipLaunchKernelGGL((lin_skinny_kernel<E, OUT, MODE, MF, NF, HALF, X, false>), dim3(blocks), dim3(NT), lds, stream, p, x);
 }
 
 template <class E, typename OUT, int MODE, int NF>
 static void lin_skinny(const Lin &p, const LinPlan &plan, hipStream_t stream) {
     if (plan.cfg == 1)
-        lin_skinny_one<E, OUT, MODE, 1, NF, false, false>(p, LinX{}, stream);
+        lin_skinny_one<E, OUT, MODE, 1, NF, false, false>(p, LinX{}, plan, stream);
     else
-        lin_skinny_one<E, OUT, MODE, 2, NF, false, false>(p, LinX{}, stream);
+        lin_skinny_one<E, OUT, MODE, 2, NF, false, false>(p, LinX{}, plan, stream);
 }
 
 template <class E, typename OUT, int MODE>
@@ -616,7 +636,7 @@ static hipError_t lin_run(const Lin &p, const LinPlan &plan, hipStream_t stream)
         if (MODE == LIN_SCALED && p.N > 16 * plan.cus)
             lin_skinny<E, OUT, MODE, MODE == LIN_SCALED ? 2 : 1>(p, plan, stream);
         else if (MODE == LIN_GATED && p.M <= LIN_HALF_ROWS)
-            lin_skinny_one<E, OUT, MODE, 1, 1, MODE == LIN_GATED, false>(p, LinX{}, stream);
+            lin_skinny_one<E, OUT, MODE, 1, 1, MODE == LIN_GATED, false>(p, LinX{}, plan, stream);
         else
             lin_skinny<E, OUT, MODE, 1>(p, plan, stream);
     } else {
@@ -627,11 +647,11 @@ static hipError_t lin_run(const Lin &p, const LinPlan &plan, hipStream_t stream)
 
 // On integers, the activations quantised in the kernel.
 template <typename OUT, int MODE>
-static hipError_t lin_run_x(const Lin &p, const LinX &x, hipStream_t stream) {
+static hipError_t lin_run_x(const Lin &p, const LinX &x, const LinPlan &plan, hipStream_t stream) {
     if (MODE == LIN_GATED && p.M <= LIN_HALF_ROWS)
-        lin_skinny_one<PtI8, OUT, MODE, 1, 1, MODE == LIN_GATED, true>(p, x, stream);
+        lin_skinny_one<PtI8, OUT, MODE, 1, 1, MODE == LIN_GATED, true>(p, x, plan, stream);
     else
-        lin_skinny_one<PtI8, OUT, MODE, 1, 1, false, true>(p, x, stream);
+        lin_skinny_one<PtI8, OUT, MODE, 1, 1, false, true>(p, x, plan, stream);
     return hipGetLastError();
 }
 

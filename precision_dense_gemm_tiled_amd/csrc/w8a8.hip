@@ -296,11 +296,11 @@ hipError_t launch_w8a8(int type, const Lin &p, const LinPlan &plan, hipStream_t 
     }
 }
 
-hipError_t launch_w8a8_x(int type, const Lin &p, const LinX &x, hipStream_t stream) {
+hipError_t launch_w8a8_x(int type, const Lin &p, const LinX &x, const LinPlan &plan, hipStream_t stream) {
     switch (type) {
-    case MPGEMM_TYPE_F16: return lin_run_x<_Float16, LIN_SCALED>(p, x, stream);
-    case MPGEMM_TYPE_BF16: return lin_run_x<__bf16, LIN_SCALED>(p, x, stream);
-    default: return lin_run_x<float, LIN_SCALED>(p, x, stream);
+    case MPGEMM_TYPE_F16: return lin_run_x<_Float16, LIN_SCALED>(p, x, plan, stream);
+    case MPGEMM_TYPE_BF16: return lin_run_x<__bf16, LIN_SCALED>(p, x, plan, stream);
+    default: return lin_run_x<float, LIN_SCALED>(p, x, plan, stream);
     }
 }
 

@@ -350,3 +350,10 @@ def test_backward_with_very_long_rows(mp, K):
         want = lu.gated_backward(*(v.cpu() for v in (dh, x[:, k], wg[:, k], wu[:, k], g, u)), "silu", dt)
         for y, (w, e) in zip(got, want):
             lu.check(y[:, k], w, e)
+
+
+# So many columns that the workgroups that have quantised the rows go on to further ones.
+@pytest.mark.parametrize("M,N,K", [(1, 12291, 260), (3, 4100, 515), (4, 9001, 4096), (7, 16399, 130)])
+@pytest.mark.parametrize("t", lu.TYPES)
+def test_on_integers_with_many_columns(mp, M, N, K, t):
+    test_on_integers(mp, M, N, K, t)

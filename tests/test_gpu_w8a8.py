@@ -234,3 +234,19 @@ def test_quantize_of_very_many_rows(mp):
     assert int((s != 0).sum()) == len(at)
     y = mp.dequantize_i8(q, s, dtype=torch.float16)
     assert torch.equal(y[at], mp.dequantize_i8(wq, ws, dtype=torch.float16))
+
+
+# So many columns that the workgroups that have quantised the rows go on to further ones.
+@pytest.mark.parametrize("M,N,K", [(1, 8193, 700), (1, 20003, 64), (5, 24579, 1000), (8, 16399, 2048)])
+@pytest.mark.parametrize("t", lu.TYPES)
+def test_quantised_in_the_call_with_many_columns(mp, M, N, K, t):
+    dt = lu.TYPES[t]
+    g = gen(M + N + K)
+    x = torch.randn(M, K, generator=g).to(dt)
+    q, s = lu.quantize(torch.randn(N, K, generator=g))
+    w = lu.on_gpu((q.to(torch.int8), s))
+    bias = torch.randn(N, generator=g).to(dt).cuda()
+    y = mp.gemm_w8a8_dyn(x.cuda(), *w, bias=bias)
+    want, mag = lu.scaled(lu.quantize(x), (q, s), bias.cpu())
+    lu.check(y, want, lu.scaled_tol(want, mag, dt))
+    assert torch.equal(y, mp.gemm_w8a8(*mp.quantize_i8(x.cuda()), *w, bias=bias, dtype=dt))
