@@ -261,7 +261,11 @@ static void lin_tile(const Lin &p, const LinPlan &plan, hipStream_t stream) {
     switch (plan.cfg) {
     case 0: lin_tile_one<E, OUT, MODE, 256, 256, 2, 4, 2>(p, stream); break;
     case 1: lin_tile_one<E, OUT, MODE, 128, 128, 2, 2, 2>(p, stream); break;
-    default: lin_tile_one<E, OUT, MODE, 64, 64, 2, 2, 4>(p, stream); break;
+    case 2: lin_tile_one<E, OUT, MODE, 64, 64, 2, 2, 4>(p, stream); break;
+    default:
+        if constexpr (MODE == LIN_SCALED || MODE == LIN_GATED)
+            lin_tile_one<E, OUT, MODE, 64, 128, 2, 2, 4>(p, stream);
+        break;
     }
 }
 

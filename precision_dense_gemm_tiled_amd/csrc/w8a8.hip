@@ -229,12 +229,13 @@ hipError_t launch_lin_fill(int type, void *c, int64_t ldc, int M, int N, const v
 
 // ------------------------------------------------------------------ plan
 
-// Tiles, and what one takes of a CU's time, in us: apart from its stages, and a stage (128 bytes of k). Tiles of
-// 128 and 64 share a CU and take that long each. Measured: 5 rounds of 64 stages in tiles of 256 491 us (gated
-// 4096 x 10240 x 4096), 2 rounds of 32 in tiles of 128 37 (integers 2048 x 4096 x 4096), 4 in tiles of 64 31.5 (1024 x
-// 4096 x 4096), a launch included.
-struct LinCfg { int BM, BN; double tile, stage; };
-static const LinCfg kLinCfg[] = {{256, 256, 6.0, 1.25}, {128, 128, 2.5, 0.55}, {64, 64, 1.0, 0.22}};
+// Tiles, what one takes of a CU's time, in us, apart from its stages and for a stage (128 bytes of k), and how many
+// are on a CU at once (LDS). Measured, with 2.5 us of a launch: 5 rounds of 64 stages in tiles of 256 491 us (gated 4096 x 10240 x
+// 4096), 2 of 16 47.7; 4.3 of 16 in tiles of 128 38.3 (gated 1920 x 4736 x 1024), one of 32 18.6; 17 of 6 in tiles of 64 35.9 (gated
+// 1088 x 8192 x 384), one of 32 10.9. The last, of the forward products only, is between the two small ones: integers 200 x
+// 8192 x 8192 in one round 27.4 us, in two of 64 x 64 32.5, in one of 128 x 128 39.8; 333 x 5000 x 2112 11.8, 12.7 and 14.0.
+struct LinCfg { int BM, BN; double tile, stage; int at_once; };
+static const LinCfg kLinCfg[] = {{256, 256, 6.0, 1.25, 1}, {128, 128, 1.4, 0.46, 2}, {64, 64, 1.0, 0.2, 2}, {64, 128, 2.6, 0.34, 1}};
 
 static int64_t lin_tiles(int mode, int c, int64_t M, int64_t N) {
     const int64_t cn = mode == LIN_GATED ? kLinCfg[c].BN / 2 : kLinCfg[c].BN;
@@ -244,9 +245,9 @@ static int64_t lin_tiles(int mode, int c, int64_t M, int64_t N) {
 static double lin_tile_us(int c, int64_t stages) { return kLinCfg[c].tile + kLinCfg[c].stage * (double)stages; }
 
 template <typename F>
-static int lin_cheapest(F us) {
+static int lin_cheapest(int cfgs, F us) {
     int cfg = 0;
-    for (int c = 1; c < 3; ++c)
+    for (int c = 1; c < cfgs; ++c)
         if (us(c) < us(cfg))
             cfg = c;
     return cfg;
@@ -267,14 +268,18 @@ LinPlan plan_lin(int mode, int64_t M, int64_t N, int64_t K, int elem_bytes, int 
         return pl;
     }
     const int64_t stages = (K * elem_bytes + 127) / 128;
-    pl.cfg = lin_cheapest([&](int c) { return lin_tile_us(c, stages) * (double)((lin_tiles(mode, c, M, N) + cu_count - 1) / cu_count); });
+    pl.cfg = lin_cheapest(mode == LIN_SCALED || mode == LIN_GATED ? 4 : 3, [&](int c) {
+        // rounds over the CUs, of two tiles at once in halves
+        const int64_t n = kLinCfg[c].at_once, rounds = (n * lin_tiles(mode, c, M, N) + cu_count - 1) / cu_count;
+        return lin_tile_us(c, stages) * (rounds > n ? (double)rounds / (double)n : 1.0);
+    });
     return pl;
 }
 
 // Both products of the backward pass in one grid, M x K over 2 part and 2 part x K over M: the work spread over the
 // CUs, or the longest tile.
 LinPlan plan_lin_pair(int64_t M, int64_t part, int64_t K, int cu_count) {
-    return {LINK_TILE, lin_cheapest([&](int c) {
+    return {LINK_TILE, lin_cheapest(3, [&](int c) {
                 const double x = lin_tile_us(c, 2 * part / 64), w = lin_tile_us(c, (M + 63) / 64);
                 const double all = (x * (double)lin_tiles(LIN_DX, c, M, K) + w * (double)lin_tiles(LIN_DW, c, 2 * part, K)) / cu_count;
                 return all > x ? (all > w ? all : w) : (x > w ? x : w);
