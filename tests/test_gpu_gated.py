@@ -357,3 +357,48 @@ def test_backward_with_very_long_rows(mp, K):
 @pytest.mark.parametrize("t", lu.TYPES)
 def test_on_integers_with_many_columns(mp, M, N, K, t):
     test_on_integers(mp, M, N, K, t)
+
+
+# Rows 2^23 bytes apart and more: above 32 rows from a copy, below as they are.
+@pytest.mark.parametrize("M", [2, 20, 70])
+def test_rows_far_apart(mp, M):
+    K, ld = 72, 4_200_000
+    gg = torch.Generator(device="cuda").manual_seed(M)
+    far = lambda rows: torch.empty(rows, ld, dtype=torch.bfloat16, device="cuda")[:, :K].copy_(torch.randn(rows, K, generator=gg, device="cuda"))  # noqa: E731
+    x, wg, wu = far(M), far(40), far(40)
+    near = [v.contiguous() for v in (x, wg, wu)]
+    h, g, u = mp.gemm_gated(x, wg, wu, keep=True)
+    assert all(torch.equal(a, b) for a, b in zip((h, g, u), mp.gemm_gated(*near, keep=True)))
+    dh = torch.randn(M, 40, generator=gg, device="cuda").bfloat16()
+    got = mp.gemm_gated_backward(dh, x, wg, wu, g, u)
+    assert all(torch.equal(a, b) for a, b in zip(got, mp.gemm_gated_backward(dh, *near, g, u)))
+    q, s = mp.quantize_i8(x)
+    qn, sn = mp.quantize_i8(near[0])
+    assert torch.equal(q, qn) and torch.equal(s, sn)
+
+
+# Calls that share the handle, side by side on two streams, each with its own scratch memory.
+def test_two_streams_at_once(mp):
+    dt = torch.bfloat16
+    gg = gen(5)
+    x, wg, wu = (v.cuda() for v in block(gg, 300, 200, 136, dt))
+    dh = torch.randn(300, 200, generator=gg).to(dt).cuda()
+    t = torch.randn(3, 521, generator=gg).to(dt).cuda()
+    w = [mp.quantize_i8(torch.randn(5000, 521, generator=gg).cuda()) for _ in range(2)]
+
+    def train(**kw):
+        h, g, u = mp.gemm_gated(x, wg, wu, keep=True, **kw)
+        return [h, *mp.gemm_gated_backward(dh, x, wg, wu, g, u, **kw)]
+
+    def serve(**kw):
+        return [mp.gemm_gated_w8a8_dyn(t, *w[0], *w[1], **kw), mp.gemm_w8a8_dyn(x, *mp.quantize_i8(wg, **kw), **kw)]
+
+    want = [train(), serve()]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for i in range(8):
+        for k, f in enumerate((train, serve)):
+            got[(i + k) % 2].append((k, f(stream=streams[(i + k) % 2])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for side in got for k, v in side for a, b in zip(v, want[k]))
