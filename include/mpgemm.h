@@ -12,6 +12,9 @@
  *                     fp16 scales, fp32 accumulate, fp16 Y
  *   mpgemm_run_w4a4   int4 x int4 with per-row and per-column fp16 scales and
  *                     a column bias applied to the exact int32 sum, fp16 Y
+ *   mpgemm_run_w8a8   int8 x int8 with an fp32 scale per row of either operand and
+ *                     a column bias applied to the exact int32 sum
+ *   mpgemm_run_gated  act(A Bg^T) * (A Bu^T) in fp16 or bf16, and its gradients
  *   mpgemm_run_{f16,i8,i4}_kn  the first three with B stored K x N (the
  *                     transposed layout, kept as a measured control)
  *

@@ -11,7 +11,8 @@
 namespace mpg {
 
 // 8 columns of a row per thread, 2^lx threads side by side in a row (a power of two: no division by a
-// row's pieces), the rest of the workgroup's 256 over rows. Bound by memory: 10 bytes per element of dH.
+// row's pieces), the rest of the workgroup's 256 over rows. Bound by memory: 10 bytes per element of dH, 4096 x 10240 in 63 us
+// (6.7 TB/s, some of it from the last level of cache).
 template <typename T, int ACT>
 __global__ __launch_bounds__(256) void gated_grads_kernel(GatedGrads p, int lx) {
     const int parts = (p.part / 8 + (1 << lx) - 1) >> lx, rb = blockIdx.x / parts;
@@ -73,7 +74,9 @@ hipError_t launch_gated_grads(int type, const GatedGrads &p, hipStream_t stream)
 }
 
 // Both products in one grid, first the tiles of dX, whose sums are longer: dW's run beside them and
-// a launch less is waited for (777 x 1000 x 520, f16: PAIRUS).
+// a launch less is waited for (777 x 1000 x 520, f16: 22.0 us, in two launches 28.6). Bound by the
+// matrix units' power like the forward pass: 4096 x 10240 x 4096 in bf16 940 to 1000 us for 1374 GFLOP (the library's two
+// products, one with its right operand and one with both across k, 519 and 613), behind 63 us of gated_grads_kernel.
 template <class E, typename OUT, int BM, int BN, int WGM, int WGN, int NS>
 __global__ __launch_bounds__(64 * WGM * WGN) void gated_pair_kernel(Lin dx, Lin dw, int first) {
     typedef LinTile<E, OUT, LIN_DX, BM, BN, WGM, WGN, NS> X;

