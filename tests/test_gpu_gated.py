@@ -402,3 +402,13 @@ def test_two_streams_at_once(mp):
             got[(i + k) % 2].append((k, f(stream=streams[(i + k) % 2])))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for side in got for k, v in side for a, b in zip(v, want[k]))
+
+
+# Large tiles that do not go round the CUs evenly.
+@pytest.mark.parametrize("M,N,K", [(2100, 5200, 600), (1800, 4500, 1030), (4097, 2200, 520)])
+def test_forward_in_uneven_rounds_of_tiles(mp, M, N, K):
+    dt = torch.bfloat16
+    x, wg, wu = block(gen(N), M, N, K, dt)
+    got = mp.gemm_gated(x.cuda(), wg.cuda(), wu.cuda(), keep=True)
+    for y, w, e in zip(got, *lu.gated(x, wg, wu, "silu")):
+        lu.check(y, w, lu.rounded_tol(w, e, dt))

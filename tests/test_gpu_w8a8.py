@@ -250,3 +250,14 @@ def test_quantised_in_the_call_with_many_columns(mp, M, N, K, t):
     want, mag = lu.scaled(lu.quantize(x), (q, s), bias.cpu())
     lu.check(y, want, lu.scaled_tol(want, mag, dt))
     assert torch.equal(y, mp.gemm_w8a8(*mp.quantize_i8(x.cuda()), *w, bias=bias, dtype=dt))
+
+
+# Large tiles that do not go round the CUs evenly.
+@pytest.mark.parametrize("M,N,K", [(2100, 10300, 1030), (4100, 5000, 2048), (777, 23000, 1040)])
+def test_product_in_uneven_rounds_of_tiles(mp, M, N, K):
+    g = gen(N)
+    a, b = (torch.randint(-127, 128, s, generator=g, dtype=torch.int8) for s in ((M, K), (N, K)))
+    one = [torch.ones(n, device="cuda") for n in (M, N)]
+    c = mp.gemm_w8a8(a.cuda(), one[0], b.cuda(), one[1])
+    want = (a.double() @ b.double().t()).float()   # (exact, then one rounding)
+    assert torch.equal(c.cpu(), want)
