@@ -380,7 +380,9 @@ __device__ __forceinline__ uint2 i8_codes8(const float (&v)[8], const I8Row &r) 
 }
 
 constexpr int LIN_SKINNY_WAVES = 8;
-constexpr int LIN_HALF_ROWS = 4;   // GATED: up to here 8 columns of either weight per workgroup, in one fragment
+// GATED: up to here 8 columns of either weight per workgroup, in one fragment, else 16 in two (16 bits, through 10240 x 4096: 4 rows
+// 31.8 us, in two 36.0; 8 rows 35.8 and 36.4, on integers 21.5 and 19.6).
+constexpr int LIN_HALF_ROWS = 4;
 constexpr int LIN_X_MAX = 32;   // rows of 512 activations, a wavefront's load, that the fused kernel takes
 
 // One output from its sums (of either weight).
@@ -639,7 +641,8 @@ template <class E, typename OUT, int MODE>
 static hipError_t lin_run(const Lin &p, const LinPlan &plan, hipStream_t stream) {
     if (plan.kind == LINK_SKINNY) {
         // 32 columns per workgroup, 16 of two weights or 32 of one, once 16 would go round the CUs more than
-        // once: the activations are then read half as often.
+        // once: the activations are then read half as often (16 rows through 6144 x 4096 8.3 us, with 16 columns
+        // 10.1; through 4096 x 4096 8.2 and 6.8).
         if (MODE == LIN_SCALED && p.N > 16 * plan.cus)
             lin_skinny<E, OUT, MODE, MODE == LIN_SCALED ? 2 : 1>(p, plan, stream);
         else if (MODE == LIN_GATED && p.M <= LIN_HALF_ROWS)

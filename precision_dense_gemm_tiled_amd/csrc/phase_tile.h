@@ -124,9 +124,10 @@ struct PhaseTile {
         }
     }
 
-    // Loads of half h of stage e into `lds`, stage after stage (at_k, across k: where the next stage begins). Buffer loads: one 32-bit offset per load in registers
-    // (the 64-bit addresses of the global form do not fit beside the sums), and what is past the
-    // operand's end gets an offset out of the buffer's range, which loads zeros. Kernels with
+    // Loads of half h of stage e into `lds`, stage after stage (at_k, across k: where the next
+    // stage begins). Buffer loads: one 32-bit offset per load in registers (the 64-bit addresses
+    // of the global form do not fit beside the sums), and what is past the operand's end gets an
+    // offset out of the buffer's range, which loads zeros. Kernels with
     // transposing reads write the load as an instruction of its own: the compiler takes those
     // reads as possible uses of any load to LDS before them and would wait for all loads in
     // front of each (4096 x 4096 x 20480 with B across k: 579 us, 461 without those waits;

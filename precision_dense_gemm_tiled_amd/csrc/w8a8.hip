@@ -236,6 +236,7 @@ hipError_t launch_lin_fill(int type, void *c, int64_t ldc, int M, int N, const v
 // 4096), 2 of 16 47.7; 4.3 of 16 in tiles of 128 38.3 (gated 1920 x 4736 x 1024), one of 32 18.6; 17 of 6 in tiles of 64 35.9 (gated
 // 1088 x 8192 x 384), one of 32 10.9. The last, of the forward products only, is between the two small ones: integers 200 x
 // 8192 x 8192 in one round 27.4 us, in two of 64 x 64 32.5, in one of 128 x 128 39.8; 333 x 5000 x 2112 11.8, 12.7 and 14.0.
+// Up to 128 x 128 a stage takes its bytes at about 70 a ns on their way into the CU, whatever the number of stages ahead.
 struct LinCfg { int BM, BN; double tile, stage; int at_once; };
 static const LinCfg kLinCfg[] = {{256, 256, 6.0, 1.25, 1}, {128, 128, 1.4, 0.46, 2}, {64, 64, 1.0, 0.2, 2}, {64, 128, 2.6, 0.34, 1}};
 
@@ -288,9 +289,12 @@ LinPlan plan_lin_pair(int64_t M, int64_t part, int64_t K, int cu_count) {
             }), cu_count};
 }
 
-// Few activations: every workgroup of the product quantises all of them.
+// Few activations: every workgroup of the product quantises all of them. In wavefront loads of 512 of a row, up to 16, of one
+// or two rows up to 32. In the product and by a launch before it, us: 1 x 4096 x 4096 6.1 and 8.2, 1 x 8192 x 16384 29.7 and
+// 37.3, 2 x 8192 x 8192 15.5 and 18.9, 2 x 4096 x 8192 11.9 and 11.0, 4 x 4096 x 2048 5.8 and 7.0, 8 x 4096 x 1024 5.2 and 5.5; 4 x 8192 x
+// 4096 12.8 and 11.2, 8 x 8192 x 2048 10.9 and 8.6, 16 x 4096 x 1024 7.3 and 5.8.
 bool lin_fuses(const LinPlan &plan, int64_t M, int64_t K) {
-    return plan.kind == LINK_SKINNY && M <= 16 && M * ((K + 511) / 512) <= LIN_X_MAX;
+    return plan.kind == LINK_SKINNY && M <= 16 && M * ((K + 511) / 512) <= (M <= 2 ? LIN_X_MAX : LIN_X_MAX / 2);
 }
 
 // ------------------------------------------------------------------ product
