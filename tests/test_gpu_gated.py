@@ -412,3 +412,22 @@ def test_forward_in_uneven_rounds_of_tiles(mp, M, N, K):
     got = mp.gemm_gated(x.cuda(), wg.cuda(), wu.cuda(), keep=True)
     for y, w, e in zip(got, *lu.gated(x, wg, wu, "silu")):
         lu.check(y, w, lu.rounded_tol(w, e, dt))
+
+
+# The C call with any of the three gradients left out.
+@pytest.mark.parametrize("M,N,K", [(70, 100, 136), (300, 520, 264)])
+def test_backward_of_some_gradients(mp, M, N, K):
+    dt = torch.bfloat16
+    gg = torch.Generator(device="cuda").manual_seed(M)
+    dh, x, wg, wu, g, u = (torch.randn(*s, generator=gg, device="cuda").to(dt) for s in ((M, N), (M, K), (N, K), (N, K), (M, N), (M, N)))
+    want = mp.gemm_gated_backward(dh, x, wg, wu, g, u)
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    ws = torch.empty(mp.mpgemm_run_gated_backward_workspace(M, N, K, 1, cus), dtype=torch.uint8, device="cuda")
+    for take in range(1, 8):
+        out = [torch.empty_like(v) if take >> i & 1 else None for i, v in enumerate(want)]
+        p = [None if v is None else v.data_ptr() for v in out]
+        assert mp.mpgemm_run_gated_backward(mp.default_handle(0), M, N, K, 1, 0, dh.data_ptr(), N, x.data_ptr(), K, wg.data_ptr(), K, wu.data_ptr(), K,
+                                            g.data_ptr(), N, u.data_ptr(), N, p[0], K, p[1], K, p[2], K, ws.data_ptr(), ws.numel(),
+                                            torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert all(v is None or torch.equal(v, w) for v, w in zip(out, want))
