@@ -66,15 +66,17 @@ bool sizes_ok(int64_t M, int64_t N, int64_t K, int64_t along) {
 }
 
 // An operand of a tile kernel: its rows as they are, or a copy in the workspace where they do
-// not start at multiples of 16 bytes, lie too far apart, or (padded) end inside 16 bytes that have to
-// hold zeros behind them.
+// not start at multiples of 16 bytes, lie too far apart (a single row has no stride: its length is none), or
+// (padded) end inside 16 bytes that have to hold zeros behind them.
 struct Operand {
     const uint8_t *p;
     int64_t ld, rows, bytes;   // ld and bytes of a row, in bytes
     bool padded;
     Operand(const void *at, int64_t stride, int64_t r, int64_t row_bytes, bool pad)
         : p(static_cast<const uint8_t *>(at)), ld(r <= 1 ? round_up(row_bytes, 16) : stride), rows(r), bytes(row_bytes), padded(pad) {}
-    bool needs_copy() const { return misaligned(p, 16) || ld % 16 != 0 || ld >= kMaxStride || (padded && bytes % 16 != 0); }
+    bool needs_copy() const {
+        return misaligned(p, 16) || ld % 16 != 0 || (rows > 1 && ld >= kMaxStride) || (padded && bytes % 16 != 0);
+    }
     int64_t copy_bytes() const { return round_up(rows * round_up(bytes, 16), 256); }
 };
 
