@@ -493,12 +493,9 @@ PyObject *quantize_i8(PyObject *const *a) {
     const int type = type_of(X.scalar_type(), "X");
     const int64_t ldx = rows_of(X, X.scalar_type(), "X"), M = X.size(0), K = X.size(1), ld = std::max<int64_t>((K + 15) / 16 * 16, 16);
     const at::Device dev = X.device();
-    // (one allocation: the codes, then the scales)
-    at::Tensor q = empty({M * (ld + 4)}, at::kChar, dev);
-    at::Tensor s = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(q.storage()), q.key_set(), caffe2::TypeMeta::Make<float>());
+    // (an allocation each: tensors of two types over one storage cannot be saved)
+    at::Tensor q = empty({M, ld}, at::kChar, dev), s = empty({M}, at::kFloat, dev);
     q.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef{M, K}, at::IntArrayRef{ld, 1});
-    s.unsafeGetTensorImpl()->set_storage_offset(M * ld / 4);
-    s.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef{M}, at::IntArrayRef{1});
     if (K == 0)
         s.zero_();
     check(mpgemm_quantize_i8(handle_of(a[1], dev), M, K, type, X.data_ptr(), ldx, static_cast<int8_t *>(q.data_ptr()), ld,

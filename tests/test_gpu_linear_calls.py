@@ -36,3 +36,20 @@ def test_backward_of_one_long_row(mp, M, N, K, need, at):
         for y, (w, e) in zip(got, want):
             if y is not None:
                 lu.check(y[:, k], w, e)
+
+
+# Weights brought into integers are kept in a checkpoint: codes and scales save and load, alone and together.
+@pytest.mark.parametrize("N,K", [(40, 200), (64, 512), (1, 7), (3, 16)])
+def test_held_matrices_are_saved_and_loaded(mp, tmp_path, N, K):
+    gg = torch.Generator(device="cuda").manual_seed(N)
+    x = torch.randn(5, K, generator=gg, device="cuda").bfloat16()
+    q, s = mp.quantize_i8(torch.randn(N, K, generator=gg, device="cuda"))
+    assert q.untyped_storage().data_ptr() != s.untyped_storage().data_ptr()
+    assert s.untyped_storage().nbytes() == 4 * N   # (and scales alone keep no codes)
+    want = mp.gemm_w8a8_dyn(x, q, s)
+    torch.save({"q": q, "s": s}, tmp_path / "held.pt")
+    held = torch.load(tmp_path / "held.pt", weights_only=True)
+    assert torch.equal(held["q"], q) and torch.equal(held["s"], s)
+    assert torch.equal(mp.gemm_w8a8_dyn(x, held["q"], held["s"]), want)
+    host = torch.load(tmp_path / "held.pt", weights_only=True, map_location="cpu")
+    assert torch.equal(mp.gemm_w8a8_dyn(x, host["q"].cuda(), host["s"].cuda()), want)
