@@ -15,12 +15,33 @@ __device__ __forceinline__ float lin_sigmoid(float v) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * v));
 }
 
+// exp(-v^2 / 2), and with it (1 + erf(v / sqrt 2)) / 2, the normal distribution at v, to a few 2^-23 of its value: 1 + erf
+// cancels far below zero (at -5.5 in fp32 the sum is 0, half of it should be 1.9e-8). The distribution at -a over exp(-a^2 / 2) is
+// t P(t), t = 1 / (1 + 0.21 a), with a polynomial of degree 8 fitted in 64 bits to the least relative error over a from 0 to
+// 13.5 (1.3e-8; past that the exponential is 0). (Gated 2048 x 10240 x 4096 on integers with gelu 166 us; by erfc 188, by 1 + erf
+// 176; with silu 156.)
+__device__ __forceinline__ float lin_bell(float v) { return __builtin_amdgcn_exp2f(-0.72134752f * v * v); }
+__device__ __forceinline__ float lin_normal(float v, float bell) {
+    const float t = __builtin_amdgcn_rcpf(1.f + 0.21f * fabsf(v));
+    float p = -0.0720338523f;
+    p = fmaf(p, t, 0.285452783f);
+    p = fmaf(p, t, -0.334188461f);
+    p = fmaf(p, t, 0.354032308f);
+    p = fmaf(p, t, -0.0972447917f);
+    p = fmaf(p, t, 0.126354769f);
+    p = fmaf(p, t, 0.0687901378f);
+    p = fmaf(p, t, 0.0851293951f);
+    p = fmaf(p, t, 0.0837077051f);
+    const float tail = bell * (t * p);
+    return v < 0.f ? tail : 1.f - tail;
+}
+
 template <int ACT>
 __device__ __forceinline__ float lin_act(float v) {
     if constexpr (ACT == MPGEMM_ACT_SILU)
         return v * lin_sigmoid(v);
     else if constexpr (ACT == MPGEMM_ACT_GELU)
-        return 0.5f * v * (1.f + erff(v * 0.70710678f));
+        return v * lin_normal(v, lin_bell(v));
     else   // 0.5 (1 + tanh z) = sigmoid(2 z)
         return v * lin_sigmoid(1.59576912f * (v + 0.044715f * v * v * v));
 }
@@ -33,7 +54,8 @@ __device__ __forceinline__ float lin_slope(float v) {
         const float s = lin_sigmoid(v);
         return s + s * (1.f - s) * w;
     } else if constexpr (ACT == MPGEMM_ACT_GELU) {
-        return 0.5f * (1.f + erff(v * 0.70710678f)) + 0.39894228f * w * __builtin_amdgcn_exp2f(-0.72134752f * w * w);
+        const float bell = lin_bell(v);
+        return lin_normal(v, bell) + 0.39894228f * w * bell;
     } else {
         const float s = lin_sigmoid(1.59576912f * (v + 0.044715f * v * v * v));
         return s + s * (1.f - s) * w * 1.59576912f * (1.f + 0.134145f * w * w);

@@ -1,5 +1,7 @@
 """Calls of the 8-bit integer layer and the gated block at the ends of what they take: single rows of great length, held
 matrices that are saved and loaded, gates far below zero, gradients that only one weight needs."""
+import math
+
 import pytest
 import torch
 
@@ -53,3 +55,89 @@ def test_held_matrices_are_saved_and_loaded(mp, tmp_path, N, K):
     assert torch.equal(mp.gemm_w8a8_dyn(x, held["q"], held["s"]), want)
     host = torch.load(tmp_path / "held.pt", weights_only=True, map_location="cpu")
     assert torch.equal(mp.gemm_w8a8_dyn(x, host["q"].cuda(), host["s"].cuda()), want)
+
+
+EPS = 2.0 ** -23
+
+
+def act64(name, v):
+    """The activation and its derivative in 64 bits, to their last digits far below zero (there 1 + tanh z is taken as 2 sigmoid(2 z))."""
+    if name != "gelu_tanh":
+        return lu.act(name, v)
+    c = 2 * math.sqrt(2 / math.pi)
+    s = torch.sigmoid(c * (v + 0.044715 * v ** 3))
+    return v * s, s + v * s * (1 - s) * c * (1 + 3 * 0.044715 * v * v)
+
+
+def act_rel(name, v):
+    """What the fp32 evaluation of an activation may be off by, relative to its value. silu: the exponent's argument |v| with a rounded constant
+    and product (1 EPS together), exp2 and the reciprocal 1 EPS each, the sum and the product half a one each. gelu_tanh: its argument z has nine
+    roundings of half an EPS. gelu: the normal distribution at v as an exponential whose argument v^2 / 2 has three roundings of
+    half an EPS, exp2 and a reciprocal (1 EPS each, 1 for the reciprocal's argument), a polynomial (its fit, its coefficients' and its steps'
+    roundings: 3.5) and three products."""
+    a = v.abs()
+    if name == "silu":
+        return (a + 4) * EPS
+    if name == "gelu_tanh":
+        return (4.5 * 1.59577 * (a + 0.044715 * a ** 3) + 4) * EPS
+    return (8 + 0.75 * v * v) * EPS
+
+
+# Far below zero an activation is small beside its gate and keeps its digits all the same. Integers with one code for each gate:
+# G = -1 |v| 1, U = -1 |v| (1 / 2), H = act(v) v / 2.
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [1, 4, 20, 32, 600])
+def test_activations_far_below_zero(mp, name, M):
+    v = -torch.cat([torch.linspace(0.01, 9, max(M - 1, 1)), torch.tensor([5.5])])[-M:]
+    N = 40
+    a = torch.full((M, 1), -1, dtype=torch.int8, device="cuda"), -v.cuda()
+    one = torch.ones(N, 1, dtype=torch.int8, device="cuda")
+    h = mp.gemm_gated_w8a8(*a, one, torch.ones(N, device="cuda"), one, torch.full((N,), 0.5, device="cuda"), act=name, dtype=torch.float32)
+    v = v.double()[:, None].expand(M, N)
+    want = act64(name, v)[0] * v / 2
+    lu.check(h, want, want.abs() * (act_rel(name, v) + 0.51 * EPS) + 2.0 ** -126)
+
+
+# The same in 16 bits, with the backward pass: tokens are rows of the identity, so that dWg and dWu are dG and dU as they were rounded.
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+def test_gradients_far_below_zero(mp, name):
+    dt, M, N = torch.bfloat16, 64, 48
+    g = -torch.linspace(0.01, 9, M * N).reshape(M, N).to(dt)
+    one = torch.ones(M, N, dtype=dt)
+    dh, x, gd = one.cuda(), torch.eye(M, dtype=dt, device="cuda"), g.cuda()
+    dx, dwg, dwu = mp.gemm_gated_backward(dh, x, None, None, gd, dh, act=name, need_dx=False)
+    v = g.double()
+    a, slope = act64(name, v)
+    lu.check(dwu.t(), a, lu.rounded_tol(a, a.abs() * act_rel(name, v), dt))
+    # the slope is a sum: the sigmoid (a over v) and what is left, by the same roundings and four more products and sums
+    part = (a / v).abs()
+    err = (part + (slope - a / v).abs()) * (act_rel(name, v) + 4 * EPS)
+    if name == "silu":
+        err = err + part * 2 * EPS * v.abs()      # (1 - s, off by 1 EPS, times v)
+    if name == "gelu_tanh":
+        err = err + part * 2 * EPS * (v.abs() * 1.6 * (1 + 0.134145 * v * v))
+    lu.check(dwg.t(), slope, lu.rounded_tol(slope, err, dt))
+    # forward: G = g exactly, U = 1
+    wg, wu = torch.zeros(N, 8, dtype=dt), torch.zeros(N, 8, dtype=dt)
+    wg[:, 0] = g[0]
+    wu[:, 1] = 1
+    for rows in (1, 3, 20, 100):
+        t = torch.zeros(rows, 8, dtype=dt)
+        t[:, :2] = 1
+        h = mp.gemm_gated(t.cuda(), wg.cuda(), wu.cuda(), act=name)
+        want = a[:1].expand(rows, N)
+        lu.check(h, want, lu.rounded_tol(want, want.abs() * act_rel(name, v[:1]), dt))
+
+
+# Gates that are not finite: the derivative of NaN is NaN, at the ends it is 0 and 1.
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+def test_slopes_of_gates_that_are_not_finite(mp, name):
+    dt = torch.bfloat16
+    g = torch.tensor([[float("nan"), float("inf"), -float("inf"), 3e38, -3e38, 0.0, -0.0, 1.0]], dtype=dt, device="cuda")
+    one = torch.ones_like(g)
+    dx, dwg, dwu = mp.gemm_gated_backward(one, torch.ones(1, 8, dtype=dt, device="cuda"), None, None, g, one, act=name, need_dx=False)
+    want = lu.act(name, torch.tensor([1.0]))[1].to(dt).item()
+    got = dwg[:, 0].tolist()
+    assert math.isnan(got[0]) and got[1:7] == [1.0, 0.0, 1.0, 0.0, 0.5, 0.5] and abs(got[7] - want) <= 2.0 ** -8 * want
+    act = dwu[:, 0].tolist()
+    assert math.isnan(act[0]) and act[1] == float("inf") and act[3] > 2.9e38 and act[4:7] == [0.0, 0.0, 0.0]
