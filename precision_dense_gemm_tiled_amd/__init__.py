@@ -738,7 +738,7 @@ def newton_schulz(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out=No
 
 def quantize_i8(X, handle=None, stream=None):
     """Codes (M x K int8) and scales (M float32) of X (M x K, fp16, bf16 or fp32):
-    scale = max |row| / 127, code = the nearest integer to x / scale."""
+    scale = max |row| / 127, code = the nearest integer to x / scale. (Weights that are trained: X.detach().)"""
     if stream is not None:
         with _on(stream, X):
             return quantize_i8(X, handle)

@@ -490,6 +490,7 @@ void shape_is(const at::Tensor &t, int64_t rows, int64_t cols, const char *name)
 // (X, handle) -> codes (rows padded to 16 bytes), scales
 PyObject *quantize_i8(PyObject *const *a) {
     const at::Tensor &X = tensor(a[0], "X");
+    no_gradient(X, "X");
     const int type = type_of(X.scalar_type(), "X");
     const int64_t ldx = rows_of(X, X.scalar_type(), "X"), M = X.size(0), K = X.size(1), ld = std::max<int64_t>((K + 15) / 16 * 16, 16);
     const at::Device dev = X.device();
