@@ -617,8 +617,8 @@ def gemm_w4a4_lowrank(A, B, K, sx, sw, X, LD, LU, bias=None, out=None, handle=No
 # again, a launch more each time, so a program that loads them keeps padded rows.
 #
 # None of the calls takes part in autograd. Those with floating-point results
-# raise where grad mode is on and an argument requires grad; quantisation, whose
-# results are codes, does not.
+# raise where grad mode is on and an argument requires grad, or where an argument
+# has a tangent of forward mode; quantisation, whose results are codes, does not.
 #
 # The calls are short enough for the host's share to count, so their checks,
 # allocations and the C-ABI call are compiled (csrc/torch_calls.cpp); a call on
@@ -733,7 +733,7 @@ def newton_schulz(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out=No
 # for each row (a token, or an output channel of a weight). quantize_i8 returns codes
 # whose rows are padded to 16 bytes; others (a copy that has lost the padding) are taken
 # too, and above 32 rows copied in the call. As the MXFP4 calls, none of these takes
-# part in autograd: they raise where a gradient would be lost.
+# part in autograd: they raise where a gradient or a tangent would be lost.
 
 
 def quantize_i8(X, handle=None, stream=None):

@@ -14,6 +14,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/hip/HIPStream.h>
@@ -61,12 +62,15 @@ const at::Tensor &tensor(PyObject *o, const char *name) {
     return THPVariable_Unpack(o);
 }
 
-// The calls that return floating-point results take no part in autograd: a gradient that
-// the caller would miss is an error, as it is for torch's own out= forms.
+// The calls that return floating-point results take no part in autograd: a gradient or a tangent
+// (of forward mode, which no_grad does not end) that the caller would miss is an error, as it is for torch's own out= forms.
 void no_gradient(const at::Tensor &t, const char *name) {
     if (c10::GradMode::is_enabled() && t.requires_grad())
         fail(PyExc_RuntimeError, std::string(name) + " requires grad, but this call takes no part in autograd: "
                                                      "detach it, call under torch.no_grad() or from an autograd.Function");
+    if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+        fail(PyExc_RuntimeError, std::string(name) + " has a tangent, but this call takes no part in autograd: "
+                                                     "unpack the dual tensor or call from an autograd.Function");
 }
 
 int type_of(at::ScalarType t, const char *name, bool f32 = true) {
@@ -436,13 +440,13 @@ struct I8Held {
 
 I8Held i8_held(PyObject *oq, PyObject *os, const char *name, const at::Device &dev) {
     const at::Tensor &q = tensor(oq, name), &s = tensor(os, name);
+    no_gradient(s, name);
     I8Held h;
     h.ld = rows_of(q, at::kChar, name);
     h.rows = q.size(0);
     h.k = q.size(1);
     if (s.scalar_type() != at::kFloat || s.dim() != 1 || s.size(0) != h.rows || !s.is_contiguous())
         fail(PyExc_ValueError, std::string(name) + ": expected " + std::to_string(h.rows) + " contiguous float32 scales");
-    no_gradient(s, name);
     if (q.device() != dev || s.device() != dev)
         fail(PyExc_ValueError, std::string(name) + ": not on " + dev.str());
     h.q = static_cast<const int8_t *>(q.data_ptr());

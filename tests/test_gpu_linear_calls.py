@@ -141,3 +141,33 @@ def test_slopes_of_gates_that_are_not_finite(mp, name):
     assert math.isnan(got[0]) and got[1:7] == [1.0, 0.0, 1.0, 0.0, 0.5, 0.5] and abs(got[7] - want) <= 2.0 ** -8 * want
     act = dwu[:, 0].tolist()
     assert math.isnan(act[0]) and act[1] == float("inf") and act[3] > 2.9e38 and act[4:7] == [0.0, 0.0, 0.0]
+
+
+# Forward mode: a tangent would be lost in the call itself; inside an autograd.Function the call runs and the function's jvp gives it.
+def test_tangents_through_an_autograd_function(mp):
+    dt = torch.bfloat16
+    gg = torch.Generator().manual_seed(1)
+    x, wg, wu, v = (torch.randn(6, 16, generator=gg).to(dt).cuda() for _ in range(4))
+
+    class Gated(torch.autograd.Function):
+        @staticmethod
+        def forward(x):
+            return mp.gemm_gated(x, wg, wu)
+
+        @staticmethod
+        def setup_context(ctx, inputs, output):
+            ctx.save_for_forward(inputs[0])
+
+        @staticmethod
+        def jvp(ctx, t):
+            x, = ctx.saved_tensors
+            return (mp.gemm_gated(x + t, wg, wu) - mp.gemm_gated(x - t, wg, wu)) / 2
+
+    fw = torch.autograd.forward_ad
+    with fw.dual_level():
+        d = fw.make_dual(x, v)
+        with pytest.raises(RuntimeError, match="tangent"):
+            mp.gemm_gated(d, wg, wu)
+        y, t = fw.unpack_dual(Gated.apply(d))
+    assert torch.equal(y, mp.gemm_gated(x, wg, wu))
+    assert torch.equal(t, (mp.gemm_gated(x + v, wg, wu) - mp.gemm_gated(x - v, wg, wu)) / 2)
