@@ -478,21 +478,25 @@ mpgemm_status_t mpgemm_run_gated_backward(mpgemm_handle_t h, int64_t M, int64_t 
     const mpg::GatedGrads gp{dH, G, U, lddh, ldg, ldu, ws, (int)M, (int)N, (int)part, act};
     if (mpg::launch_gated_grads(type, gp, s) != hipSuccess)
         return MPGEMM_ERR_HIP;
-    mpg::Lin x = product(M, K, N, dX, lddx), w = product(N, K, M, dWg, lddwg);
-    x.a = w.a = ws;
+    // (dWu alone: from its part of [dG, dU])
+    const int parts = dWg && dWu ? 2 : 1;
+    mpg::Lin x = product(M, K, N, dX, lddx), w = dWg ? product(N, K, M, dWg, lddwg) : product(N, K, M, dWu, lddwu);
+    x.a = ws;
+    w.a = dWg ? ws : ws + 2 * part;
+    w.parts = parts;
     x.lda = w.lda = 2 * part * 2;
     x.part = w.part = (int)part;
     x.b[0] = og.p;
     x.b[1] = ou.p;
     x.ldb[0] = x.ldb[1] = og.ld;
-    w.c2 = dWu;
+    w.c2 = parts == 2 ? dWu : nullptr;
     w.ldc2 = lddwu;
     w.b[0] = ox.p;
     w.ldb[0] = ox.ld;
     if (need_dx && need_dw)
-        return status_of(mpg::launch_gated_pair(type, x, w, mpg::plan_lin_pair(M, part, K, h->cu_count), s));
+        return status_of(mpg::launch_gated_pair(type, x, w, mpg::plan_lin_pair(M, part, parts, K, h->cu_count), s));
     return status_of(need_dx ? mpg::launch_gated_dx(type, x, mpg::plan_lin(mpg::LIN_DX, M, K, 2 * part, 2, h->cu_count), s)
-                             : mpg::launch_gated_dw(type, w, mpg::plan_lin(mpg::LIN_DW, 2 * part, K, M, 2, h->cu_count), s));
+                             : mpg::launch_gated_dw(type, w, mpg::plan_lin(mpg::LIN_DW, parts * part, K, M, 2, h->cu_count), s));
 }
 
 int64_t mpgemm_run_gated_backward_workspace(int64_t M, int64_t N, int64_t K, int aligned, int cu_count) {

@@ -37,7 +37,7 @@ hipError_t launch_i8_dequantize(int type, const I8Dequantize &p, hipStream_t str
 //   SCALED  int8: C = (A B^T) sa sb + bias
 //   GATED   C = act(A B0^T) (A B1^T), of int8 operands each product scaled; G and U where wanted
 //   DX      C = A [B0; B1], A M x 2 Kp, B0 and B1 K x N (across k), K of each
-//   DW      rows [0, N1) of A^T B to C, rows [Kp, Kp + N1) to C2; A K x M, B K x N, both across k
+//   DW      rows [0, N1) of A^T B to C, with two parts rows [Kp, Kp + N1) to C2; A K x parts Kp, B K x N, both across k
 enum LinMode { LIN_SCALED = 0, LIN_GATED = 1, LIN_DX = 2, LIN_DW = 3 };
 
 struct Lin {
@@ -49,7 +49,7 @@ struct Lin {
     void *g, *u;             // (GATED, or null)
     int64_t ldc, ldc2, ldg, ldu;   // elements
     int M, N, K;             // of the result; of the sum (DX: of one of its two parts)
-    int part;                // (DX, DW) the columns of A that belong to the first part, padding included
+    int part, parts;         // (DX, DW) the columns of A that belong to one part, padding included; (DW) its parts, 1 or 2
     int act;
 };
 
@@ -60,7 +60,7 @@ struct LinPlan {
     int cus;
 };
 LinPlan plan_lin(int mode, int64_t M, int64_t N, int64_t K, int elem_bytes, int cu_count);
-LinPlan plan_lin_pair(int64_t M, int64_t part, int64_t K, int cu_count);
+LinPlan plan_lin_pair(int64_t M, int64_t part, int parts, int64_t K, int cu_count);
 hipError_t launch_w8a8(int type, const Lin &p, const LinPlan &plan, hipStream_t stream);
 hipError_t launch_gated_w8a8(int type, const Lin &p, const LinPlan &plan, hipStream_t stream);
 hipError_t launch_gated(int type, const Lin &p, const LinPlan &plan, hipStream_t stream);

@@ -221,7 +221,7 @@ struct LinTile {
     typedef PhaseTile<E, BM, BN, WGM, WGN, NS, AC, BC, MODE == LIN_DX> PT;
     static constexpr int EB = sizeof(typename E::T), CN = MODE == LIN_GATED ? BN / 2 : BN;
 
-    static __host__ __device__ int rows(const Lin &p) { return MODE == LIN_DW ? 2 * p.part : p.M; }
+    static __host__ __device__ int rows(const Lin &p) { return MODE == LIN_DW ? p.parts * p.part : p.M; }
     static __host__ __device__ int tiles_m(const Lin &p) { return (rows(p) + BM - 1) / BM; }
     static __host__ __device__ int tiles_n(const Lin &p) { return (p.N + CN - 1) / CN; }
 

@@ -279,12 +279,12 @@ LinPlan plan_lin(int mode, int64_t M, int64_t N, int64_t K, int elem_bytes, int 
     return pl;
 }
 
-// Both products of the backward pass in one grid, M x K over 2 part and 2 part x K over M: the work spread over the
-// CUs, or the longest tile.
-LinPlan plan_lin_pair(int64_t M, int64_t part, int64_t K, int cu_count) {
+// Both products of the backward pass in one grid, M x K over 2 part and (one weight's gradient or both) parts part x K over M:
+// the work spread over the CUs, or the longest tile.
+LinPlan plan_lin_pair(int64_t M, int64_t part, int parts, int64_t K, int cu_count) {
     return {LINK_TILE, lin_cheapest(3, [&](int c) {
                 const double x = lin_tile_us(c, 2 * part / 64), w = lin_tile_us(c, (M + 63) / 64);
-                const double all = (x * (double)lin_tiles(LIN_DX, c, M, K) + w * (double)lin_tiles(LIN_DW, c, 2 * part, K)) / cu_count;
+                const double all = (x * (double)lin_tiles(LIN_DX, c, M, K) + w * (double)lin_tiles(LIN_DW, c, parts * part, K)) / cu_count;
                 return all > x ? (all > w ? all : w) : (x > w ? x : w);
             }), cu_count};
 }

@@ -171,3 +171,57 @@ def test_tangents_through_an_autograd_function(mp):
         y, t = fw.unpack_dual(Gated.apply(d))
     assert torch.equal(y, mp.gemm_gated(x, wg, wu))
     assert torch.equal(t, (mp.gemm_gated(x + v, wg, wu) - mp.gemm_gated(x - v, wg, wu)) / 2)
+
+
+def backward_call(mp, t, want, ws, act=0):
+    """The C call on dH, X, Wg, Wu, G and U (contiguous, bf16) for those of dX, dWg and dWu that are wanted; its launches follow the
+    current stream."""
+    dh, x, wg, wu, g, u = t
+    (M, N), K = dh.shape, x.shape[1]
+    out = [torch.full(s, 7.0, dtype=dh.dtype, device="cuda") if y else None for y, s in zip(want, ((M, K), (N, K), (N, K)))]
+    p = [None if v is None else v.data_ptr() for v in out]
+
+    def run():
+        assert mp.mpgemm_run_gated_backward(mp.default_handle(0), M, N, K, 1, act, dh.data_ptr(), N, x.data_ptr(), K, wg.data_ptr(), K, wu.data_ptr(), K,
+                                            g.data_ptr(), N, u.data_ptr(), N, p[0], K, p[1], K, p[2], K, ws.data_ptr(), ws.numel(),
+                                            torch.cuda.current_stream().cuda_stream) == 0
+    return run, out
+
+
+def backward_inputs(mp, M, N, K):
+    gg = torch.Generator(device="cuda").manual_seed(M + N)
+    t = [torch.randn(*s, generator=gg, device="cuda").bfloat16() for s in ((M, N), (M, K), (N, K), (N, K), (M, N), (M, N))]
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    return t, torch.empty(mp.mpgemm_run_gated_backward_workspace(M, N, K, 1, cus), dtype=torch.uint8, device="cuda")
+
+
+# Either weight's gradient alone, in tiles of every size and N that ends anywhere in its last tile.
+@pytest.mark.parametrize("M,N,K", [(1, 3, 8), (40, 64, 16), (70, 65, 136), (300, 129, 264), (700, 1000, 520), (2048, 2050, 1032), (1500, 4480, 2056)])
+def test_backward_of_one_weight(mp, M, N, K):
+    t, ws = backward_inputs(mp, M, N, K)
+    whole = mp.gemm_gated_backward(*t)
+    for want in ((0, 1, 0), (0, 0, 1), (1, 1, 0), (1, 0, 1)):
+        ws.fill_(0x7F)
+        run, out = backward_call(mp, t, want, ws)
+        run()
+        torch.cuda.synchronize()
+        assert all(v is None or torch.equal(v, w) for v, w in zip(out, whole))
+
+
+# A gradient that is not wanted is not computed either: one weight's takes half of the time of both.
+def test_backward_of_one_weight_takes_half(mp):
+    t, ws = backward_inputs(mp, 4096, 4096, 4096)
+    runs = [backward_call(mp, t, want, ws) for want in ((0, 1, 1), (0, 1, 0), (0, 0, 1))]
+    best = [1e9] * 3
+    for _ in range(12):
+        for i, (run, _) in enumerate(runs):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            run()
+            a.record()
+            for _ in range(3):
+                run()
+            b.record()
+            torch.cuda.synchronize()
+            best[i] = min(best[i], a.elapsed_time(b) / 3)
+    print("both, dWg, dWu (ms):", best)
+    assert max(best[1:]) < 0.8 * best[0]
