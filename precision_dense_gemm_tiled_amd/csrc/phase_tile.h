@@ -131,8 +131,8 @@ struct PhaseTile {
     // transposing reads write the load as an instruction of its own: the compiler takes those
     // reads as possible uses of any load to LDS before them and would wait for all loads in
     // front of each (4096 x 4096 x 20480 with B across k: 579 us, 461 without those waits;
-    // 20480 x 4096 x 4096 with both: 548 and 495). The load has no result in registers,
-    // and nothing else in these kernels uses m0.
+    // 20480 x 4096 x 4096 with both: 548 and 495). The load has no result in registers; its
+    // LDS address is an operand bound to m0, so the compiler knows of that register's use.
     template <bool COL, int H, int L>
     static __device__ __forceinline__ void load(const PtSource &s, int h, int e, const uint8_t *(&at_k)[2], const uint32_t (&off)[L],
                                                 uint8_t *lds, int tid, int wave) {
@@ -154,8 +154,8 @@ struct PhaseTile {
             if constexpr (ACOL || BCOL) {
                 const uint64_t at64 = reinterpret_cast<uint64_t>(base);
                 const pt_u32x4 r = {(uint32_t)at64, (uint32_t)(at64 >> 32) & 0xFFFFu, kPtRange, 0x00020000u};
-                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                             : : "s"((uint32_t)(uintptr_t)to), "v"(o), "s"(r), "s"(ahead));
+                asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                             : : "{m0}"((uint32_t)(uintptr_t)to), "v"(o), "s"(r), "s"(ahead));
             } else {
                 const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, kPtRange, 0x00020000);
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, o, ahead, 0, 0);
