@@ -413,7 +413,7 @@ int64_t mpgemm_run_newton_schulz_workspace(int64_t batch, int64_t M, int64_t N);
 #define MPGEMM_MAX_DIM_LINEAR (1 << 24)
 #define MPGEMM_MAX_ALONG_LINEAR ((1 << 22) - 128)
 
-/* X (M x K, `type`, row stride ldx elements) into codes Q and scales S. */
+/* X (M x K, `type`, row stride ldx elements) into codes Q and scales S (K == 0: nothing is written). */
 mpgemm_status_t mpgemm_quantize_i8(mpgemm_handle_t h, int64_t M, int64_t K, int type, const void *X, int64_t ldx,
                                    int8_t *Q, int64_t ldq, float *S, void *stream);
 
@@ -459,8 +459,10 @@ int64_t mpgemm_run_gated_workspace(int64_t M, int64_t N, int64_t K, int aligned,
  *   dG = dH U act'(G), dU = dH act(G)   in fp32, rounded once to `type`
  *   dX = dG Wg + dU Wu                  M x K
  *   dWg = dG^T X, dWu = dU^T X          N x K
- * with fp32 sums, each result rounded once to `type`. dX may be NULL (then Wg and Wu may
- * be), and so may dWg and dWu (X, where both are): those gradients are not computed. */
+ * with fp32 sums, each result rounded once to `type`. dG and dU are the matrix instruction's operands, hence their
+ * type. In fp16 a dG or dU past 65504 becomes an infinity, and with it the sums that it enters, and one below
+ * 2^-14 is held in steps of 2^-24: a loss is scaled with these products in mind, not dH alone. dX may be NULL (then
+ * Wg and Wu may be), and so may dWg and dWu (X, where both are): those gradients are not computed. */
 mpgemm_status_t mpgemm_run_gated_backward(mpgemm_handle_t h, int64_t M, int64_t N, int64_t K, int type, int act,
                                           const void *dH, int64_t lddh, const void *X, int64_t ldx, const void *Wg,
                                           int64_t ldwg, const void *Wu, int64_t ldwu, const void *G, int64_t ldg,

@@ -784,7 +784,8 @@ def gemm_gated(X, Wg, Wu, act="silu", keep=False, out=None, handle=None, stream=
 def gemm_gated_backward(dH, X, Wg, Wu, G, U, act="silu", need_dx=True, need_dw=True, handle=None, stream=None):
     """Gradients of gemm_gated from dH (M x N) and the G and U that it kept:
     (dX, dWg, dWu) in dH's type. What is not needed is None (need_dx=False: Wg and Wu may
-    be None; need_dw=False: X)."""
+    be None; need_dw=False: X). On the way dH U act'(G) and dH act(G) are rounded to that
+    type too: in fp16 they overflow past 65504, so a loss is scaled with them in mind."""
     if stream is not None:
         with _on(stream, dH):
             return gemm_gated_backward(dH, X, Wg, Wu, G, U, act, need_dx, need_dw, handle)

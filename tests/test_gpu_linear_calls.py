@@ -225,3 +225,40 @@ def test_backward_of_one_weight_takes_half(mp):
             best[i] = min(best[i], a.elapsed_time(b) / 3)
     print("both, dWg, dWu (ms):", best)
     assert max(best[1:]) < 0.8 * best[0]
+
+
+# dG = dH U act'(G) and dU = dH act(G) are held in the operands' type. With a gate of 100 (of any activation act' is 1, act is the gate) and
+# tokens that are rows of the identity, dWg and dWu show them.
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+def test_fp16_gradients_below_its_normal_numbers(mp, name):
+    M = N = 64
+    # quarters of the smallest subnormal: every remainder, ties too (numbers of up to 11 bits, so that dH is exact)
+    k = (torch.arange(M * N, dtype=torch.float64).reshape(M, N) - 2000).clamp(max=2048)
+    dh = (k * 2.0 ** -13).half()
+    u = torch.full((M, N), 2.0 ** -13, dtype=torch.float16)
+    g = torch.full((M, N), 100.0, dtype=torch.float16)
+    x = (1024 * torch.eye(M)).half()
+    _, dwg, _ = mp.gemm_gated_backward(dh.cuda(), x.cuda(), None, None, g.cuda(), u.cuda(), act=name, need_dx=False)
+    want = (dh.double() * u.double()).half()   # (one rounding of an exact product)
+    assert (want != 0).any() and want.abs().max() < 2.0 ** -13
+    assert torch.equal(dwg.t().cpu().double(), want.double() * 1024)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+def test_gradients_past_the_largest_fp16(mp, t):
+    dt = lu.TYPES[t]
+    M, N, K = 70, 40, 72
+    gg = torch.Generator().manual_seed(4)
+    x, wg, wu = (torch.rand(*s, generator=gg).to(dt) + 1 for s in ((M, K), (N, K), (N, K)))
+    dh, u = (torch.randn(M, N, generator=gg).to(dt) for _ in range(2))
+    g = torch.randn(M, N, generator=gg).to(dt)
+    dh[33, 7], u[33, 7], g[33, 7] = 400.0, 200.0, 100.0   # dG = 80000, dU = 40000
+    want = lu.gated_backward(dh, x, wg, wu, g, u, "silu", torch.bfloat16)
+    dx, dwg, dwu = (y.cpu() for y in mp.gemm_gated_backward(*(v.cuda() for v in (dh, x, wg, wu, g, u))))
+    if t == "bf16":
+        for y, (w, e) in zip((dx, dwg, dwu), want):
+            lu.check(y, w, e)
+        return
+    assert (dx[33] == float("inf")).all() and (dwg[7] == float("inf")).all()
+    rest = torch.arange(M) != 33
+    assert torch.isfinite(dx[rest]).all() and torch.isfinite(dwg[torch.arange(N) != 7]).all() and torch.isfinite(dwu[torch.arange(N) != 7]).all()
