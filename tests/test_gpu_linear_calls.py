@@ -262,3 +262,22 @@ def test_gradients_past_the_largest_fp16(mp, t):
     assert (dx[33] == float("inf")).all() and (dwg[7] == float("inf")).all()
     rest = torch.arange(M) != 33
     assert torch.isfinite(dx[rest]).all() and torch.isfinite(dwg[torch.arange(N) != 7]).all() and torch.isfinite(dwu[torch.arange(N) != 7]).all()
+
+
+# Every activation in large tiles, in 16 bits and on integers.
+@pytest.mark.parametrize("name", ["gelu", "gelu_tanh"])
+def test_activations_in_large_tiles(mp, name):
+    dt, (M, N, K) = torch.bfloat16, (2100, 1030, 72)
+    gg = torch.Generator().manual_seed(9)
+    x = torch.randn(M, K, generator=gg).to(dt)
+    wg, wu = ((0.3 * torch.randn(N, K, generator=gg)).to(dt) for _ in range(2))
+    want, tol = lu.gated(x, wg, wu, name)
+    for y, w, e in zip(mp.gemm_gated(x.cuda(), wg.cuda(), wu.cuda(), act=name, keep=True), want, tol):
+        lu.check(y, w, lu.rounded_tol(w, e, dt))
+    a, b, c = (lu.quantize(v) for v in (x, wg, wu))
+    (pg, mg), (pu, mu) = lu.scaled(a, b), lu.scaled(a, c)
+    (h, _, _), (e, _, _) = lu.gated_from(pg, pu, 3.01 * 2.0 ** -24 * mg, 3.01 * 2.0 ** -24 * mu, name)
+    held = [(q.to(torch.int8).cuda(), s.cuda()) for q, s in (b, c)]
+    for t in (torch.float32, dt):
+        y = mp.gemm_gated_w8a8(*mp.quantize_i8(x.cuda()), *held[0], *held[1], act=name, dtype=t)
+        lu.check(y, h, lu.rounded_tol(h, e, t))
