@@ -2,7 +2,7 @@
 // product in fp32, one rounding. A tile's columns are half Wg's, half Wu's (phase_tile.h), so that a
 // lane holds the two sums of an output: X goes through LDS once for both, and nothing but H
 // (and G and U, each rounded once, where the backward pass is to have them) is written. 4096 x 10240 x 4096 in bf16 with G
-// and U: 472 to 499 us by the card (1.4 PFLOP/s; the library's plain product of that size 433 to 453); one token 30.7 (168 MB, 5.5 TB/s).
+// and U: 464 to 510 us by the card (1.3 to 1.5 PFLOP/s; the library's plain product of that size 433 to 453); one token 30.7 (168 MB, 5.5 TB/s).
 #include "linear_device.h"
 
 namespace mpg {

@@ -207,7 +207,7 @@ hipError_t launch_lin_copy(const LinCopy &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Rows of `row_bytes` bytes, each a copy of `row` (or zeros): results of empty sums.
+// C (M x N, row stride ldc), each row a copy of `row`, or zeros: results of empty sums.
 template <typename T>
 __global__ __launch_bounds__(256) void lin_fill_kernel(T *c, int64_t ldc, int M, int N, const T *row) {
     const int64_t total = (int64_t)M * N;
@@ -291,8 +291,8 @@ LinPlan plan_lin_pair(int64_t M, int64_t part, int parts, int64_t K, int cu_coun
 
 // Few activations: every workgroup of the product quantises all of them. In wavefront loads of 512 of a row, up to 16, of one
 // or two rows up to 32. In the product and by a launch before it, us: 1 x 4096 x 4096 6.1 and 8.2, 1 x 8192 x 16384 29.7 and
-// 37.3, 2 x 8192 x 8192 15.5 and 18.9, 2 x 4096 x 8192 11.9 and 11.0, 4 x 4096 x 2048 5.8 and 7.0, 8 x 4096 x 1024 5.2 and 5.5; 4 x 8192 x
-// 4096 12.8 and 11.2, 8 x 8192 x 2048 10.9 and 8.6, 16 x 4096 x 1024 7.3 and 5.8.
+// 37.3, 2 x 8192 x 8192 15.5 and 18.9, 2 x 4096 x 8192 11.9 and 11.0 (the rule has no N: it takes the slower side there), 4 x 4096 x
+// 2048 5.8 and 7.0, 8 x 4096 x 1024 5.2 and 5.5; 4 x 8192 x 4096 12.8 and 11.2, 8 x 8192 x 2048 10.9 and 8.6, 16 x 4096 x 1024 7.3 and 5.8.
 bool lin_fuses(const LinPlan &plan, int64_t M, int64_t K) {
     return plan.kind == LINK_SKINNY && M <= 16 && M * ((K + 511) / 512) <= (M <= 2 ? LIN_X_MAX : LIN_X_MAX / 2);
 }
